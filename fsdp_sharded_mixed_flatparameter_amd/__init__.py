@@ -17,6 +17,9 @@ LIB_PATH = os.path.join(HERE, "libzeroflat.so")
 ZERO_F32, ZERO_F16, ZERO_BF16 = 0, 1, 2
 ZERO_SUM, ZERO_AVG = 0, 1
 ZERO_STEP_FINALIZE = 1
+ZERO_MULTI_RESET = 2
+ZERO_ROW = 256
+ZERO_NONE = -1
 ZERO_MAX_RANKS = 256
 ZERO_MAX_PARTIALS = 65536
 
@@ -24,7 +27,8 @@ EXPORTS = ("zero_last_error", "zero_flat_layout", "zero_step_state_init",
            "zero_grad_reduce_shard", "zero_unscale_norm", "zero_adamw_shard_step",
            "zero_quant_allgather_slot", "zero_dequant_allgather", "zero_grad_accumulate_shard",
            "zero_grad_reduce_shard_int8", "zero_offload_adamw_host", "zero_offload_step",
-           "zero_grad_reduce_shard_noalloc")
+           "zero_grad_reduce_shard_noalloc", "zero_multi_plan_init", "zero_multi_bind",
+           "zero_multi_unscale_norm", "zero_multi_adamw_step")
 
 
 class zero_span_t(C.Structure):
@@ -60,6 +64,14 @@ class zero_adamw_hparams_t(C.Structure):
                 ("max_grad_norm", C.c_double)]
 
 
+class zero_multi_plan_t(C.Structure):
+    _fields_ = [(f, C.c_int64) for f in
+                ("total", "rows", "image_bytes", "bind_bytes", "sumsq_off", "tiles_off",
+                 "spans_off", "partials_off", "counters_off", "span")] + \
+               [(f, C.c_int32) for f in
+                ("n_tensors", "grad_dtype", "param_dtype", "state_bits", "n_tiles", "n_spans")]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError("libzeroflat.so is not built (%s); run __graft_entry__.build()" % LIB_PATH)
@@ -93,6 +105,14 @@ def _load():
     L.zero_offload_step.restype = C.c_int
     L.zero_offload_step.argtypes = [vp, i32, i64, vp, vp, vp, vp, vp, vp, i32, i64, vp, vp, i64,
                                     i32, vp]
+    L.zero_multi_plan_init.restype = C.c_int
+    L.zero_multi_plan_init.argtypes = [vp, i32, i32, i32, i32, vp, vp, i64]
+    L.zero_multi_bind.restype = C.c_int
+    L.zero_multi_bind.argtypes = [vp, vp, vp, vp, vp, vp]
+    L.zero_multi_unscale_norm.restype = C.c_int
+    L.zero_multi_unscale_norm.argtypes = [vp, vp, u32, vp, vp]
+    L.zero_multi_adamw_step.restype = C.c_int
+    L.zero_multi_adamw_step.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, u32, u32, vp, vp]
     return L
 
 
@@ -234,6 +254,14 @@ class StepState:
         st.remote_sumsq = float(sumsq)
         st.remote_overflow = int(overflow)
         self.upload(st)
+
+    def field(self, name):
+        """A 0-d device tensor that views one scalar of the state (no copy)."""
+        import torch
+        ctype = dict(zero_step_state_t._fields_)[name]
+        dtype = {C.c_double: torch.float64, C.c_float: torch.float32, C.c_int32: torch.int32}[ctype]
+        off = getattr(zero_step_state_t, name).offset
+        return self.buf[off:off + C.sizeof(ctype)].view(dtype)[0]
 
     def ptr(self):
         return C.c_void_p(self.buf.data_ptr())
@@ -463,5 +491,48 @@ def unflatten(flat, shapes, n_ranks=1, align=1):
     return [flat[a:b].view(tuple(sh)) for (a, b), sh in zip(lay["spans"], shapes)]
 
 
-from . import shard  # noqa: E402
+# ------------------------------------------------------------------ lists of tensors
+def zero_multi_unscale_norm(plan, state, reset=False, stream=None):
+    """Statistics over the tensors bound to `plan` (a MultiPlan): the sum of
+    squares of each unscaled gradient into plan.tensor_sumsq, their sum and the
+    overflow flag into `state` (added to it, or set with `reset`)."""
+    plan._require_bound()
+    _check(_lib.zero_multi_unscale_norm(plan._ref, plan._image_ptr,
+                                        ZERO_MULTI_RESET if reset else 0, _state_ptr(state),
+                                        _stream(stream)))
+
+
+def zero_multi_adamw_step(plan, master, exp_avg, exp_avg_sq, hp, state, exp_avg_scale=None,
+                          exp_avg_sq_scale=None, seed=0, finalize=True, stream=None):
+    """Skip-on-overflow, clip and AdamW over the list bound to `plan`, on arenas
+    of plan.rows rows of ZERO_ROW elements, with the 16-bit copies and the
+    scaler update."""
+    plan._require_bound()
+    n, q8 = plan.rows * ZERO_ROW, plan.state_bits == 8
+    kinds = ("float8_e4m3fn", "float8_e5m2") if q8 else ("float32", "float32")
+    for name, t, dt, size in (("master", master, "float32", n), ("exp_avg", exp_avg, kinds[0], n),
+                              ("exp_avg_sq", exp_avg_sq, kinds[1], n)):
+        _dev(t, name, (dt,))
+        if t.numel() != size:
+            raise ValueError("%s must hold the plan's %d elements" % (name, size))
+    for name, t in (("exp_avg_scale", exp_avg_scale), ("exp_avg_sq_scale", exp_avg_sq_scale)):
+        if not q8:
+            if t is not None:
+                raise ValueError("%s belongs to 8-bit states" % name)
+            continue
+        if t is None:
+            raise ValueError("8-bit states need %s" % name)
+        _dev(t, name, ("float32",))
+        if t.numel() != plan.rows:
+            raise ValueError("%s must hold one scale per row (%d)" % (name, plan.rows))
+    h = hp if isinstance(hp, zero_adamw_hparams_t) else zero_adamw_hparams_t(**hp)
+    _check(_lib.zero_multi_adamw_step(plan._ref, plan._image_ptr, _ptr(master), _ptr(exp_avg),
+                                      _ptr(exp_avg_sq), _ptr(exp_avg_scale),
+                                      _ptr(exp_avg_sq_scale), C.byref(h), seed & 0xffffffff,
+                                      ZERO_STEP_FINALIZE if finalize else 0, _state_ptr(state),
+                                      _stream(stream)))
+
+
+from . import multi, shard  # noqa: E402
+from .multi import MultiPlan, TensorListOptimizer  # noqa: E402,F401
 from .shard import MultiShardOptimizer, OffloadShardOptimizer, ShardOptimizer  # noqa: E402,F401

@@ -7,6 +7,7 @@ The host-only source (the ZeRO-Offload step) is built by ROCm's clang++ with
 the same contraction rule and -fno-math-errno, which lets its square roots
 vectorize and changes no result.
 """
+import concurrent.futures
 import os
 import subprocess
 
@@ -14,6 +15,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libzeroflat.so")
 SOURCES = [os.path.join(HERE, "csrc", "zeroflat_kernels.hip"),
+           os.path.join(HERE, "csrc", "zeroflat_multi.hip"),
            os.path.join(HERE, "csrc", "zeroflat_api.cpp")]
 # host-only C++ (the ZeRO-Offload host step): built by the host compiler, so
 # that it can carry one machine-code clone per x86 ISA level
@@ -39,15 +41,17 @@ def build(verbose: bool = False, extra_flags=()) -> str:
             print(" ".join(cmd), flush=True)
         subprocess.run(cmd, check=True)
 
+    cmds = []
+    for src in SOURCES + HOST_SOURCES:
+        obj = os.path.join(HERE, os.path.splitext(os.path.basename(src))[0] + tag)
+        objs.append(obj)
+        cc = (["hipcc"] + HIPCC_FLAGS + list(extra_flags) if src in SOURCES
+              else [os.path.join(ROCM, "llvm", "bin", "clang++")] + HOST_FLAGS)
+        cmds.append(cc + ["-c", "-o", obj, src])
     try:
-        for src in SOURCES:
-            obj = os.path.join(HERE, os.path.splitext(os.path.basename(src))[0] + tag)
-            objs.append(obj)
-            run(["hipcc"] + HIPCC_FLAGS + list(extra_flags) + ["-c", "-o", obj, src])
-        for src in HOST_SOURCES:
-            obj = os.path.join(HERE, os.path.splitext(os.path.basename(src))[0] + tag)
-            objs.append(obj)
-            run([os.path.join(ROCM, "llvm", "bin", "clang++")] + HOST_FLAGS + ["-c", "-o", obj, src])
+        # every source at once: the kernels take minutes
+        with concurrent.futures.ThreadPoolExecutor(len(cmds)) as pool:
+            list(pool.map(run, cmds))
         run(["hipcc", "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp] + objs)
     finally:
         for obj in objs:

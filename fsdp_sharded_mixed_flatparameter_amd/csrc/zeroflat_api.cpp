@@ -545,4 +545,225 @@ int zero_dequant_allgather(const int8_t* q_buf, const float* q_scales, int32_t n
     return ok();
 }
 
+// ---------------------------------------------------------------------------
+// The step over a list of tensors.
+namespace {
+int64_t ceil_div(int64_t a, int64_t b) { return a / b + (a % b ? 1 : 0); }
+int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
+
+// elements one block of the statistics pass reads: the smallest power of two
+// from kMinSpan on that leaves at most kMaxSpans full spans
+constexpr int64_t kMinSpan = 4096, kMaxSpans = 4096;
+
+int check_plan(const char* fn, const zero_multi_plan_t* plan) {
+    if (!plan) return fail(ZERO_EINVAL, "%s: NULL plan", fn);
+    if (plan->n_tensors < 0 || plan->n_tensors > ZERO_MAX_TENSORS || plan->image_bytes <= 0 ||
+        !valid_dtype(plan->grad_dtype) || plan->span < kMinSpan)
+        return fail(ZERO_EINVAL, "%s: the plan is not one of zero_multi_plan_init", fn);
+    return ZERO_OK;
+}
+}  // namespace
+
+int zero_multi_plan_init(const int64_t* numels, int32_t n_tensors, int32_t grad_dtype,
+                         int32_t param_dtype, int32_t state_bits, zero_multi_plan_t* plan,
+                         void* image, int64_t image_bytes) {
+    const char* fn = "zero_multi_plan_init";
+    if (!plan) return fail(ZERO_EINVAL, "%s: NULL plan", fn);
+    if (n_tensors < 0 || (n_tensors > 0 && !numels))
+        return fail(ZERO_EINVAL, "%s: bad tensor list", fn);
+    if (n_tensors > ZERO_MAX_TENSORS)
+        return fail(ZERO_ERANGE, "%s: more than %d tensors", fn, ZERO_MAX_TENSORS);
+    if (!valid_dtype(grad_dtype)) return fail(ZERO_EINVAL, "%s: bad grad_dtype %d", fn, grad_dtype);
+    if (param_dtype != ZERO_NONE && param_dtype != ZERO_F16 && param_dtype != ZERO_BF16)
+        return fail(ZERO_EINVAL, "%s: param_dtype must be fp16, bf16 or none", fn);
+    if (state_bits != 0 && state_bits != 8 && state_bits != 32)
+        return fail(ZERO_EINVAL, "%s: state_bits must be 32, 8 or 0", fn);
+    const int64_t rows_per_tile = state_bits == 8 ? zf::kMultiRows8 : zf::kMultiRows32;
+    int64_t total = 0, rows = 0, tiles = 0;
+    for (int32_t k = 0; k < n_tensors; ++k) {
+        if (numels[k] < 0) return fail(ZERO_EINVAL, "%s: numel[%d] < 0", fn, k);
+        // 4-byte elements: byte counts stay far from int64's end
+        if (numels[k] > ((int64_t)1 << 56) || !add_ok(total, numels[k], &total) ||
+            total > ((int64_t)1 << 56))
+            return fail(ZERO_ERANGE, "%s: total overflows", fn);
+        const int64_t r = ceil_div(numels[k], ZERO_ROW);
+        rows += r;
+        tiles += ceil_div(r, rows_per_tile);
+    }
+    int64_t span = kMinSpan;
+    while (ceil_div(total, span) > kMaxSpans) span *= 2;
+    int64_t spans = 0;
+    for (int32_t k = 0; k < n_tensors; ++k) spans += ceil_div(numels[k], span);
+    if (state_bits == 0) tiles = 0;
+    // tile and row indices are 32-bit in the kernels
+    if (tiles > 0x3fffffff || rows > 0x7fffffff)
+        return fail(ZERO_ERANGE, "%s: the list is too long", fn);
+
+    zero_multi_plan_t P;
+    memset(&P, 0, sizeof P);
+    P.total = total;
+    P.rows = rows;
+    P.n_tensors = n_tensors;
+    P.grad_dtype = grad_dtype;
+    P.param_dtype = param_dtype;
+    P.state_bits = state_bits;
+    P.n_tiles = (int32_t)tiles;
+    P.n_spans = (int32_t)spans;
+    P.span = span;
+    int64_t off = 0;
+    auto part = [&](int64_t bytes) { const int64_t at = off; off = round_up(off + bytes, 256); return at; };
+    P.bind_bytes = (int64_t)n_tensors * (int64_t)sizeof(zf::MultiEntry);
+    part(P.bind_bytes);
+    P.counters_off = part((int64_t)zf::kMultiCounters * 4);
+    P.tiles_off = part(tiles * 4);
+    P.spans_off = part(spans * 4);
+    P.sumsq_off = part((int64_t)n_tensors * 8);
+    P.partials_off = part(spans * 8);
+    P.image_bytes = off;
+    if (image) {
+        if (!aligned(image, 8)) return fail(ZERO_EALIGN, "%s: image not 8-byte aligned", fn);
+        if (image_bytes < P.image_bytes)
+            return fail(ZERO_ERANGE, "%s: image holds %lld of %lld bytes", fn, (long long)image_bytes,
+                        (long long)P.image_bytes);
+        char* base = static_cast<char*>(image);
+        memset(base, 0, (size_t)P.image_bytes);
+        auto* e = reinterpret_cast<zf::MultiEntry*>(base);
+        auto* tile_tensor = reinterpret_cast<int32_t*>(base + P.tiles_off);
+        auto* span_tensor = reinterpret_cast<int32_t*>(base + P.spans_off);
+        int64_t row = 0, tile = 0, sp = 0;
+        for (int32_t k = 0; k < n_tensors; ++k) {
+            const int64_t r = ceil_div(numels[k], ZERO_ROW);
+            const int64_t nt = state_bits ? ceil_div(r, rows_per_tile) : 0;
+            const int64_t ns = ceil_div(numels[k], span);
+            e[k].numel = numels[k];
+            e[k].row0 = row;
+            e[k].tile0 = (int32_t)tile;
+            e[k].span0 = (int32_t)sp;
+            e[k].n_spans = (int32_t)ns;
+            e[k].lr_mult = 1.0;
+            e[k].decay_mult = 1.0;
+            for (int64_t i = 0; i < nt; ++i) tile_tensor[tile + i] = k;
+            for (int64_t i = 0; i < ns; ++i) span_tensor[sp + i] = k;
+            row += r;
+            tile += nt;
+            sp += ns;
+        }
+    }
+    *plan = P;
+    return ok();
+}
+
+int zero_multi_bind(const zero_multi_plan_t* plan, const void* const* grads, void* const* params,
+                    const double* lr_mult, const double* decay_mult, void* image) {
+    const char* fn = "zero_multi_bind";
+    if (int e = check_plan(fn, plan)) return e;
+    if (!image) return fail(ZERO_EINVAL, "%s: NULL image", fn);
+    if (!aligned(image, 8)) return fail(ZERO_EALIGN, "%s: image not 8-byte aligned", fn);
+    const bool copy = plan->param_dtype != ZERO_NONE;
+    const int32_t n = plan->n_tensors;
+    if (n > 0 && (!grads || (copy && !params)))
+        return fail(ZERO_EINVAL, "%s: NULL pointer table", fn);
+    if (!copy && params) return fail(ZERO_EINVAL, "%s: the plan has no param_dtype", fn);
+    auto* e = static_cast<zf::MultiEntry*>(image);
+    const int es = esize(plan->grad_dtype);
+    for (int32_t k = 0; k < n; ++k) {   // nothing is written on error
+        if (e[k].numel > 0 && (!grads[k] || (copy && !params[k])))
+            return fail(ZERO_EINVAL, "%s: tensor %d is NULL", fn, k);
+        if (e[k].numel > 0 && (!aligned(grads[k], es) || (copy && !aligned(params[k], 2))))
+            return fail(ZERO_EALIGN, "%s: tensor %d is not aligned to its element size", fn, k);
+        if ((lr_mult && !(lr_mult[k] >= 0.0 && isfinite(lr_mult[k]))) ||
+            (decay_mult && !(decay_mult[k] >= 0.0 && isfinite(decay_mult[k]))))
+            return fail(ZERO_EINVAL, "%s: factors of tensor %d out of range", fn, k);
+    }
+    for (int32_t k = 0; k < n; ++k) {
+        e[k].grad = grads[k];
+        e[k].param = copy ? params[k] : nullptr;
+        e[k].lr_mult = lr_mult ? lr_mult[k] : 1.0;
+        e[k].decay_mult = decay_mult ? decay_mult[k] : 1.0;
+    }
+    return ok();
+}
+
+int zero_multi_unscale_norm(const zero_multi_plan_t* plan, void* d_plan, uint32_t flags,
+                            zero_step_state_t* d_state, void* stream) {
+    const char* fn = "zero_multi_unscale_norm";
+    if (int e = check_plan(fn, plan)) return e;
+    if (!d_plan || !d_state) return fail(ZERO_EINVAL, "%s: NULL plan buffer or state", fn);
+    if (!aligned(d_plan, 256)) return fail(ZERO_EALIGN, "%s: plan buffer not 256-byte aligned", fn);
+    if (!aligned(d_state, 8)) return fail(ZERO_EALIGN, "%s: state not 8-byte aligned", fn);
+    if (flags & ~ZERO_MULTI_RESET) return fail(ZERO_EINVAL, "%s: unknown flags 0x%x", fn, flags);
+    char* base = static_cast<char*>(d_plan);
+    zf::MultiNormLaunch a;
+    memset(&a, 0, sizeof a);
+    a.entries = reinterpret_cast<const zf::MultiEntry*>(base);
+    a.span_tensor = reinterpret_cast<const int32_t*>(base + plan->spans_off);
+    a.tensor_sumsq = reinterpret_cast<double*>(base + plan->sumsq_off);
+    a.partials = reinterpret_cast<double*>(base + plan->partials_off);
+    a.counters = reinterpret_cast<unsigned*>(base + plan->counters_off);
+    a.span = plan->span;
+    a.n_tensors = plan->n_tensors;
+    a.n_spans = plan->n_spans;
+    a.dtype = plan->grad_dtype;
+    a.reset = flags & ZERO_MULTI_RESET ? 1 : 0;
+    a.st = d_state;
+    const int e = zf::launch_multi_norm(a, stream);
+    if (e) return hip_fail(e, fn);
+    return ok();
+}
+
+int zero_multi_adamw_step(const zero_multi_plan_t* plan, void* d_plan, float* master,
+                          void* exp_avg, void* exp_avg_sq, float* m_scale, float* v_scale,
+                          const zero_adamw_hparams_t* hp, uint32_t seed, uint32_t flags,
+                          zero_step_state_t* d_state, void* stream) {
+    const char* fn = "zero_multi_adamw_step";
+    if (int e = check_plan(fn, plan)) return e;
+    if (int e = check_hp(fn, hp)) return e;
+    if (!d_plan || !d_state) return fail(ZERO_EINVAL, "%s: NULL plan buffer or state", fn);
+    if (flags & ~ZERO_STEP_FINALIZE) return fail(ZERO_EINVAL, "%s: unknown flags 0x%x", fn, flags);
+    if (!aligned(d_plan, 256)) return fail(ZERO_EALIGN, "%s: plan buffer not 256-byte aligned", fn);
+    if (!aligned(d_state, 8)) return fail(ZERO_EALIGN, "%s: state not 8-byte aligned", fn);
+    if (plan->state_bits != 8 && plan->state_bits != 32)
+        return fail(ZERO_EINVAL, "%s: the plan only serves the statistics", fn);
+    const bool q8 = plan->state_bits == 8;
+    if (plan->rows > 0) {
+        if (!master || !exp_avg || !exp_avg_sq || (q8 && (!m_scale || !v_scale)))
+            return fail(ZERO_EINVAL, "%s: NULL state arena", fn);
+        const uintptr_t al = q8 ? 4 : 16;
+        if (!aligned(master, 16) || !aligned(exp_avg, al) || !aligned(exp_avg_sq, al) ||
+            (q8 && (!aligned(m_scale, 4) || !aligned(v_scale, 4))))
+            return fail(ZERO_EALIGN, "%s: a state arena is misaligned", fn);
+    }
+    char* base = static_cast<char*>(d_plan);
+    zf::MultiAdamLaunch a;
+    memset(&a, 0, sizeof a);
+    a.entries = reinterpret_cast<const zf::MultiEntry*>(base);
+    a.tile_tensor = reinterpret_cast<const int32_t*>(base + plan->tiles_off);
+    a.counters = reinterpret_cast<unsigned*>(base + plan->counters_off);
+    a.p = master;
+    a.m = exp_avg;
+    a.v = exp_avg_sq;
+    a.ms = m_scale;
+    a.vs = v_scale;
+    a.n_tiles = plan->n_tiles;
+    a.gdtype = plan->grad_dtype;
+    a.pdtype = plan->param_dtype;
+    a.bits = plan->state_bits;
+    a.flags = flags;
+    a.seed = seed;
+    a.b1 = (float)hp->beta1;
+    a.c1 = (float)(1.0 - hp->beta1);
+    a.b2 = (float)hp->beta2;
+    a.c2 = (float)(1.0 - hp->beta2);
+    a.eps = (float)hp->eps;
+    a.lr = hp->lr;
+    a.wd = hp->weight_decay;
+    a.beta1 = hp->beta1;
+    a.beta2 = hp->beta2;
+    a.max_norm = hp->max_grad_norm;
+    a.st = d_state;
+    const int e = zf::launch_multi_adamw(a, stream);
+    if (e) return hip_fail(e, fn);
+    return ok();
+}
+
 }  // extern "C"

@@ -1,0 +1,678 @@
+// zeroflat_multi.hip -- gfx950 (MI355X, CDNA4, wave64) kernels of the step
+// over a list of tensors:
+//   multi_stats_kernel  sums of squares of the unscaled gradients, one partial
+//                       per span of a tensor
+//   multi_fold_kernel   the partials per tensor and over all, in a fixed order
+//   multi_adamw_kernel  skip/clip prologue, AdamW with 32-bit or 8-bit states,
+//                       16-bit copy
+//   multi_finalize_kernel  loss scaler and counters
+//
+// Everything here streams HBM once; none of it is a contraction.  The state
+// arenas are rows of 256 elements, so a wave owns whole rows: in a row lane l
+// holds elements 4l .. 4l+3 (16 bytes of each fp32 array, 8 of a 16-bit one,
+// 4 of an 8-bit one per lane).  Only the gradients and the 16-bit parameters
+// lie elsewhere, at any element offset; the plan's tables say which tensor a
+// tile (of rows) or a span (of gradient elements) belongs to.
+//
+// Built with -ffp-contract=off and correctly rounded fp32 division and square
+// root, as the flat step's kernels; the 32-bit form repeats their operation
+// order, so a list of one tensor gives the flat step's bits.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "zf_launch.h"
+
+namespace zf {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWaves = kThreads / 64;
+constexpr int kRow = ZERO_ROW;
+static_assert(kRow == 256, "one quad per lane and row");
+
+typedef float v4f __attribute__((ext_vector_type(4)));
+typedef unsigned int v2u __attribute__((ext_vector_type(2)));
+typedef unsigned int v4u __attribute__((ext_vector_type(4)));
+// fp32 gradients may start at any element: quads of 4-byte alignment
+typedef float v4f_a4 __attribute__((ext_vector_type(4), aligned(4)));
+
+// The plan's tables do not change while a kernel runs: reading them through
+// the constant address space keeps wave-uniform reads scalar.
+#define ZF_CONST __attribute__((address_space(4)))
+template <typename T>
+__device__ __forceinline__ const ZF_CONST T* as_const(const T* p) {
+    return (const ZF_CONST T*)(uintptr_t)p;
+}
+
+template <typename T>
+__device__ __forceinline__ T ldnt(const void* p) {
+    return __builtin_nontemporal_load(static_cast<const T*>(p));
+}
+template <typename T>
+__device__ __forceinline__ void stnt(void* p, T x) {
+    __builtin_nontemporal_store(x, static_cast<T*>(p));
+}
+
+// ---------------------------------------------------------------- formats
+__device__ __forceinline__ float h2f(uint32_t h) {
+    return (float)__builtin_bit_cast(_Float16, (uint16_t)h);
+}
+__device__ __forceinline__ float b2f(uint32_t h) { return __uint_as_float(h << 16); }
+template <int DT>
+__device__ __forceinline__ float cvt16(uint32_t h) {
+    return DT == ZERO_F16 ? h2f(h) : b2f(h);
+}
+// to binary16 / bfloat16, to nearest, ties to even, on the bit patterns (the
+// flat step's rounding: no hardware conversion mode is involved)
+__device__ __forceinline__ uint32_t f2h(float x) {
+    const uint32_t u = __float_as_uint(x);
+    const uint32_t sign = (u >> 16) & 0x8000u;
+    const uint32_t a = u & 0x7fffffffu;
+    uint32_t h;
+    if (a >= 0x7f800000u) h = a > 0x7f800000u ? 0x7e00u : 0x7c00u;
+    else if (a >= 0x477ff000u) h = 0x7c00u;                      // 65520 and more
+    else if (a >= 0x38800000u) {                                 // normal binary16
+        const uint32_t m = a - 0x38000000u;
+        h = (m + 0xfffu + ((m >> 13) & 1u)) >> 13;
+    } else {                                                     // quantum 2^-24 = ulp of 0.5
+        h = __float_as_uint(__uint_as_float(a) + 0.5f) - 0x3f000000u;
+    }
+    return sign | h;
+}
+__device__ __forceinline__ uint32_t f2b(float x) {
+    const uint32_t u = __float_as_uint(x);
+    if ((u & 0x7fffffffu) > 0x7f800000u) return ((u >> 16) & 0x8000u) | 0x7fc0u;
+    return (u + 0x7fffu + ((u >> 16) & 1u)) >> 16;
+}
+template <int DT>
+__device__ __forceinline__ uint32_t round16(float x) {
+    return DT == ZERO_F16 ? f2h(x) : f2b(x);
+}
+template <int DT>
+__device__ __forceinline__ float load_one(const void* p, int64_t i) {
+    if constexpr (DT == ZERO_F32) return static_cast<const float*>(p)[i];
+    else return cvt16<DT>(static_cast<const uint16_t*>(p)[i]);
+}
+
+// ---------------------------------------------------------------- lanes
+// DPP wave shifts (gfx9-family controls): the neighbour's value, `edge` in the
+// lane that has none.
+constexpr int kDppWaveShl1 = 0x130, kDppWaveShr1 = 0x138;
+__device__ __forceinline__ uint32_t from_above(uint32_t x, uint32_t edge) {
+    return (uint32_t)__builtin_amdgcn_update_dpp((int)edge, (int)x, kDppWaveShl1, 0xf, 0xf, false);
+}
+__device__ __forceinline__ uint32_t from_below(uint32_t x, uint32_t edge) {
+    return (uint32_t)__builtin_amdgcn_update_dpp((int)edge, (int)x, kDppWaveShr1, 0xf, 0xf, false);
+}
+__device__ __forceinline__ uint32_t lane_value(uint32_t x, int lane) {
+    return (uint32_t)__builtin_amdgcn_readlane((int)x, lane);
+}
+__device__ __forceinline__ double wave_sum(double x) {
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) x += __shfl_xor(x, off, 64);
+    return x;
+}
+__device__ __forceinline__ float wave_max(float x) {
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) x = fmaxf(x, __shfl_xor(x, off, 64));
+    return x;
+}
+// fixed order; valid in thread 0
+template <int WAVES>
+__device__ __forceinline__ double block_sum(double x) {
+    __shared__ double sh[WAVES];
+    x = wave_sum(x);
+    if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = x;
+    __syncthreads();
+    double t = 0.0;
+    if (threadIdx.x == 0) {
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) t += sh[w];
+    }
+    return t;
+}
+
+// ---------------------------------------------------------------- statistics
+// One block per span: E consecutive elements of one tensor, from the tensor's
+// first 16-byte boundary on (the first span also takes the elements before it,
+// the last one what is left).  Squares and sums in fp64, where the square of
+// an fp32 value is exact; the loss scale is a power of two, so it is applied
+// to the sum, exactly as to every element.
+constexpr int kStatU = 8;   // 16-byte loads in flight per thread
+
+template <int DT>
+__device__ __forceinline__ void add_squares(v4u w, double& s0, double& s1) {
+    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (DT == ZERO_F32) {
+            const double d = (double)__uint_as_float(x[i]);
+            if (i & 1) s1 = __builtin_fma(d, d, s1);
+            else s0 = __builtin_fma(d, d, s0);
+        } else {
+            const double a = (double)cvt16<DT>(x[i] & 0xffffu);
+            const double b = (double)cvt16<DT>(x[i] >> 16);
+            s0 = __builtin_fma(a, a, s0);
+            s1 = __builtin_fma(b, b, s1);
+        }
+    }
+}
+
+template <int DT>
+__global__ void __launch_bounds__(kThreads) multi_stats_kernel(MultiNormLaunch a) {
+    constexpr int kEs = DT == ZERO_F32 ? 4 : 2;
+    constexpr int kV = 16 / kEs;   // elements per 16-byte load
+    const int s = blockIdx.x;
+    const int k = as_const(a.span_tensor)[s];
+    const ZF_CONST MultiEntry* e = as_const(a.entries) + k;
+    const char* g = static_cast<const char*>(e->grad);
+    const int64_t n = e->numel;
+    const int local = s - e->span0;
+    const bool last = local == e->n_spans - 1;
+    int64_t head = (int64_t)((16 - ((uintptr_t)g & 15)) & 15) / kEs;
+    if (head > n) head = n;
+    int64_t lo = head + (int64_t)local * a.span;
+    if (lo > n) lo = n;
+    int64_t hi = lo + a.span;
+    if (hi > n || last) hi = n;
+    const char* base = g + lo * kEs;
+    const int nvec = (int)((hi - lo) / kV);   // a span holds at most 2^31 elements
+    const int tid = threadIdx.x;
+    double s0 = 0.0, s1 = 0.0;
+    int v = 0;
+    for (; v + kThreads * kStatU <= nvec; v += kThreads * kStatU) {
+        v4u w[kStatU];
+#pragma unroll
+        for (int u = 0; u < kStatU; ++u)
+            w[u] = ldnt<v4u>(base + 16 * (int64_t)(v + u * kThreads + tid));
+#pragma unroll
+        for (int u = 0; u < kStatU; ++u) add_squares<DT>(w[u], s0, s1);
+    }
+    if (v < nvec) {
+        v4u w[kStatU];
+#pragma unroll
+        for (int u = 0; u < kStatU; ++u) {
+            const int i = v + u * kThreads + tid;
+            w[u] = i < nvec ? ldnt<v4u>(base + 16 * (int64_t)i) : v4u{0u, 0u, 0u, 0u};
+        }
+#pragma unroll
+        for (int u = 0; u < kStatU; ++u) add_squares<DT>(w[u], s0, s1);
+    }
+    // fewer than kV elements after the last vector, fewer than kV before the first
+    const int64_t rest = lo + (int64_t)nvec * kV + tid;
+    if (rest < hi) {
+        const double d = (double)load_one<DT>(g, rest);
+        s0 = __builtin_fma(d, d, s0);
+    }
+    if (local == 0 && tid < head) {
+        const double d = (double)load_one<DT>(g, tid);
+        s1 = __builtin_fma(d, d, s1);
+    }
+    const double t = block_sum<kWaves>(s0 + s1);
+    if (tid == 0) {
+        const double inv = 1.0 / (double)a.st->loss_scale;   // a power of two
+        a.partials[s] = t * inv * inv;
+    }
+}
+
+// Block 0: the total; the others: one wave per tensor.
+constexpr int kFoldThreads = 1024;
+__global__ void __launch_bounds__(kFoldThreads) multi_fold_kernel(MultiNormLaunch a) {
+    const int lane = threadIdx.x & 63;
+    if (blockIdx.x == 0) {
+        double x = 0.0;
+        for (int i = threadIdx.x; i < a.n_spans; i += kFoldThreads) x += a.partials[i];
+        x = block_sum<kFoldThreads / 64>(x);
+        if (threadIdx.x == 0) {
+            const int bad = !isfinite(x);
+            a.st->sumsq = a.reset ? x : a.st->sumsq + x;
+            a.st->overflow = a.reset ? bad : a.st->overflow | bad;
+        }
+        return;
+    }
+    const int k = (int)(blockIdx.x - 1) * (kFoldThreads / 64) + (int)(threadIdx.x >> 6);
+    if (k >= a.n_tensors) return;
+    const int p0 = a.entries[k].span0, np = a.entries[k].n_spans;
+    double x = 0.0;
+    for (int i = lane; i < np; i += 64) x += a.partials[p0 + i];
+    x = wave_sum(x);
+    if (lane == 0) a.tensor_sumsq[k] = x;
+}
+
+// ---------------------------------------------------------------- step scalars
+struct StepScalars {
+    int skip;
+    float coef, inv, bc1, bc2, rs;
+    double rbc1;
+    uint32_t key;
+};
+__device__ __forceinline__ uint32_t mix(uint32_t h) {
+    h = (h ^ (h >> 16)) * 0x7FEB352Du;
+    h = (h ^ (h >> 15)) * 0x846CA68Bu;
+    return h ^ (h >> 16);
+}
+// The decisions of the flat step (skip, clip, unscale, bias corrections with
+// t = step + 1), and the 8-bit form's factors and random key.
+template <int BITS>
+__device__ __forceinline__ StepScalars read_step(const MultiAdamLaunch& a) {
+    const zero_step_state_t* st = a.st;
+    StepScalars s;
+    s.skip = (st->overflow | st->remote_overflow) != 0;
+    const double total = st->sumsq + st->remote_sumsq;
+    s.coef = 1.0f;
+    if (a.max_norm > 0.0) {
+        const double c = a.max_norm / (sqrt(total) + 1e-6);
+        s.coef = (float)(c < 1.0 ? c : 1.0);
+    }
+    s.inv = (float)(1.0 / (double)st->loss_scale);
+    const double bc1 = 1.0 - st->beta1_pow * a.beta1, bc2 = 1.0 - st->beta2_pow * a.beta2;
+    s.bc1 = (float)bc1;
+    s.bc2 = (float)bc2;
+    s.rs = 0.0f;
+    s.rbc1 = 1.0;
+    s.key = 0;
+    if constexpr (BITS == 8) {
+        s.rs = (float)(1.0 / sqrt(bc2));
+        s.rbc1 = bc1;
+        s.key = mix((uint32_t)st->step + 1u + a.seed);
+    }
+    return s;
+}
+struct TensorScalars {
+    float rate, keep;
+};
+template <int BITS>
+__device__ __forceinline__ TensorScalars tensor_scalars(const MultiAdamLaunch& a,
+                                                        const StepScalars& s,
+                                                        const ZF_CONST MultiEntry* e) {
+    const double lr = a.lr * e->lr_mult;
+    TensorScalars t;
+    t.keep = (float)(1.0 - lr * (a.wd * e->decay_mult));
+    t.rate = BITS == 8 ? (float)(lr / s.rbc1) : (float)lr;
+    return t;
+}
+
+// ---------------------------------------------------------------- 8-bit codes
+constexpr float kMost4 = 448.0f, kMost5 = 57344.0f;
+__device__ __forceinline__ float row_scale(float top, float most_inv) {
+    return top > 0.0f ? fmaxf(fminf(top, 0x1.fffffep127f) * most_inv, 0x1p-126f) : 0.0f;
+}
+// four second moments (times 1/scale) as e5m2, rounded with the row's numbers
+__device__ __forceinline__ uint32_t round_e5m2(const float v[4], float inv, uint32_t key, int lane) {
+    const uint32_t h = mix(key + (uint32_t)lane * 0x9E3779B9u);
+    uint32_t k = h * 0x2C1B3C6Du;
+    k ^= k >> 13;
+    const uint32_t r[4] = {h & 0xffffu, h >> 16, k & 0xffffu, k >> 16};
+    uint32_t out = 0;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        const uint32_t y = __float_as_uint(fmaxf(v[c] * inv, 0x1p-14f)) + (r[c] << 5);
+        uint32_t q = (y >> 21) - (112u << 2);     // exponent bias 127 -> 15
+        q = q < 0x7Bu ? q : 0x7Bu;                // not past 57344
+        out |= (v[c] > 0.0f ? q : 0u) << (8 * c);
+    }
+    return out;
+}
+
+// ---------------------------------------------------------------- the update
+// One lane's quad of one row.  m, v hold fp32 values or, with 8-bit states,
+// four codes in their first word.
+template <int BITS>
+struct Quad {
+    float p[4];
+    v4u m, v;          // BITS 8: .x only
+};
+template <int BITS>
+__device__ __forceinline__ void load_state(const MultiAdamLaunch& a, int64_t i, Quad<BITS>& q) {
+    const v4f x = ldnt<v4f>(a.p + i);
+    q.p[0] = x.x; q.p[1] = x.y; q.p[2] = x.z; q.p[3] = x.w;
+    if constexpr (BITS == 32) {
+        q.m = ldnt<v4u>(static_cast<const float*>(a.m) + i);
+        q.v = ldnt<v4u>(static_cast<const float*>(a.v) + i);
+    } else {
+        q.m.x = ldnt<uint32_t>(static_cast<const uint8_t*>(a.m) + i);
+        q.v.x = ldnt<uint32_t>(static_cast<const uint8_t*>(a.v) + i);
+    }
+}
+template <int BITS>
+__device__ __forceinline__ void store_state(const MultiAdamLaunch& a, int64_t i, const Quad<BITS>& q) {
+    stnt<v4f>(a.p + i, v4f{q.p[0], q.p[1], q.p[2], q.p[3]});
+    if constexpr (BITS == 32) {
+        stnt<v4u>(static_cast<float*>(a.m) + i, q.m);
+        stnt<v4u>(static_cast<float*>(a.v) + i, q.v);
+    } else {
+        stnt<uint32_t>(static_cast<uint8_t*>(a.m) + i, q.m.x);
+        stnt<uint32_t>(static_cast<uint8_t*>(a.v) + i, q.v.x);
+    }
+}
+
+// The update of a row's quads, in place; ms / vs: the row's scales (8-bit).
+template <int BITS>
+__device__ __forceinline__ void update_quad(const MultiAdamLaunch& a, const StepScalars& s,
+                                            const TensorScalars& t, const float gv[4],
+                                            Quad<BITS>& q, float& ms, float& vs, uint32_t key,
+                                            int lane) {
+    if constexpr (BITS == 32) {
+        float m[4] = {__uint_as_float(q.m.x), __uint_as_float(q.m.y), __uint_as_float(q.m.z),
+                      __uint_as_float(q.m.w)};
+        float v[4] = {__uint_as_float(q.v.x), __uint_as_float(q.v.y), __uint_as_float(q.v.z),
+                      __uint_as_float(q.v.w)};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const float u = gv[c] * s.inv;
+            const float g = u * s.coef;
+            m[c] = a.b1 * m[c] + a.c1 * g;
+            v[c] = a.b2 * v[c] + a.c2 * (g * g);
+            const float mh = m[c] / s.bc1;
+            const float vh = v[c] / s.bc2;
+            const float d = sqrtf(vh) + a.eps;
+            q.p[c] = q.p[c] * t.keep - (t.rate * mh) / d;
+        }
+        q.m = v4u{__float_as_uint(m[0]), __float_as_uint(m[1]), __float_as_uint(m[2]),
+                  __float_as_uint(m[3])};
+        q.v = v4u{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                  __float_as_uint(v[3])};
+    } else {
+        typedef float v2f __attribute__((ext_vector_type(2)));
+        const v2f m01 = __builtin_amdgcn_cvt_pk_f32_fp8((int)q.m.x, false);
+        const v2f m23 = __builtin_amdgcn_cvt_pk_f32_fp8((int)q.m.x, true);
+        const v2f v01 = __builtin_amdgcn_cvt_pk_f32_bf8((int)q.v.x, false);
+        const v2f v23 = __builtin_amdgcn_cvt_pk_f32_bf8((int)q.v.x, true);
+        float m[4] = {m01.x, m01.y, m23.x, m23.y}, v[4] = {v01.x, v01.y, v23.x, v23.y};
+        float tm = 0.0f, tv = 0.0f;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const float u = gv[c] * s.inv;
+            const float g = u * s.coef;
+            m[c] = a.b1 * (m[c] * ms) + a.c1 * g;
+            v[c] = a.b2 * (v[c] * vs) + a.c2 * (g * g);
+            const float d = sqrtf(v[c]) * s.rs + a.eps;
+            q.p[c] = q.p[c] * t.keep - (t.rate * m[c]) / d;
+            tm = fmaxf(tm, fabsf(m[c]));
+            tv = fmaxf(tv, v[c]);
+        }
+        ms = row_scale(wave_max(tm), 1.0f / kMost4);
+        vs = row_scale(wave_max(tv), 1.0f / kMost5);
+        const float mi = ms > 0.0f ? 1.0f / ms : 0.0f;
+        const float vi = vs > 0.0f ? 1.0f / vs : 0.0f;
+        int w = __builtin_amdgcn_cvt_pk_fp8_f32(m[0] * mi, m[1] * mi, 0, false);
+        q.m.x = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(m[2] * mi, m[3] * mi, w, true);
+        q.v.x = round_e5m2(v, vi, key, lane);
+    }
+}
+
+// A tile's gradients at any element offset.  16-bit: aligned 8-byte words from
+// the one that holds the tile's first element; with the tile ms elements into
+// it, a quad is the upper part of its lane's word and the lower part of the
+// next lane's (the next row's first word for lane 63; one more word after the
+// last row).  Every word read holds an element of the tile, so none leaves the
+// memory the tensor lies in.  fp32: quads of 4-byte alignment.
+template <int GT, int R>
+struct GradTile {
+    v4f f[GT == ZERO_F32 ? R : 1];
+    v2u w[GT == ZERO_F32 ? 1 : R + 1];
+    int ms;
+    __device__ __forceinline__ void load(const void* g, int lane) {
+        if constexpr (GT == ZERO_F32) {
+#pragma unroll
+            for (int u = 0; u < R; ++u)
+                f[u] = ldnt<v4f_a4>(static_cast<const float*>(g) + u * kRow + 4 * lane);
+        } else {
+            const uintptr_t at = (uintptr_t)g;
+            ms = __builtin_amdgcn_readfirstlane((int)(at >> 1) & 3);
+            const char* base = reinterpret_cast<const char*>(at & ~(uintptr_t)7);
+#pragma unroll
+            for (int u = 0; u < R; ++u) w[u] = ldnt<v2u>(base + u * 2 * kRow + 8 * lane);
+            if (ms) w[R] = *reinterpret_cast<const v2u*>(base + R * 2 * kRow);
+        }
+    }
+    __device__ __forceinline__ void quad(int u, float out[4]) const {
+        if constexpr (GT == ZERO_F32) {
+            out[0] = f[u].x; out[1] = f[u].y; out[2] = f[u].z; out[3] = f[u].w;
+        } else {
+            uint32_t lo = w[u].x, hi = w[u].y;
+            if (ms) {
+                const uint32_t nlo = from_above(lo, lane_value(w[u + 1].x, 0));
+                const uint32_t nhi = from_above(hi, lane_value(w[u + 1].y, 0));
+                const uint64_t x = ((uint64_t)hi << 32 | lo) >> (16 * ms) |
+                                   ((uint64_t)nhi << 32 | nlo) << (64 - 16 * ms);
+                lo = (uint32_t)x;
+                hi = (uint32_t)(x >> 32);
+            }
+            out[0] = cvt16<GT>(lo & 0xffffu);
+            out[1] = cvt16<GT>(lo >> 16);
+            out[2] = cvt16<GT>(hi & 0xffffu);
+            out[3] = cvt16<GT>(hi >> 16);
+        }
+    }
+};
+
+// A full tile's 16-bit parameters at any element offset: whole aligned words,
+// each joined from a lane's values and the top of the lane below; the words
+// shared with the tiles before and after are written element by element.
+template <int R>
+struct CopyTile {
+    uint16_t* lp;
+    int ms;
+    uint32_t carry_lo, carry_hi;
+    __device__ __forceinline__ explicit CopyTile(uint16_t* at)
+        : lp(at), ms((int)((uintptr_t)at >> 1) & 3), carry_lo(0), carry_hi(0) {}
+    __device__ __forceinline__ void store(int u, const uint32_t h[4], int lane) {
+        const int e = u * kRow + 4 * lane;
+        const uint32_t lo = h[0] | h[1] << 16, hi = h[2] | h[3] << 16;
+        if (ms == 0) {
+            stnt<v2u>(lp + e, v2u{lo, hi});
+            return;
+        }
+        const uint32_t blo = from_below(lo, carry_lo), bhi = from_below(hi, carry_hi);
+        const uint64_t x = ((uint64_t)hi << 32 | lo) << (16 * ms) |
+                           ((uint64_t)bhi << 32 | blo) >> (64 - 16 * ms);
+        carry_lo = lane_value(lo, 63);
+        carry_hi = lane_value(hi, 63);
+        if (u == 0 && lane == 0) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                if (c < 4 - ms) lp[c] = (uint16_t)h[c];
+        } else {
+            stnt<v2u>(lp + e - ms, v2u{(uint32_t)x, (uint32_t)(x >> 32)});
+        }
+        if (u == R - 1 && lane == 63) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                if (c >= 4 - ms) lp[e + c] = (uint16_t)h[c];
+        }
+    }
+};
+
+// A tile of R whole rows: every load is issued before any arithmetic.
+template <int GT, int PT, int BITS, int R>
+__device__ __forceinline__ void tile_full(const MultiAdamLaunch& a, const StepScalars& s,
+                                          const TensorScalars& t, const char* g, uint16_t* lp,
+                                          int64_t row, int lane) {
+    GradTile<GT, R> gt;
+    Quad<BITS> q[R];
+    gt.load(g, lane);
+#pragma unroll
+    for (int u = 0; u < R; ++u) load_state<BITS>(a, (row + u) * kRow + 4 * lane, q[u]);
+    uint32_t scales = 0;   // lane u: the m scale of row u, lane R + u: its v scale
+    if constexpr (BITS == 8)
+        if (lane < 2 * R)
+            scales = __float_as_uint(lane < R ? a.ms[row + lane] : a.vs[row + lane - R]);
+    CopyTile<R> copy(lp);
+    uint32_t out = 0;
+#pragma unroll
+    for (int u = 0; u < R; ++u) {
+        float gv[4];
+        gt.quad(u, gv);
+        float ms = 0.0f, vs = 0.0f;
+        uint32_t key = 0;
+        if constexpr (BITS == 8) {
+            ms = __uint_as_float(lane_value(scales, u));
+            vs = __uint_as_float(lane_value(scales, R + u));
+            key = mix(s.key + (uint32_t)(row + u));
+        }
+        update_quad<BITS>(a, s, t, gv, q[u], ms, vs, key, lane);
+        store_state<BITS>(a, (row + u) * kRow + 4 * lane, q[u]);
+        if constexpr (PT != ZERO_NONE) {
+            uint32_t h[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) h[c] = round16<PT>(q[u].p[c]);
+            copy.store(u, h, lane);
+        }
+        if constexpr (BITS == 8) {
+            if (lane == u) out = __float_as_uint(ms);
+            if (lane == R + u) out = __float_as_uint(vs);
+        }
+    }
+    if constexpr (BITS == 8)
+        if (lane < 2 * R)
+            (lane < R ? a.ms : a.vs - R)[row + lane] = __uint_as_float(out);
+}
+
+// A tensor's last tile: its rows one at a time, the last row of n % 256
+// elements; gradient and copy element-wise.
+template <int GT, int PT, int BITS>
+__device__ __forceinline__ void tile_part(const MultiAdamLaunch& a, const StepScalars& s,
+                                          const TensorScalars& t, const char* g, uint16_t* lp,
+                                          int64_t row, int64_t left, int lane) {
+#pragma unroll 1
+    for (; left > 0; left -= kRow, row += 1, lp += kRow, g += kRow * (GT == ZERO_F32 ? 4 : 2)) {
+        Quad<BITS> q;
+        load_state<BITS>(a, row * kRow + 4 * lane, q);
+        float gv[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) gv[c] = 4 * lane + c < left ? load_one<GT>(g, 4 * lane + c) : 0.0f;
+        float ms = 0.0f, vs = 0.0f;
+        uint32_t key = 0;
+        if constexpr (BITS == 8) {
+            ms = a.ms[row];
+            vs = a.vs[row];
+            key = mix(s.key + (uint32_t)row);
+        }
+        update_quad<BITS>(a, s, t, gv, q, ms, vs, key, lane);
+        store_state<BITS>(a, row * kRow + 4 * lane, q);
+        if constexpr (PT != ZERO_NONE) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                if (4 * lane + c < left) lp[4 * lane + c] = (uint16_t)round16<PT>(q.p[c]);
+        }
+        if constexpr (BITS == 8) {
+            if (lane == 0) {
+                a.ms[row] = ms;
+                a.vs[row] = vs;
+            }
+        }
+    }
+}
+
+template <int GT, int PT, int BITS>
+__global__ void __launch_bounds__(kThreads) multi_adamw_kernel(MultiAdamLaunch a) {
+    constexpr int R = BITS == 8 ? kMultiRows8 : kMultiRows32;
+    constexpr int kGs = GT == ZERO_F32 ? 4 : 2;
+    const StepScalars s = read_step<BITS>(a);
+    if (s.skip) return;
+    const int lane = threadIdx.x & 63;
+    const int tile = (int)blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    if (tile >= a.n_tiles) return;
+    const ZF_CONST MultiEntry* e = as_const(a.entries) + as_const(a.tile_tensor)[tile];
+    const int64_t row_in = (int64_t)(tile - e->tile0) * R;
+    const int64_t at = row_in * kRow;
+    const int64_t left = e->numel - at;
+    const int64_t row = e->row0 + row_in;
+    const char* g = static_cast<const char*>(e->grad) + at * kGs;
+    uint16_t* lp = PT == ZERO_NONE ? nullptr : static_cast<uint16_t*>(e->param) + at;
+    const TensorScalars t = tensor_scalars<BITS>(a, s, e);
+    if (left >= R * kRow) tile_full<GT, PT, BITS, R>(a, s, t, g, lp, row, lane);
+    else tile_part<GT, PT, BITS>(a, s, t, g, lp, row, left, lane);
+}
+
+// The loss scaler and the counters, as the flat step's (one thread).
+__global__ void multi_finalize_kernel(zero_step_state_t* st, double beta1, double beta2,
+                                      double max_norm) {
+    if (threadIdx.x != 0) return;
+    const double total = st->sumsq + st->remote_sumsq;
+    const int skip = (st->overflow | st->remote_overflow) != 0;
+    float coef = 1.0f;
+    if (max_norm > 0.0) {
+        const double c = max_norm / (sqrt(total) + 1e-6);
+        coef = (float)(c < 1.0 ? c : 1.0);
+    }
+    st->last_norm = sqrt(total);
+    st->last_skipped = skip;
+    st->last_coef = skip ? 0.0f : coef;
+    if (skip) {
+        if (st->dynamic) {
+            const float h = st->loss_scale / 2.0f;
+            st->loss_scale = h > st->min_scale ? h : st->min_scale;
+        }
+        st->good_steps = 0;
+    } else {
+        st->step = st->step + 1;
+        st->beta1_pow = st->beta1_pow * beta1;
+        st->beta2_pow = st->beta2_pow * beta2;
+        if (st->dynamic) {
+            st->good_steps = st->good_steps + 1;
+            if (st->good_steps == st->window) {
+                if (st->loss_scale < 0x1p127f) st->loss_scale = st->loss_scale * 2.0f;
+                st->good_steps = 0;
+            }
+        }
+    }
+    st->sumsq = 0.0;
+    st->overflow = 0;
+}
+
+template <int GT, int PT>
+void launch_update(const MultiAdamLaunch& a, unsigned grid, hipStream_t s) {
+    if (a.bits == 8)
+        hipLaunchKernelGGL((multi_adamw_kernel<GT, PT, 8>), dim3(grid), dim3(kThreads), 0, s, a);
+    else
+        hipLaunchKernelGGL((multi_adamw_kernel<GT, PT, 32>), dim3(grid), dim3(kThreads), 0, s, a);
+}
+template <int GT>
+void launch_update(const MultiAdamLaunch& a, unsigned grid, hipStream_t s) {
+    if (a.pdtype == ZERO_F16) launch_update<GT, ZERO_F16>(a, grid, s);
+    else if (a.pdtype == ZERO_BF16) launch_update<GT, ZERO_BF16>(a, grid, s);
+    else launch_update<GT, ZERO_NONE>(a, grid, s);
+}
+
+}  // namespace
+
+int launch_multi_norm(const MultiNormLaunch& a, void* stream) {
+    hipStream_t s = (hipStream_t)stream;
+    if (a.n_spans > 0) {
+        const dim3 grid((unsigned)a.n_spans), block(kThreads);
+        if (a.dtype == ZERO_F32)
+            hipLaunchKernelGGL((multi_stats_kernel<ZERO_F32>), grid, block, 0, s, a);
+        else if (a.dtype == ZERO_F16)
+            hipLaunchKernelGGL((multi_stats_kernel<ZERO_F16>), grid, block, 0, s, a);
+        else
+            hipLaunchKernelGGL((multi_stats_kernel<ZERO_BF16>), grid, block, 0, s, a);
+        const int e = (int)hipGetLastError();
+        if (e) return e;
+    }
+    const unsigned per = kFoldThreads / 64;
+    hipLaunchKernelGGL(multi_fold_kernel, dim3(1 + ((unsigned)a.n_tensors + per - 1) / per),
+                       dim3(kFoldThreads), 0, s, a);
+    return (int)hipGetLastError();
+}
+
+int launch_multi_adamw(const MultiAdamLaunch& a, void* stream) {
+    hipStream_t s = (hipStream_t)stream;
+    if (a.n_tiles > 0) {
+        const unsigned grid = ((unsigned)a.n_tiles + kWaves - 1) / kWaves;
+        if (a.gdtype == ZERO_F32) launch_update<ZERO_F32>(a, grid, s);
+        else if (a.gdtype == ZERO_F16) launch_update<ZERO_F16>(a, grid, s);
+        else launch_update<ZERO_BF16>(a, grid, s);
+        const int e = (int)hipGetLastError();
+        if (e) return e;
+    }
+    if (a.flags & ZERO_STEP_FINALIZE) {
+        hipLaunchKernelGGL(multi_finalize_kernel, dim3(1), dim3(64), 0, s, a.st, a.beta1, a.beta2,
+                           a.max_norm);
+        return (int)hipGetLastError();
+    }
+    return 0;
+}
+
+}  // namespace zf

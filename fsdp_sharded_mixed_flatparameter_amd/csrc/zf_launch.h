@@ -82,6 +82,59 @@ struct DequantLaunch {
 };
 int launch_dequant(const DequantLaunch& a, void* stream);
 
+// The step over a list of tensors (zeroflat_multi.hip).  One table entry per
+// tensor, in the plan's device image.
+struct MultiEntry {
+    const void* grad;
+    void* param;         // 16-bit copy, or null
+    int64_t numel;
+    int64_t row0;        // first row of the arenas
+    double lr_mult;
+    double decay_mult;
+    int32_t tile0;       // first tile of the update
+    int32_t span0;       // first span of the statistics
+    int32_t n_spans;
+    int32_t reserved;
+};
+static_assert(sizeof(MultiEntry) == 64, "the table's entries are 64 bytes");
+
+// rows of one wave's tile of the update
+constexpr int kMultiRows32 = 4, kMultiRows8 = 8;
+// counters of a plan's image, 32-bit, zero between launches
+constexpr int kMultiCounters = 64;
+
+struct MultiNormLaunch {
+    const MultiEntry* entries;
+    const int32_t* span_tensor;
+    double* tensor_sumsq;
+    double* partials;
+    unsigned* counters;
+    int64_t span;
+    int32_t n_tensors, n_spans;
+    int32_t dtype;
+    int32_t reset;
+    zero_step_state_t* st;
+};
+int launch_multi_norm(const MultiNormLaunch& a, void* stream);
+
+struct MultiAdamLaunch {
+    const MultiEntry* entries;
+    const int32_t* tile_tensor;
+    unsigned* counters;
+    float* p;
+    void* m;
+    void* v;
+    float* ms;
+    float* vs;
+    int32_t n_tiles;
+    int32_t gdtype, pdtype, bits;
+    uint32_t flags, seed;
+    float b1, c1, b2, c2, eps;
+    double lr, wd, beta1, beta2, max_norm;
+    zero_step_state_t* st;
+};
+int launch_multi_adamw(const MultiAdamLaunch& a, void* stream);
+
 // ZeRO-Offload (zeroflat_offload.cpp).  The host update over host arrays:
 // *skipped = 1 (and nothing written) when the state says overflow.
 int offload_adam_host(const void* g, int32_t gdt, float* p, float* m, float* v, int64_t n,

@@ -1,0 +1,180 @@
+"""One rank's optimizer over a list of tensors: the plan that names them to the
+library, and the optimizer that owns the state arenas and issues the calls of
+one step.  No arithmetic happens here; the statistics and the step run in
+libzeroflat.
+"""
+import ctypes as C
+import itertools
+
+import torch
+
+from . import (_DTYPE_CODES, _FLOATS, ZERO_NONE, ZERO_ROW, StepState, _check, _current_raw_stream,
+               _dev, _dtype_name, _lib, zero_adamw_hparams_t, zero_multi_adamw_step,
+               zero_multi_plan_t, zero_multi_unscale_norm)
+
+
+def _doubles(x, n, name):
+    if x is None:
+        return None
+    x = [float(v) for v in x]
+    if len(x) != n:
+        raise ValueError("%s must have one entry per tensor (%d)" % (name, n))
+    return (C.c_double * max(n, 1))(*x)
+
+
+class MultiPlan:
+    """The tables and the workspace of a list of tensors, on the device.
+
+    `numels` and the dtypes are fixed; bind() names the tensors and may be called
+    again whenever they move.  The plan keeps the tensors alive.  A plan is used
+    by one stream at a time."""
+
+    def __init__(self, numels, grad_dtype, param_dtype=None, state_bits=0, device="cuda"):
+        numels = [int(x) for x in numels]
+        n = len(numels)
+        gname = _dtype_name(grad_dtype)
+        pname = None if param_dtype is None else _dtype_name(param_dtype)
+        if gname not in _FLOATS:
+            raise ValueError("grad_dtype must be %s" % " or ".join(_FLOATS))
+        if pname not in (None, "float16", "bfloat16"):
+            raise ValueError("param_dtype must be float16 or bfloat16, or None")
+        self.numels, self.grad_dtype, self.param_dtype = numels, grad_dtype, param_dtype
+        self.state_bits = state_bits
+        self._plan = zero_multi_plan_t()
+        self._ref = C.byref(self._plan)
+        arr = (C.c_int64 * max(n, 1))(*numels)
+        args = (arr, n, _DTYPE_CODES[gname], ZERO_NONE if pname is None else _DTYPE_CODES[pname],
+                state_bits, self._ref)
+        _check(_lib.zero_multi_plan_init(*args, None, 0))
+        self.rows = self._plan.rows
+        host = torch.empty(self._plan.image_bytes, dtype=torch.uint8)
+        _check(_lib.zero_multi_plan_init(*args, C.c_void_p(host.data_ptr()), host.numel()))
+        self._image = host.to(device)
+        self._image_ptr = C.c_void_p(self._image.data_ptr())
+        self._entries = host[:self._plan.bind_bytes].clone()
+        off = self._plan.sumsq_off
+        self.tensor_sumsq = self._image[off:off + 8 * n].view(torch.float64)
+        self._grads = self._params = None
+        self._bound = n == 0
+
+    def __len__(self):
+        return len(self.numels)
+
+    def _require_bound(self):
+        if not self._bound:
+            raise RuntimeError("the plan names no tensors yet: call bind first")
+
+    def _tensors(self, tensors, name, dtype):
+        tensors = list(tensors)
+        if len(tensors) != len(self):
+            raise ValueError("%s must have one entry per tensor (%d)" % (name, len(self)))
+        for k, (t, n) in enumerate(zip(tensors, self.numels)):
+            _dev(t, "%s[%d]" % (name, k), (_dtype_name(dtype),))
+            if t.numel() != n:
+                raise ValueError("%s[%d] has %d elements, the plan says %d" % (name, k, t.numel(), n))
+            if t.device != self._image.device:
+                raise ValueError("%s[%d] is on %s, the plan on %s" % (name, k, t.device,
+                                                                     self._image.device))
+        return tensors, (C.c_void_p * max(len(self), 1))(*[t.data_ptr() or None for t in tensors])
+
+    def bind(self, grads, params=None, lr_mult=None, decay_mult=None):
+        """Name the gradients, and the 16-bit parameters if the plan has them,
+        with a learning-rate and a decay factor per tensor (all ones when not
+        given).  Copies the table to the device and waits for the device before
+        and after, so no step in flight sees half of it; not during capture."""
+        grads, g = self._tensors(grads, "grads", self.grad_dtype)
+        p = None
+        if self.param_dtype is None:
+            if params is not None:
+                raise ValueError("the plan has no param_dtype")
+        elif params is None:
+            raise ValueError("the plan has a param_dtype: params are needed")
+        else:
+            params, p = self._tensors(params, "params", self.param_dtype)
+        if torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("bind copies from the host: not during graph capture")
+        _check(_lib.zero_multi_bind(self._ref, g, p, _doubles(lr_mult, len(self), "lr_mult"),
+                                    _doubles(decay_mult, len(self), "decay_mult"),
+                                    C.c_void_p(self._entries.data_ptr())))
+        if len(self):
+            torch.cuda.synchronize(self._image.device)
+            self._image[:self._plan.bind_bytes].copy_(self._entries)
+            torch.cuda.synchronize(self._image.device)
+        self._grads, self._params, self._bound = grads, params, True
+
+
+class TensorListOptimizer:
+    """AdamW over a list of tensors with one step state: one norm, clip, skip
+    and loss scale over all of them, and a learning-rate and decay factor each.
+
+    master, exp_avg and exp_avg_sq are arenas of rows of 256 elements, tensor k
+    from row first_row[k] on (views() gives the tensors inside one); the
+    constructor copies `masters` into the first.  With state_bits 8, exp_avg is
+    e4m3 and exp_avg_sq e5m2, with one scale per row in exp_avg_scale and
+    exp_avg_sq_scale, and `seed` fixes the second moment's random rounding.
+    bind() names the gradients and the 16-bit parameters that step() reads and
+    writes; without a param_dtype the fp32 master is all there is.  With
+    statistics=False a step neither clips nor looks for an overflow."""
+
+    def __init__(self, masters, hp, state_bits=32, loss_scale=65536.0, dynamic=False, window=1000,
+                 min_scale=1.0, lr_mult=None, decay_mult=None, statistics=True, seed=0,
+                 grad_dtype=torch.bfloat16, param_dtype=torch.bfloat16):
+        masters = list(masters)
+        if not masters:
+            raise ValueError("need at least one master tensor")
+        for k, t in enumerate(masters):
+            _dev(t, "masters[%d]" % k, ("float32",))
+        if state_bits not in (8, 32):
+            raise ValueError("state_bits must be 32 or 8")
+        if not statistics and hp.get("max_grad_norm", 0.0) > 0.0:
+            raise ValueError("clipping needs the statistics: max_grad_norm must be 0 without them")
+        dev = masters[0].device
+        n = [t.numel() for t in masters]
+        self.plan = MultiPlan(n, grad_dtype, param_dtype, state_bits, device=dev)
+        rows = [-(-x // ZERO_ROW) for x in n]
+        self.first_row = [0] + list(itertools.accumulate(rows))[:-1]
+        size = self.plan.rows * ZERO_ROW
+        self.master = torch.zeros(size, device=dev)
+        kinds = (torch.float8_e4m3fn, torch.float8_e5m2) if state_bits == 8 else (torch.float32,) * 2
+        self.exp_avg, self.exp_avg_sq = (
+            torch.zeros(size * k.itemsize, dtype=torch.uint8, device=dev).view(k) for k in kinds)
+        self.exp_avg_scale = self.exp_avg_sq_scale = None
+        if state_bits == 8:
+            self.exp_avg_scale = torch.zeros(self.plan.rows, device=dev)
+            self.exp_avg_sq_scale = torch.zeros(self.plan.rows, device=dev)
+        for v, t in zip(self.views(self.master), masters):
+            v.copy_(t.view(-1))
+        self.hp = dict(hp)
+        self.statistics, self.seed = bool(statistics), int(seed)
+        self.lr_mult, self.decay_mult = lr_mult, decay_mult
+        self.state = StepState(loss_scale, dynamic, window, min_scale, device=dev)
+        self._h = (None, None)   # (hp items, their C struct)
+
+    def views(self, arena):
+        """The tensors inside an arena (flat views, without the rows' padding)."""
+        return [arena[r * ZERO_ROW:r * ZERO_ROW + n]
+                for r, n in zip(self.first_row, self.plan.numels)]
+
+    def bind(self, grads, params=None):
+        """Name the gradients and the 16-bit parameters; again when they move."""
+        self.plan.bind(grads, params, self.lr_mult, self.decay_mult)
+
+    def _hparams(self):
+        """The C hyper-parameter struct, rebuilt only when self.hp changed."""
+        key = tuple(self.hp.items())
+        if self._h[0] != key:
+            if not self.statistics and self.hp.get("max_grad_norm", 0.0) > 0.0:
+                raise ValueError("clipping needs the statistics: max_grad_norm must be 0 without them")
+            self._h = (key, zero_adamw_hparams_t(**self.hp))
+        return self._h[1]
+
+    def step(self, stream=None):
+        """Statistics over the bound gradients, then the step."""
+        if stream is None:
+            stream = _current_raw_stream()
+        h = self._hparams()
+        if self.statistics:
+            zero_multi_unscale_norm(self.plan, self.state, stream=stream)
+        zero_multi_adamw_step(self.plan, self.master, self.exp_avg, self.exp_avg_sq, h, self.state,
+                              self.exp_avg_scale, self.exp_avg_sq_scale, seed=self.seed,
+                              stream=stream)

@@ -28,6 +28,9 @@
  *   8. zero_offload_adamw_host / zero_offload_step  ZeRO-Offload: the step of
  *                              3 on host cores over host-resident fp32 state,
  *                              with the transfers pipelined around it.
+ *   9. zero_multi_unscale_norm / zero_multi_adamw_step  the statistics and the
+ *                              step of 2 and 3 over a list of tensors, with
+ *                              32-bit or 8-bit states.
  *
  * Sources (three web pages, cited by title and section):
  *   "DeepSpeed 与 FSDP" (docs.ifdog.com): ZeRO-1/2/3 memory arithmetic,
@@ -431,6 +434,112 @@ int zero_offload_step(const void* d_grad, int32_t grad_dtype, int64_t n, float* 
                       void* d_allgather, int32_t param_dtype, int64_t slot_offset,
                       const zero_adamw_hparams_t* hp, zero_step_state_t* d_state, int64_t chunk,
                       int32_t n_threads, void* stream);
+/* ------------------------------------------------------------------------
+ * 9. The step over a list of tensors.
+ *
+ * Sections 2 and 3 work on one flat shard.  A rank that keeps its parameters
+ * as tensors of their own (per-parameter shards, adapters, the unflattened
+ * views of a bucket) has hundreds of them, with a learning-rate and decay
+ * factor each; these entry points take the whole list in one launch per pass.
+ *
+ * State arenas: master, exp_avg and exp_avg_sq of a list are arrays of rows of
+ * ZERO_ROW elements.  Tensor k takes ceil(numel_k / ZERO_ROW) consecutive
+ * rows, its last row padded with zeros, which stay zero.  A row is also the
+ * block of the 8-bit states.  Gradients and 16-bit parameters stay where the
+ * caller has them, at any element offset.
+ *
+ * The plan: a host struct of sizes, and one device buffer (plan->image_bytes
+ * bytes, 256-byte aligned) holding the list's tables and the workspace.
+ *   zero_multi_plan_init  sizes *plan from the list; with `image` also fills
+ *     a HOST copy of that buffer, which the caller copies to the device once.
+ *   zero_multi_bind       writes the list's pointers and factors into the host
+ *     copy; they lie in its first plan->bind_bytes bytes, which is all the
+ *     caller copies again.
+ * Both are host arithmetic.  The tensors are only named by address: the caller
+ * keeps them alive, and copies the image again when one of them moves.
+ * A plan, like a step state, must not be used by two streams at once.
+ * ---------------------------------------------------------------------- */
+#define ZERO_ROW 256
+#define ZERO_NONE (-1)            /* param_dtype: no 16-bit copy of the parameters */
+#define ZERO_MAX_TENSORS (1 << 20)
+
+typedef struct {
+    int64_t total;       /* elements of the list */
+    int64_t rows;        /* rows of every state arena */
+    int64_t image_bytes; /* size of the device buffer */
+    int64_t bind_bytes;  /* its first part, rewritten by zero_multi_bind */
+    int64_t sumsq_off;   /* byte offset of the per-tensor sums, double[n_tensors] */
+    /* internal: the other parts of the buffer and the launch shapes */
+    int64_t tiles_off, spans_off, partials_off, counters_off;
+    int64_t span;        /* elements one block of the statistics pass reads */
+    int32_t n_tensors, grad_dtype, param_dtype, state_bits;
+    int32_t n_tiles, n_spans;
+} zero_multi_plan_t;
+
+/* numels: HOST int64[n_tensors], each >= 0, 0 <= n_tensors <=
+ * ZERO_MAX_TENSORS.  grad_dtype: of every gradient.  param_dtype: ZERO_F16,
+ * ZERO_BF16 or ZERO_NONE.  state_bits: 32 or 8, or 0 for a plan that only
+ * serves the statistics.  image: NULL, or HOST memory of image_bytes >=
+ * plan->image_bytes, 8-byte aligned. */
+int zero_multi_plan_init(const int64_t* numels, int32_t n_tensors, int32_t grad_dtype,
+                         int32_t param_dtype, int32_t state_bits, zero_multi_plan_t* plan,
+                         void* image, int64_t image_bytes);
+
+/* grads / params: HOST arrays of n_tensors DEVICE pointers (params NULL when
+ * the plan has no param_dtype); an empty tensor's may be NULL.  lr_mult /
+ * decay_mult: HOST double[n_tensors] >= 0, or NULL for all ones. */
+int zero_multi_bind(const zero_multi_plan_t* plan, const void* const* grads, void* const* params,
+                    const double* lr_mult, const double* decay_mult, void* image);
+
+/* Statistics over the list: with u = f32(g) * (1/loss_scale),
+ *   tensor_sumsq[k] = sum of (double)u^2 over tensor k (plan->sumsq_off)
+ *   sumsq += their sum;  overflow |= (that sum is not finite)
+ * as zero_unscale_norm takes them over a shard, in an order fixed by the list's
+ * sizes and its gradients' alignment.  With ZERO_MULTI_RESET sumsq and
+ * overflow are set instead (statistics outside a step; the scaler and
+ * counters are not touched). */
+#define ZERO_MULTI_RESET 2u
+int zero_multi_unscale_norm(const zero_multi_plan_t* plan, void* d_plan, uint32_t flags,
+                            zero_step_state_t* d_state, void* stream);
+
+/* One AdamW step over the list: skip, clip, update, 16-bit copy and (flags &
+ * ZERO_STEP_FINALIZE) the loss-scaler / counter update, as section 3 has them,
+ * with the step state's statistics and, per tensor, lr_k = lr * lr_mult[k] and
+ * wd_k = weight_decay * decay_mult[k].  Per element, each a separately rounded
+ * fp32 operation unless said otherwise:
+ *     u = f32(grad) * (1/loss_scale);  g = u * coef
+ *     m = b1*m + c1*g;  v = b2*v + c2*(g*g)
+ *   state_bits 32 (exp_avg, exp_avg_sq: DEVICE fp32 arenas), section 3's order:
+ *     p = p*keep_k - (f32(lr_k) * (m/bc1)) / (sqrtf(v/bc2) + eps)
+ *   state_bits 8 (exp_avg: e4m3 arena, exp_avg_sq: e5m2 arena, one fp32 scale
+ *   per row each; a value is code * scale):
+ *     p = p*keep_k - (rate_k * m) / (sqrtf(v) * rs + eps)
+ *     rate_k = f32(lr_k / (1 - beta1^t)), rs = f32(1 / sqrt(1 - beta2^t))
+ *     (square root and quotient to about 2 units in the last place)
+ *   with keep_k = f32(1 - lr_k * wd_k).
+ * The 8-bit states are then written back per row: top = min(max|x|, FLT_MAX),
+ * scale = max(top * f32(1/most), 2^-126) (0 for a row of zeros), y =
+ * x * (1/scale); m (most 448) is rounded to the nearest e4m3, ties to even.
+ * v (most 57344) moves in a step by far less than the distance of two codes,
+ * so it is rounded at random, up with the probability of the part cut off:
+ * the 21 low bits of max(y, 2^-14)'s fp32 pattern are cut after adding 32 * r
+ * (not past most), r a 16-bit number fixed by (seed, t, row, place):
+ *     mix(h): h ^= h>>16; h *= 0x7FEB352D; h ^= h>>15; h *= 0x846CA68B; h ^= h>>16
+ *     h = mix(mix(mix(t + seed) + row) + (place/4) * 0x9E3779B9)   (mod 2^32)
+ *     k = h * 0x2C1B3C6D;  k ^= k >> 13
+ *     r = the low, high half of h, low, high half of k at place%4 = 0, 1, 2, 3
+ *   row counts from the arena's start.  A second moment above 0 never becomes
+ *   0.  Only a step without statistics meets a gradient that is not finite:
+ *   its parameter becomes NaN, its first moment's code NaN, its second
+ *   moment's 0 (NaN) or the largest (inf), and a NaN leaves its row's scales
+ *   to the other elements.
+ * master: DEVICE fp32 arena; m_scale / v_scale: DEVICE fp32[rows], NULL for
+ *   state_bits 32.  master and 32-bit states 16-byte, 8-bit states 4-byte aligned.
+ * ---------------------------------------------------------------------- */
+int zero_multi_adamw_step(const zero_multi_plan_t* plan, void* d_plan, float* master,
+                          void* exp_avg, void* exp_avg_sq, float* m_scale, float* v_scale,
+                          const zero_adamw_hparams_t* hp, uint32_t seed, uint32_t flags,
+                          zero_step_state_t* d_state, void* stream);
 #ifdef __cplusplus
 }
 #endif
