@@ -18,6 +18,7 @@ ZERO_F32, ZERO_F16, ZERO_BF16 = 0, 1, 2
 ZERO_SUM, ZERO_AVG = 0, 1
 ZERO_STEP_FINALIZE = 1
 ZERO_MULTI_RESET = 2
+ZERO_MULTI_STATISTICS = 4
 ZERO_ROW = 256
 ZERO_NONE = -1
 ZERO_MAX_RANKS = 256
@@ -67,7 +68,7 @@ class zero_adamw_hparams_t(C.Structure):
 class zero_multi_plan_t(C.Structure):
     _fields_ = [(f, C.c_int64) for f in
                 ("total", "rows", "image_bytes", "bind_bytes", "sumsq_off", "tiles_off",
-                 "spans_off", "partials_off", "counters_off", "span")] + \
+                 "spans_off", "partials_off", "scalars_off", "span")] + \
                [(f, C.c_int32) for f in
                 ("n_tensors", "grad_dtype", "param_dtype", "state_bits", "n_tiles", "n_spans")]
 
@@ -503,10 +504,12 @@ def zero_multi_unscale_norm(plan, state, reset=False, stream=None):
 
 
 def zero_multi_adamw_step(plan, master, exp_avg, exp_avg_sq, hp, state, exp_avg_scale=None,
-                          exp_avg_sq_scale=None, seed=0, finalize=True, stream=None):
+                          exp_avg_sq_scale=None, seed=0, finalize=True, statistics=False,
+                          stream=None):
     """Skip-on-overflow, clip and AdamW over the list bound to `plan`, on arenas
     of plan.rows rows of ZERO_ROW elements, with the 16-bit copies and the
-    scaler update."""
+    scaler update; with `statistics`, zero_multi_unscale_norm over the list
+    first."""
     plan._require_bound()
     n, q8 = plan.rows * ZERO_ROW, plan.state_bits == 8
     kinds = ("float8_e4m3fn", "float8_e5m2") if q8 else ("float32", "float32")
@@ -529,8 +532,9 @@ def zero_multi_adamw_step(plan, master, exp_avg, exp_avg_sq, hp, state, exp_avg_
     _check(_lib.zero_multi_adamw_step(plan._ref, plan._image_ptr, _ptr(master), _ptr(exp_avg),
                                       _ptr(exp_avg_sq), _ptr(exp_avg_scale),
                                       _ptr(exp_avg_sq_scale), C.byref(h), seed & 0xffffffff,
-                                      ZERO_STEP_FINALIZE if finalize else 0, _state_ptr(state),
-                                      _stream(stream)))
+                                      (ZERO_STEP_FINALIZE if finalize else 0) |
+                                      (ZERO_MULTI_STATISTICS if statistics else 0),
+                                      _state_ptr(state), _stream(stream)))
 
 
 from . import multi, shard  # noqa: E402

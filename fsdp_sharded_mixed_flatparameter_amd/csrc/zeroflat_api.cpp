@@ -562,6 +562,24 @@ int check_plan(const char* fn, const zero_multi_plan_t* plan) {
         return fail(ZERO_EINVAL, "%s: the plan is not one of zero_multi_plan_init", fn);
     return ZERO_OK;
 }
+
+zf::MultiNormLaunch norm_launch(const zero_multi_plan_t* plan, void* d_plan, int reset,
+                                zero_step_state_t* st) {
+    char* base = static_cast<char*>(d_plan);
+    zf::MultiNormLaunch a;
+    memset(&a, 0, sizeof a);
+    a.entries = reinterpret_cast<const zf::MultiEntry*>(base);
+    a.span_tensor = reinterpret_cast<const int32_t*>(base + plan->spans_off);
+    a.tensor_sumsq = reinterpret_cast<double*>(base + plan->sumsq_off);
+    a.partials = reinterpret_cast<double*>(base + plan->partials_off);
+    a.span = plan->span;
+    a.n_tensors = plan->n_tensors;
+    a.n_spans = plan->n_spans;
+    a.dtype = plan->grad_dtype;
+    a.reset = reset;
+    a.st = st;
+    return a;
+}
 }  // namespace
 
 int zero_multi_plan_init(const int64_t* numels, int32_t n_tensors, int32_t grad_dtype,
@@ -578,7 +596,6 @@ int zero_multi_plan_init(const int64_t* numels, int32_t n_tensors, int32_t grad_
         return fail(ZERO_EINVAL, "%s: param_dtype must be fp16, bf16 or none", fn);
     if (state_bits != 0 && state_bits != 8 && state_bits != 32)
         return fail(ZERO_EINVAL, "%s: state_bits must be 32, 8 or 0", fn);
-    const int64_t rows_per_tile = state_bits == 8 ? zf::kMultiRows8 : zf::kMultiRows32;
     int64_t total = 0, rows = 0, tiles = 0;
     for (int32_t k = 0; k < n_tensors; ++k) {
         if (numels[k] < 0) return fail(ZERO_EINVAL, "%s: numel[%d] < 0", fn, k);
@@ -588,7 +605,7 @@ int zero_multi_plan_init(const int64_t* numels, int32_t n_tensors, int32_t grad_
             return fail(ZERO_ERANGE, "%s: total overflows", fn);
         const int64_t r = ceil_div(numels[k], ZERO_ROW);
         rows += r;
-        tiles += ceil_div(r, rows_per_tile);
+        tiles += ceil_div(r, zf::kMultiRows);
     }
     int64_t span = kMinSpan;
     while (ceil_div(total, span) > kMaxSpans) span *= 2;
@@ -614,7 +631,7 @@ int zero_multi_plan_init(const int64_t* numels, int32_t n_tensors, int32_t grad_
     auto part = [&](int64_t bytes) { const int64_t at = off; off = round_up(off + bytes, 256); return at; };
     P.bind_bytes = (int64_t)n_tensors * (int64_t)sizeof(zf::MultiEntry);
     part(P.bind_bytes);
-    P.counters_off = part((int64_t)zf::kMultiCounters * 4);
+    P.scalars_off = part(sizeof(zf::MultiScalars));
     P.tiles_off = part(tiles * 4);
     P.spans_off = part(spans * 4);
     P.sumsq_off = part((int64_t)n_tensors * 8);
@@ -633,7 +650,7 @@ int zero_multi_plan_init(const int64_t* numels, int32_t n_tensors, int32_t grad_
         int64_t row = 0, tile = 0, sp = 0;
         for (int32_t k = 0; k < n_tensors; ++k) {
             const int64_t r = ceil_div(numels[k], ZERO_ROW);
-            const int64_t nt = state_bits ? ceil_div(r, rows_per_tile) : 0;
+            const int64_t nt = state_bits ? ceil_div(r, zf::kMultiRows) : 0;
             const int64_t ns = ceil_div(numels[k], span);
             e[k].numel = numels[k];
             e[k].row0 = row;
@@ -692,21 +709,10 @@ int zero_multi_unscale_norm(const zero_multi_plan_t* plan, void* d_plan, uint32_
     if (!aligned(d_plan, 256)) return fail(ZERO_EALIGN, "%s: plan buffer not 256-byte aligned", fn);
     if (!aligned(d_state, 8)) return fail(ZERO_EALIGN, "%s: state not 8-byte aligned", fn);
     if (flags & ~ZERO_MULTI_RESET) return fail(ZERO_EINVAL, "%s: unknown flags 0x%x", fn, flags);
-    char* base = static_cast<char*>(d_plan);
-    zf::MultiNormLaunch a;
-    memset(&a, 0, sizeof a);
-    a.entries = reinterpret_cast<const zf::MultiEntry*>(base);
-    a.span_tensor = reinterpret_cast<const int32_t*>(base + plan->spans_off);
-    a.tensor_sumsq = reinterpret_cast<double*>(base + plan->sumsq_off);
-    a.partials = reinterpret_cast<double*>(base + plan->partials_off);
-    a.counters = reinterpret_cast<unsigned*>(base + plan->counters_off);
-    a.span = plan->span;
-    a.n_tensors = plan->n_tensors;
-    a.n_spans = plan->n_spans;
-    a.dtype = plan->grad_dtype;
-    a.reset = flags & ZERO_MULTI_RESET ? 1 : 0;
-    a.st = d_state;
-    const int e = zf::launch_multi_norm(a, stream);
+    const zf::MultiNormLaunch a = norm_launch(plan, d_plan, flags & ZERO_MULTI_RESET ? 1 : 0, d_state);
+    zf::MultiStep none;
+    memset(&none, 0, sizeof none);
+    const int e = zf::launch_multi_norm(a, none, stream);
     if (e) return hip_fail(e, fn);
     return ok();
 }
@@ -719,12 +725,16 @@ int zero_multi_adamw_step(const zero_multi_plan_t* plan, void* d_plan, float* ma
     if (int e = check_plan(fn, plan)) return e;
     if (int e = check_hp(fn, hp)) return e;
     if (!d_plan || !d_state) return fail(ZERO_EINVAL, "%s: NULL plan buffer or state", fn);
-    if (flags & ~ZERO_STEP_FINALIZE) return fail(ZERO_EINVAL, "%s: unknown flags 0x%x", fn, flags);
+    if (flags & ~(ZERO_STEP_FINALIZE | ZERO_MULTI_STATISTICS))
+        return fail(ZERO_EINVAL, "%s: unknown flags 0x%x", fn, flags);
     if (!aligned(d_plan, 256)) return fail(ZERO_EALIGN, "%s: plan buffer not 256-byte aligned", fn);
     if (!aligned(d_state, 8)) return fail(ZERO_EALIGN, "%s: state not 8-byte aligned", fn);
     if (plan->state_bits != 8 && plan->state_bits != 32)
         return fail(ZERO_EINVAL, "%s: the plan only serves the statistics", fn);
     const bool q8 = plan->state_bits == 8;
+    // the 8-bit form's reciprocal of the denominator needs a normal number
+    if (q8 && (float)hp->eps < 1.17549435e-38f)
+        return fail(ZERO_EINVAL, "%s: 8-bit states need eps >= 2^-126", fn);
     if (plan->rows > 0) {
         if (!master || !exp_avg || !exp_avg_sq || (q8 && (!m_scale || !v_scale)))
             return fail(ZERO_EINVAL, "%s: NULL state arena", fn);
@@ -738,7 +748,6 @@ int zero_multi_adamw_step(const zero_multi_plan_t* plan, void* d_plan, float* ma
     memset(&a, 0, sizeof a);
     a.entries = reinterpret_cast<const zf::MultiEntry*>(base);
     a.tile_tensor = reinterpret_cast<const int32_t*>(base + plan->tiles_off);
-    a.counters = reinterpret_cast<unsigned*>(base + plan->counters_off);
     a.p = master;
     a.m = exp_avg;
     a.v = exp_avg_sq;
@@ -748,20 +757,28 @@ int zero_multi_adamw_step(const zero_multi_plan_t* plan, void* d_plan, float* ma
     a.gdtype = plan->grad_dtype;
     a.pdtype = plan->param_dtype;
     a.bits = plan->state_bits;
-    a.flags = flags;
-    a.seed = seed;
     a.b1 = (float)hp->beta1;
     a.c1 = (float)(1.0 - hp->beta1);
     a.b2 = (float)hp->beta2;
     a.c2 = (float)(1.0 - hp->beta2);
     a.eps = (float)hp->eps;
-    a.lr = hp->lr;
-    a.wd = hp->weight_decay;
-    a.beta1 = hp->beta1;
-    a.beta2 = hp->beta2;
-    a.max_norm = hp->max_grad_norm;
-    a.st = d_state;
-    const int e = zf::launch_multi_adamw(a, stream);
+    zf::MultiStep step;
+    memset(&step, 0, sizeof step);
+    step.scalars = reinterpret_cast<zf::MultiScalars*>(base + plan->scalars_off);
+    step.st = d_state;
+    step.lr = hp->lr;
+    step.wd = hp->weight_decay;
+    step.beta1 = hp->beta1;
+    step.beta2 = hp->beta2;
+    step.max_norm = hp->max_grad_norm;
+    step.seed = seed;
+    step.advance = flags & ZERO_STEP_FINALIZE ? 1 : 0;
+    a.scalars = step.scalars;
+    int e = flags & ZERO_MULTI_STATISTICS
+                ? zf::launch_multi_norm(norm_launch(plan, d_plan, 0, d_state), step, stream)
+                : zf::launch_multi_prepare(step, stream);
+    if (e) return hip_fail(e, fn);
+    e = zf::launch_multi_adamw(a, stream);
     if (e) return hip_fail(e, fn);
     return ok();
 }

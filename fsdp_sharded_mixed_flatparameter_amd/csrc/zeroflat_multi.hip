@@ -1,11 +1,11 @@
 // zeroflat_multi.hip -- gfx950 (MI355X, CDNA4, wave64) kernels of the step
 // over a list of tensors:
-//   multi_stats_kernel  sums of squares of the unscaled gradients, one partial
-//                       per span of a tensor
-//   multi_fold_kernel   the partials per tensor and over all, in a fixed order
-//   multi_adamw_kernel  skip/clip prologue, AdamW with 32-bit or 8-bit states,
-//                       16-bit copy
-//   multi_finalize_kernel  loss scaler and counters
+//   multi_stats_kernel  sums of squares of the unscaled gradients, per span of
+//                       a tensor
+//   multi_fold_kernel   those sums per tensor and over all; for a step also its
+//                       scalars, loss scaler and counters (multi_prepare_kernel
+//                       does only that)
+//   multi_adamw_kernel  AdamW with 32-bit or 8-bit states, 16-bit copy
 //
 // Everything here streams HBM once; none of it is a contraction.  The state
 // arenas are rows of 256 elements, so a wave owns whole rows: in a row lane l
@@ -62,31 +62,22 @@ template <int DT>
 __device__ __forceinline__ float cvt16(uint32_t h) {
     return DT == ZERO_F16 ? h2f(h) : b2f(h);
 }
-// to binary16 / bfloat16, to nearest, ties to even, on the bit patterns (the
-// flat step's rounding: no hardware conversion mode is involved)
-__device__ __forceinline__ uint32_t f2h(float x) {
-    const uint32_t u = __float_as_uint(x);
-    const uint32_t sign = (u >> 16) & 0x8000u;
-    const uint32_t a = u & 0x7fffffffu;
-    uint32_t h;
-    if (a >= 0x7f800000u) h = a > 0x7f800000u ? 0x7e00u : 0x7c00u;
-    else if (a >= 0x477ff000u) h = 0x7c00u;                      // 65520 and more
-    else if (a >= 0x38800000u) {                                 // normal binary16
-        const uint32_t m = a - 0x38000000u;
-        h = (m + 0xfffu + ((m >> 13) & 1u)) >> 13;
-    } else {                                                     // quantum 2^-24 = ulp of 0.5
-        h = __float_as_uint(__uint_as_float(a) + 0.5f) - 0x3f000000u;
-    }
-    return sign | h;
-}
-__device__ __forceinline__ uint32_t f2b(float x) {
-    const uint32_t u = __float_as_uint(x);
-    if ((u & 0x7fffffffu) > 0x7f800000u) return ((u >> 16) & 0x8000u) | 0x7fc0u;
-    return (u + 0x7fffu + ((u >> 16) & 1u)) >> 16;
-}
+// To binary16 / bfloat16, to nearest, ties to even.  binary16 by the scalar
+// conversion, one instruction per value (the packed one does not always round
+// to nearest); bfloat16 on the bit patterns.  Rounding on the bit patterns
+// alone, as the flat step does it, is 14 instructions per value for binary16,
+// which the 8-bit form has no time for.
 template <int DT>
 __device__ __forceinline__ uint32_t round16(float x) {
-    return DT == ZERO_F16 ? f2h(x) : f2b(x);
+    if constexpr (DT == ZERO_F16) {
+        uint32_t h;
+        asm("v_cvt_f16_f32 %0, %1" : "=v"(h) : "v"(x));
+        return x != x ? ((h & 0x8000u) | 0x7e00u) : h;   // the quiet NaN
+    } else {
+        const uint32_t u = __float_as_uint(x);
+        if (x != x) return ((u >> 16) & 0x8000u) | 0x7fc0u;
+        return (u + 0x7fffu + ((u >> 16) & 1u)) >> 16;
+    }
 }
 template <int DT>
 __device__ __forceinline__ float load_one(const void* p, int64_t i) {
@@ -112,10 +103,25 @@ __device__ __forceinline__ double wave_sum(double x) {
     for (int off = 32; off > 0; off >>= 1) x += __shfl_xor(x, off, 64);
     return x;
 }
+// The largest of the lanes' values, none of them negative or NaN, as a scalar:
+// DPP shifts within rows of 16 lanes, then the row broadcasts (gfx9-family
+// controls); lane 63 ends with all of it.  Patterns of floats >= 0 are ordered
+// as integers.
 __device__ __forceinline__ float wave_max(float x) {
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) x = fmaxf(x, __shfl_xor(x, off, 64));
-    return x;
+    uint32_t u = __float_as_uint(x);
+#define ZF_MAX_STEP(ctrl, rows)                                                                 \
+    {                                                                                           \
+        const uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)u, ctrl, rows, 0xf, false); \
+        u = u > o ? u : o;                                                                      \
+    }
+    ZF_MAX_STEP(0x111, 0xf)   // row_shr:1
+    ZF_MAX_STEP(0x112, 0xf)   // row_shr:2
+    ZF_MAX_STEP(0x114, 0xf)   // row_shr:4
+    ZF_MAX_STEP(0x118, 0xf)   // row_shr:8
+    ZF_MAX_STEP(0x142, 0xa)   // row_bcast:15
+    ZF_MAX_STEP(0x143, 0xc)   // row_bcast:31
+#undef ZF_MAX_STEP
+    return __uint_as_float(lane_value(u, 63));
 }
 // fixed order; valid in thread 0
 template <int WAVES>
@@ -136,9 +142,15 @@ __device__ __forceinline__ double block_sum(double x) {
 // One block per span: E consecutive elements of one tensor, from the tensor's
 // first 16-byte boundary on (the first span also takes the elements before it,
 // the last one what is left).  Squares and sums in fp64, where the square of
-// an fp32 value is exact; the loss scale is a power of two, so it is applied
-// to the sum, exactly as to every element.
+// an fp32 value is exact.
 constexpr int kStatU = 8;   // 16-byte loads in flight per thread
+// The pass streams with non-temporal loads, except that before an update it
+// leaves the first gradients, up to the size of the memory-side cache, where
+// the update finds them again: the 2.02e8-element bf16 block's step took 957 us
+// with none kept, 944 with 128 MiB, 930 with 256 and 933 with all of it (405
+// MB), the 1.25e9-element fp16 shard's 3613, 3599, 3594 and 3754.  On its own
+// the pass is 16% slower with plain loads (72 against 62 us).
+constexpr int64_t kKeepBytes = (int64_t)256 << 20;
 
 template <int DT>
 __device__ __forceinline__ void add_squares(v4u w, double& s0, double& s1) {
@@ -155,6 +167,33 @@ __device__ __forceinline__ void add_squares(v4u w, double& s0, double& s1) {
             s0 = __builtin_fma(a, a, s0);
             s1 = __builtin_fma(b, b, s1);
         }
+    }
+}
+
+template <int DT, bool KEEP>
+__device__ __forceinline__ void sum_vectors(const char* base, int nvec, double& s0, double& s1) {
+    const int tid = threadIdx.x;
+    auto load = [&](int i) {
+        const char* p = base + 16 * (int64_t)i;
+        return KEEP ? *reinterpret_cast<const v4u*>(p) : ldnt<v4u>(p);
+    };
+    int v = 0;
+    for (; v + kThreads * kStatU <= nvec; v += kThreads * kStatU) {
+        v4u w[kStatU];
+#pragma unroll
+        for (int u = 0; u < kStatU; ++u) w[u] = load(v + u * kThreads + tid);
+#pragma unroll
+        for (int u = 0; u < kStatU; ++u) add_squares<DT>(w[u], s0, s1);
+    }
+    if (v < nvec) {
+        v4u w[kStatU];
+#pragma unroll
+        for (int u = 0; u < kStatU; ++u) {
+            const int i = v + u * kThreads + tid;
+            w[u] = i < nvec ? load(i) : v4u{0u, 0u, 0u, 0u};
+        }
+#pragma unroll
+        for (int u = 0; u < kStatU; ++u) add_squares<DT>(w[u], s0, s1);
     }
 }
 
@@ -179,25 +218,8 @@ __global__ void __launch_bounds__(kThreads) multi_stats_kernel(MultiNormLaunch a
     const int nvec = (int)((hi - lo) / kV);   // a span holds at most 2^31 elements
     const int tid = threadIdx.x;
     double s0 = 0.0, s1 = 0.0;
-    int v = 0;
-    for (; v + kThreads * kStatU <= nvec; v += kThreads * kStatU) {
-        v4u w[kStatU];
-#pragma unroll
-        for (int u = 0; u < kStatU; ++u)
-            w[u] = ldnt<v4u>(base + 16 * (int64_t)(v + u * kThreads + tid));
-#pragma unroll
-        for (int u = 0; u < kStatU; ++u) add_squares<DT>(w[u], s0, s1);
-    }
-    if (v < nvec) {
-        v4u w[kStatU];
-#pragma unroll
-        for (int u = 0; u < kStatU; ++u) {
-            const int i = v + u * kThreads + tid;
-            w[u] = i < nvec ? ldnt<v4u>(base + 16 * (int64_t)i) : v4u{0u, 0u, 0u, 0u};
-        }
-#pragma unroll
-        for (int u = 0; u < kStatU; ++u) add_squares<DT>(w[u], s0, s1);
-    }
+    if (s < a.keep_spans) sum_vectors<DT, true>(base, nvec, s0, s1);
+    else sum_vectors<DT, false>(base, nvec, s0, s1);
     // fewer than kV elements after the last vector, fewer than kV before the first
     const int64_t rest = lo + (int64_t)nvec * kV + tid;
     if (rest < hi) {
@@ -208,87 +230,152 @@ __global__ void __launch_bounds__(kThreads) multi_stats_kernel(MultiNormLaunch a
         const double d = (double)load_one<DT>(g, tid);
         s1 = __builtin_fma(d, d, s1);
     }
-    const double t = block_sum<kWaves>(s0 + s1);
+    const double sum = block_sum<kWaves>(s0 + s1);
     if (tid == 0) {
-        const double inv = 1.0 / (double)a.st->loss_scale;   // a power of two
-        a.partials[s] = t * inv * inv;
+        // the loss scale is a power of two: applied to the sum as exactly as
+        // to every element
+        const double inv = 1.0 / (double)a.st->loss_scale;
+        a.partials[s] = sum * inv * inv;
     }
-}
-
-// Block 0: the total; the others: one wave per tensor.
-constexpr int kFoldThreads = 1024;
-__global__ void __launch_bounds__(kFoldThreads) multi_fold_kernel(MultiNormLaunch a) {
-    const int lane = threadIdx.x & 63;
-    if (blockIdx.x == 0) {
-        double x = 0.0;
-        for (int i = threadIdx.x; i < a.n_spans; i += kFoldThreads) x += a.partials[i];
-        x = block_sum<kFoldThreads / 64>(x);
-        if (threadIdx.x == 0) {
-            const int bad = !isfinite(x);
-            a.st->sumsq = a.reset ? x : a.st->sumsq + x;
-            a.st->overflow = a.reset ? bad : a.st->overflow | bad;
-        }
-        return;
-    }
-    const int k = (int)(blockIdx.x - 1) * (kFoldThreads / 64) + (int)(threadIdx.x >> 6);
-    if (k >= a.n_tensors) return;
-    const int p0 = a.entries[k].span0, np = a.entries[k].n_spans;
-    double x = 0.0;
-    for (int i = lane; i < np; i += 64) x += a.partials[p0 + i];
-    x = wave_sum(x);
-    if (lane == 0) a.tensor_sumsq[k] = x;
 }
 
 // ---------------------------------------------------------------- step scalars
-struct StepScalars {
-    int skip;
-    float coef, inv, bc1, bc2, rs;
-    double rbc1;
-    uint32_t key;
-};
 __device__ __forceinline__ uint32_t mix(uint32_t h) {
     h = (h ^ (h >> 16)) * 0x7FEB352Du;
     h = (h ^ (h >> 15)) * 0x846CA68Bu;
     return h ^ (h >> 16);
 }
-// The decisions of the flat step (skip, clip, unscale, bias corrections with
-// t = step + 1), and the 8-bit form's factors and random key.
-template <int BITS>
-__device__ __forceinline__ StepScalars read_step(const MultiAdamLaunch& a) {
-    const zero_step_state_t* st = a.st;
-    StepScalars s;
-    s.skip = (st->overflow | st->remote_overflow) != 0;
-    const double total = st->sumsq + st->remote_sumsq;
-    s.coef = 1.0f;
-    if (a.max_norm > 0.0) {
-        const double c = a.max_norm / (sqrt(total) + 1e-6);
-        s.coef = (float)(c < 1.0 ? c : 1.0);
+// What the update needs of the step state, formed once per step: skip, clip,
+// unscale and bias corrections with t = step + 1 as the flat step has them, the
+// 8-bit form's factors and the key of its random numbers.  Then, with advance,
+// the loss scaler and the counters move on as after the flat step: the update
+// reads only the record.  One thread; old is the state as the launch found it,
+// with this launch's statistics in it.
+struct StateScalars {
+    double sumsq, remote_sumsq, beta1_pow, beta2_pow;
+    float loss_scale, min_scale;
+    int32_t overflow, remote_overflow, dynamic, window, good_steps, step;
+};
+__device__ __forceinline__ StateScalars read_state(const zero_step_state_t* st) {
+    return {st->sumsq, st->remote_sumsq, st->beta1_pow, st->beta2_pow, st->loss_scale, st->min_scale,
+            st->overflow, st->remote_overflow, st->dynamic, st->window, st->good_steps, st->step};
+}
+__device__ __forceinline__ void prepare(const MultiStep& p, const StateScalars& old) {
+    zero_step_state_t* st = p.st;
+    MultiScalars r;
+    r.skip = (old.overflow | old.remote_overflow) != 0;
+    const double total = old.sumsq + old.remote_sumsq;
+    const double norm = sqrt(total);
+    r.coef = 1.0f;
+    if (p.max_norm > 0.0) {
+        const double c = p.max_norm / (norm + 1e-6);
+        r.coef = (float)(c < 1.0 ? c : 1.0);
     }
-    s.inv = (float)(1.0 / (double)st->loss_scale);
-    const double bc1 = 1.0 - st->beta1_pow * a.beta1, bc2 = 1.0 - st->beta2_pow * a.beta2;
-    s.bc1 = (float)bc1;
-    s.bc2 = (float)bc2;
-    s.rs = 0.0f;
-    s.rbc1 = 1.0;
-    s.key = 0;
-    if constexpr (BITS == 8) {
-        s.rs = (float)(1.0 / sqrt(bc2));
-        s.rbc1 = bc1;
-        s.key = mix((uint32_t)st->step + 1u + a.seed);
+    r.inv = (float)(1.0 / (double)old.loss_scale);
+    r.inv_coef = r.inv * r.coef;
+    const double b1p = old.beta1_pow * p.beta1, b2p = old.beta2_pow * p.beta2;
+    const double bc1 = 1.0 - b1p, bc2 = 1.0 - b2p;
+    r.bc1 = (float)bc1;
+    r.bc2 = (float)bc2;
+    r.rs = (float)(1.0 / sqrt(bc2));
+    r.lr = p.lr;
+    r.lr_bc1 = p.lr / bc1;
+    r.wd = p.wd;
+    r.key = mix((uint32_t)old.step + 1u + p.seed);
+    *p.scalars = r;
+    if (!p.advance) {
+        st->sumsq = old.sumsq;
+        st->overflow = old.overflow;
+        return;
     }
+    st->last_norm = norm;
+    st->last_skipped = r.skip;
+    st->last_coef = r.skip ? 0.0f : r.coef;
+    if (r.skip) {
+        if (old.dynamic) {
+            const float h = old.loss_scale / 2.0f;
+            st->loss_scale = h > old.min_scale ? h : old.min_scale;
+        }
+        st->good_steps = 0;
+    } else {
+        st->step = old.step + 1;
+        st->beta1_pow = b1p;
+        st->beta2_pow = b2p;
+        if (old.dynamic) {
+            const bool grow = old.good_steps + 1 == old.window;
+            if (grow && old.loss_scale < 0x1p127f) st->loss_scale = old.loss_scale * 2.0f;
+            st->good_steps = grow ? 0 : old.good_steps + 1;
+        }
+    }
+    st->sumsq = 0.0;
+    st->overflow = 0;
+}
+
+// Block 0: the total, and with `step` what the update needs of it; the other
+// blocks: a tensor's sum each.  A launch of its own: folding in the block that
+// finishes last instead (stores and a count at device scope) made the small
+// MLP's statistics 8.3 us against 6.0 and the 2.02e8-element block's 70 against
+// 66, and a count per block of the update costs about 12 ns each, one after
+// the other.
+constexpr int kFoldThreads = 512;
+__global__ void __launch_bounds__(kFoldThreads) multi_fold_kernel(MultiNormLaunch a, MultiStep step) {
+    int p0 = 0, np = a.n_spans;
+    // read first: thread 0's chain is the whole launch
+    StateScalars st = {};
+    if (blockIdx.x == 0 && threadIdx.x == 0) st = read_state(a.st);
+    if (blockIdx.x > 0) {
+        p0 = a.entries[blockIdx.x - 1].span0;
+        np = a.entries[blockIdx.x - 1].n_spans;
+    }
+    double x = 0.0;
+    for (int i = threadIdx.x; i < np; i += kFoldThreads * kStatU) {
+        double v[kStatU];
+#pragma unroll
+        for (int u = 0; u < kStatU; ++u) {
+            const int j = i + u * kFoldThreads;
+            v[u] = j < np ? a.partials[p0 + j] : 0.0;
+        }
+#pragma unroll
+        for (int u = 0; u < kStatU; ++u) x += v[u];
+    }
+    x = block_sum<kFoldThreads / 64>(x);
+    if (threadIdx.x != 0) return;
+    if (blockIdx.x > 0) {
+        a.tensor_sumsq[blockIdx.x - 1] = x;
+        return;
+    }
+    const int bad = !isfinite(x);
+    st.sumsq = a.reset ? x : st.sumsq + x;
+    st.overflow = a.reset ? bad : st.overflow | bad;
+    if (step.scalars) {
+        prepare(step, st);
+    } else {
+        a.st->sumsq = st.sumsq;
+        a.st->overflow = st.overflow;
+    }
+}
+__global__ void multi_prepare_kernel(MultiStep step) {
+    if (threadIdx.x == 0) prepare(step, read_state(step.st));
+}
+
+__device__ __forceinline__ MultiScalars load_scalars(const MultiScalars* p) {
+    const ZF_CONST MultiScalars* c = as_const(p);
+    MultiScalars s;
+    s.lr = c->lr; s.lr_bc1 = c->lr_bc1; s.wd = c->wd;
+    s.inv = c->inv; s.coef = c->coef; s.inv_coef = c->inv_coef;
+    s.bc1 = c->bc1; s.bc2 = c->bc2; s.rs = c->rs;
+    s.key = c->key; s.skip = c->skip;
     return s;
 }
 struct TensorScalars {
     float rate, keep;
 };
 template <int BITS>
-__device__ __forceinline__ TensorScalars tensor_scalars(const MultiAdamLaunch& a,
-                                                        const StepScalars& s,
+__device__ __forceinline__ TensorScalars tensor_scalars(const MultiScalars& s,
                                                         const ZF_CONST MultiEntry* e) {
-    const double lr = a.lr * e->lr_mult;
     TensorScalars t;
-    t.keep = (float)(1.0 - lr * (a.wd * e->decay_mult));
-    t.rate = BITS == 8 ? (float)(lr / s.rbc1) : (float)lr;
+    t.keep = (float)(1.0 - s.lr * e->lr_mult * (s.wd * e->decay_mult));
+    t.rate = (float)((BITS == 8 ? s.lr_bc1 : s.lr) * e->lr_mult);
     return t;
 }
 
@@ -297,18 +384,21 @@ constexpr float kMost4 = 448.0f, kMost5 = 57344.0f;
 __device__ __forceinline__ float row_scale(float top, float most_inv) {
     return top > 0.0f ? fmaxf(fminf(top, 0x1.fffffep127f) * most_inv, 0x1p-126f) : 0.0f;
 }
-// four second moments (times 1/scale) as e5m2, rounded with the row's numbers
+// Four second moments (times 1/scale) as e5m2, rounded with the row's numbers.
+// e5m2's exponent is fp32's less 112; the difference, modulo the 6 exponent
+// bits that are kept, is added before the cut.  The largest, 57344, has no bit
+// below the cut, so nothing added carries past it.
 __device__ __forceinline__ uint32_t round_e5m2(const float v[4], float inv, uint32_t key, int lane) {
     const uint32_t h = mix(key + (uint32_t)lane * 0x9E3779B9u);
     uint32_t k = h * 0x2C1B3C6Du;
     k ^= k >> 13;
-    const uint32_t r[4] = {h & 0xffffu, h >> 16, k & 0xffffu, k >> 16};
+    constexpr uint32_t kMask = 0xffffu << 5, kBias = (uint32_t)(64 - 48) << 23;
+    const uint32_t r[4] = {(h << 5) & kMask, (h >> 11) & kMask, (k << 5) & kMask, (k >> 11) & kMask};
     uint32_t out = 0;
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-        const uint32_t y = __float_as_uint(fmaxf(v[c] * inv, 0x1p-14f)) + (r[c] << 5);
-        uint32_t q = (y >> 21) - (112u << 2);     // exponent bias 127 -> 15
-        q = q < 0x7Bu ? q : 0x7Bu;                // not past 57344
+        const float y = __builtin_amdgcn_fmed3f(v[c] * inv, 0x1p-14f, kMost5);
+        const uint32_t q = ((__float_as_uint(y) + r[c] + kBias) >> 21) & 0xffu;
         out |= (v[c] > 0.0f ? q : 0u) << (8 * c);
     }
     return out;
@@ -348,7 +438,7 @@ __device__ __forceinline__ void store_state(const MultiAdamLaunch& a, int64_t i,
 
 // The update of a row's quads, in place; ms / vs: the row's scales (8-bit).
 template <int BITS>
-__device__ __forceinline__ void update_quad(const MultiAdamLaunch& a, const StepScalars& s,
+__device__ __forceinline__ void update_quad(const MultiAdamLaunch& a, const MultiScalars& s,
                                             const TensorScalars& t, const float gv[4],
                                             Quad<BITS>& q, float& ms, float& vs, uint32_t key,
                                             int lane) {
@@ -379,22 +469,24 @@ __device__ __forceinline__ void update_quad(const MultiAdamLaunch& a, const Step
         const v2f v01 = __builtin_amdgcn_cvt_pk_f32_bf8((int)q.v.x, false);
         const v2f v23 = __builtin_amdgcn_cvt_pk_f32_bf8((int)q.v.x, true);
         float m[4] = {m01.x, m01.y, m23.x, m23.y}, v[4] = {v01.x, v01.y, v23.x, v23.y};
+        // one product of the row's scale and the decay, one fused multiply-add
+        const float bm = a.b1 * ms, bv = a.b2 * vs;
         float tm = 0.0f, tv = 0.0f;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-            const float u = gv[c] * s.inv;
-            const float g = u * s.coef;
-            m[c] = a.b1 * (m[c] * ms) + a.c1 * g;
-            v[c] = a.b2 * (v[c] * vs) + a.c2 * (g * g);
-            const float d = sqrtf(v[c]) * s.rs + a.eps;
-            q.p[c] = q.p[c] * t.keep - (t.rate * m[c]) / d;
+            const float g = gv[c] * s.inv_coef;
+            m[c] = __builtin_fmaf(bm, m[c], a.c1 * g);
+            v[c] = __builtin_fmaf(bv, v[c], (a.c2 * g) * g);
+            const float d = __builtin_fmaf(__builtin_amdgcn_sqrtf(v[c]), s.rs, a.eps);
+            q.p[c] = __builtin_fmaf(q.p[c], t.keep, -((t.rate * m[c]) * __builtin_amdgcn_rcpf(d)));
             tm = fmaxf(tm, fabsf(m[c]));
             tv = fmaxf(tv, v[c]);
         }
         ms = row_scale(wave_max(tm), 1.0f / kMost4);
         vs = row_scale(wave_max(tv), 1.0f / kMost5);
-        const float mi = ms > 0.0f ? 1.0f / ms : 0.0f;
-        const float vi = vs > 0.0f ? 1.0f / vs : 0.0f;
+        // scales lie well inside the range where the reciprocal is normal
+        const float mi = ms > 0.0f ? __builtin_amdgcn_rcpf(ms) : 0.0f;
+        const float vi = vs > 0.0f ? __builtin_amdgcn_rcpf(vs) : 0.0f;
         int w = __builtin_amdgcn_cvt_pk_fp8_f32(m[0] * mi, m[1] * mi, 0, false);
         q.m.x = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(m[2] * mi, m[3] * mi, w, true);
         q.v.x = round_e5m2(v, vi, key, lane);
@@ -484,10 +576,11 @@ struct CopyTile {
     }
 };
 
-// A tile of R whole rows: every load is issued before any arithmetic.
+// A tile of R whole rows: every load is issued before any arithmetic, and
+// before the step's scalars are looked at.
 template <int GT, int PT, int BITS, int R>
-__device__ __forceinline__ void tile_full(const MultiAdamLaunch& a, const StepScalars& s,
-                                          const TensorScalars& t, const char* g, uint16_t* lp,
+__device__ __forceinline__ void tile_full(const MultiAdamLaunch& a, const MultiScalars& s,
+                                          const ZF_CONST MultiEntry* e, const char* g, uint16_t* lp,
                                           int64_t row, int lane) {
     GradTile<GT, R> gt;
     Quad<BITS> q[R];
@@ -498,6 +591,8 @@ __device__ __forceinline__ void tile_full(const MultiAdamLaunch& a, const StepSc
     if constexpr (BITS == 8)
         if (lane < 2 * R)
             scales = __float_as_uint(lane < R ? a.ms[row + lane] : a.vs[row + lane - R]);
+    if (s.skip) return;
+    const TensorScalars t = tensor_scalars<BITS>(s, e);
     CopyTile<R> copy(lp);
     uint32_t out = 0;
 #pragma unroll
@@ -532,9 +627,11 @@ __device__ __forceinline__ void tile_full(const MultiAdamLaunch& a, const StepSc
 // A tensor's last tile: its rows one at a time, the last row of n % 256
 // elements; gradient and copy element-wise.
 template <int GT, int PT, int BITS>
-__device__ __forceinline__ void tile_part(const MultiAdamLaunch& a, const StepScalars& s,
-                                          const TensorScalars& t, const char* g, uint16_t* lp,
+__device__ __forceinline__ void tile_part(const MultiAdamLaunch& a, const MultiScalars& s,
+                                          const ZF_CONST MultiEntry* e, const char* g, uint16_t* lp,
                                           int64_t row, int64_t left, int lane) {
+    if (s.skip) return;
+    const TensorScalars t = tensor_scalars<BITS>(s, e);
 #pragma unroll 1
     for (; left > 0; left -= kRow, row += 1, lp += kRow, g += kRow * (GT == ZERO_F32 ? 4 : 2)) {
         Quad<BITS> q;
@@ -565,15 +662,30 @@ __device__ __forceinline__ void tile_part(const MultiAdamLaunch& a, const StepSc
     }
 }
 
+// One wave per tile, in launches of at most kSliceTiles tiles over consecutive
+// ranges, at most kBlocksPerCu blocks per compute unit (a dynamic LDS
+// reservation that the kernel does not use): both keep the addresses in flight
+// in one window of every array.  Whole steps, us, same allocation:
+//                       one launch, full   slices, full   slices, 4 per CU   2 per CU
+//   2.02e8, 32-bit            976               944              929            931
+//   2.02e8, 8-bit             575               565              563            577
+//   1.25e9, 8-bit            3700              3545             3518           3524
+//   3e7, 8-bit                 83                83               82             86
+// Half the slice: 941, 572 and 3546.  Tiles of two rows run within 2% of tiles
+// of four.  A resident grid taking tiles from a counter in the order its blocks
+// ask (the flat step's form for large shards): 8-10% slower here, since a
+// request, about 12 ns one after the other, must not cover more than 100 KB.
+constexpr int kSliceTiles = 131072;
+constexpr unsigned kLdsFourBlocks = 40 * 1024;
 template <int GT, int PT, int BITS>
-__global__ void __launch_bounds__(kThreads) multi_adamw_kernel(MultiAdamLaunch a) {
-    constexpr int R = BITS == 8 ? kMultiRows8 : kMultiRows32;
+__global__ void __launch_bounds__(kThreads) multi_adamw_kernel(MultiAdamLaunch a, int tile0) {
+    constexpr int R = kMultiRows;
     constexpr int kGs = GT == ZERO_F32 ? 4 : 2;
-    const StepScalars s = read_step<BITS>(a);
-    if (s.skip) return;
     const int lane = threadIdx.x & 63;
-    const int tile = (int)blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    const int tile = tile0 + (int)blockIdx.x * kWaves +
+                     __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     if (tile >= a.n_tiles) return;
+    const MultiScalars s = load_scalars(a.scalars);
     const ZF_CONST MultiEntry* e = as_const(a.entries) + as_const(a.tile_tensor)[tile];
     const int64_t row_in = (int64_t)(tile - e->tile0) * R;
     const int64_t at = row_in * kRow;
@@ -581,65 +693,39 @@ __global__ void __launch_bounds__(kThreads) multi_adamw_kernel(MultiAdamLaunch a
     const int64_t row = e->row0 + row_in;
     const char* g = static_cast<const char*>(e->grad) + at * kGs;
     uint16_t* lp = PT == ZERO_NONE ? nullptr : static_cast<uint16_t*>(e->param) + at;
-    const TensorScalars t = tensor_scalars<BITS>(a, s, e);
-    if (left >= R * kRow) tile_full<GT, PT, BITS, R>(a, s, t, g, lp, row, lane);
-    else tile_part<GT, PT, BITS>(a, s, t, g, lp, row, left, lane);
+    if (left >= R * kRow) tile_full<GT, PT, BITS, R>(a, s, e, g, lp, row, lane);
+    else tile_part<GT, PT, BITS>(a, s, e, g, lp, row, left, lane);
 }
 
-// The loss scaler and the counters, as the flat step's (one thread).
-__global__ void multi_finalize_kernel(zero_step_state_t* st, double beta1, double beta2,
-                                      double max_norm) {
-    if (threadIdx.x != 0) return;
-    const double total = st->sumsq + st->remote_sumsq;
-    const int skip = (st->overflow | st->remote_overflow) != 0;
-    float coef = 1.0f;
-    if (max_norm > 0.0) {
-        const double c = max_norm / (sqrt(total) + 1e-6);
-        coef = (float)(c < 1.0 ? c : 1.0);
+template <int GT, int PT, int BITS>
+int launch_update(const MultiAdamLaunch& a, hipStream_t s) {
+    for (int t0 = 0; t0 < a.n_tiles; t0 += kSliceTiles) {
+        const int n = a.n_tiles - t0 < kSliceTiles ? a.n_tiles - t0 : kSliceTiles;
+        hipLaunchKernelGGL((multi_adamw_kernel<GT, PT, BITS>),
+                           dim3((unsigned)((n + kWaves - 1) / kWaves)), dim3(kThreads),
+                           kLdsFourBlocks, s, a, t0);
     }
-    st->last_norm = sqrt(total);
-    st->last_skipped = skip;
-    st->last_coef = skip ? 0.0f : coef;
-    if (skip) {
-        if (st->dynamic) {
-            const float h = st->loss_scale / 2.0f;
-            st->loss_scale = h > st->min_scale ? h : st->min_scale;
-        }
-        st->good_steps = 0;
-    } else {
-        st->step = st->step + 1;
-        st->beta1_pow = st->beta1_pow * beta1;
-        st->beta2_pow = st->beta2_pow * beta2;
-        if (st->dynamic) {
-            st->good_steps = st->good_steps + 1;
-            if (st->good_steps == st->window) {
-                if (st->loss_scale < 0x1p127f) st->loss_scale = st->loss_scale * 2.0f;
-                st->good_steps = 0;
-            }
-        }
-    }
-    st->sumsq = 0.0;
-    st->overflow = 0;
+    return (int)hipGetLastError();
 }
-
 template <int GT, int PT>
-void launch_update(const MultiAdamLaunch& a, unsigned grid, hipStream_t s) {
-    if (a.bits == 8)
-        hipLaunchKernelGGL((multi_adamw_kernel<GT, PT, 8>), dim3(grid), dim3(kThreads), 0, s, a);
-    else
-        hipLaunchKernelGGL((multi_adamw_kernel<GT, PT, 32>), dim3(grid), dim3(kThreads), 0, s, a);
+int launch_update(const MultiAdamLaunch& a, hipStream_t s) {
+    return a.bits == 8 ? launch_update<GT, PT, 8>(a, s) : launch_update<GT, PT, 32>(a, s);
 }
 template <int GT>
-void launch_update(const MultiAdamLaunch& a, unsigned grid, hipStream_t s) {
-    if (a.pdtype == ZERO_F16) launch_update<GT, ZERO_F16>(a, grid, s);
-    else if (a.pdtype == ZERO_BF16) launch_update<GT, ZERO_BF16>(a, grid, s);
-    else launch_update<GT, ZERO_NONE>(a, grid, s);
+int launch_update(const MultiAdamLaunch& a, hipStream_t s) {
+    if (a.pdtype == ZERO_F16) return launch_update<GT, ZERO_F16>(a, s);
+    if (a.pdtype == ZERO_BF16) return launch_update<GT, ZERO_BF16>(a, s);
+    return launch_update<GT, ZERO_NONE>(a, s);
 }
 
 }  // namespace
 
-int launch_multi_norm(const MultiNormLaunch& a, void* stream) {
+int launch_multi_norm(MultiNormLaunch a, const MultiStep& step, void* stream) {
     hipStream_t s = (hipStream_t)stream;
+    if (step.scalars) {
+        const int64_t keep = kKeepBytes / (a.span * (a.dtype == ZERO_F32 ? 4 : 2));
+        a.keep_spans = keep < a.n_spans ? (int32_t)keep : a.n_spans;
+    }
     if (a.n_spans > 0) {
         const dim3 grid((unsigned)a.n_spans), block(kThreads);
         if (a.dtype == ZERO_F32)
@@ -651,28 +737,22 @@ int launch_multi_norm(const MultiNormLaunch& a, void* stream) {
         const int e = (int)hipGetLastError();
         if (e) return e;
     }
-    const unsigned per = kFoldThreads / 64;
-    hipLaunchKernelGGL(multi_fold_kernel, dim3(1 + ((unsigned)a.n_tensors + per - 1) / per),
-                       dim3(kFoldThreads), 0, s, a);
+    hipLaunchKernelGGL(multi_fold_kernel, dim3(1 + (unsigned)a.n_tensors), dim3(kFoldThreads), 0, s,
+                       a, step);
+    return (int)hipGetLastError();
+}
+
+int launch_multi_prepare(const MultiStep& step, void* stream) {
+    hipLaunchKernelGGL(multi_prepare_kernel, dim3(1), dim3(64), 0, (hipStream_t)stream, step);
     return (int)hipGetLastError();
 }
 
 int launch_multi_adamw(const MultiAdamLaunch& a, void* stream) {
     hipStream_t s = (hipStream_t)stream;
-    if (a.n_tiles > 0) {
-        const unsigned grid = ((unsigned)a.n_tiles + kWaves - 1) / kWaves;
-        if (a.gdtype == ZERO_F32) launch_update<ZERO_F32>(a, grid, s);
-        else if (a.gdtype == ZERO_F16) launch_update<ZERO_F16>(a, grid, s);
-        else launch_update<ZERO_BF16>(a, grid, s);
-        const int e = (int)hipGetLastError();
-        if (e) return e;
-    }
-    if (a.flags & ZERO_STEP_FINALIZE) {
-        hipLaunchKernelGGL(multi_finalize_kernel, dim3(1), dim3(64), 0, s, a.st, a.beta1, a.beta2,
-                           a.max_norm);
-        return (int)hipGetLastError();
-    }
-    return 0;
+    if (a.n_tiles == 0) return 0;
+    if (a.gdtype == ZERO_F32) return launch_update<ZERO_F32>(a, s);
+    if (a.gdtype == ZERO_F16) return launch_update<ZERO_F16>(a, s);
+    return launch_update<ZERO_BF16>(a, s);
 }
 
 }  // namespace zf

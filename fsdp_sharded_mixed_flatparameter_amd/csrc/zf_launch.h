@@ -99,28 +99,42 @@ struct MultiEntry {
 static_assert(sizeof(MultiEntry) == 64, "the table's entries are 64 bytes");
 
 // rows of one wave's tile of the update
-constexpr int kMultiRows32 = 4, kMultiRows8 = 8;
-// counters of a plan's image, 32-bit, zero between launches
-constexpr int kMultiCounters = 64;
+constexpr int kMultiRows = 4;
+// a step's scalars, formed once and read by every block of the update
+struct MultiScalars {
+    double lr, lr_bc1, wd;      // lr, lr / (1 - beta1^t), weight decay
+    float inv, coef, inv_coef, bc1, bc2, rs;
+    uint32_t key;
+    int32_t skip;
+};
+
+struct MultiStep {
+    MultiScalars* scalars;      // null: statistics alone
+    zero_step_state_t* st;
+    double lr, wd, beta1, beta2, max_norm;
+    uint32_t seed;
+    int32_t advance;            // 1: the loss scaler and the counters move on
+};
+int launch_multi_prepare(const MultiStep& step, void* stream);
 
 struct MultiNormLaunch {
     const MultiEntry* entries;
     const int32_t* span_tensor;
     double* tensor_sumsq;
     double* partials;
-    unsigned* counters;
     int64_t span;
     int32_t n_tensors, n_spans;
+    int32_t keep_spans;  // the first spans, read again by the update: kept in the caches
     int32_t dtype;
     int32_t reset;
     zero_step_state_t* st;
 };
-int launch_multi_norm(const MultiNormLaunch& a, void* stream);
+// step.scalars set: the fold also prepares the step
+int launch_multi_norm(MultiNormLaunch a, const MultiStep& step, void* stream);
 
 struct MultiAdamLaunch {
     const MultiEntry* entries;
     const int32_t* tile_tensor;
-    unsigned* counters;
     float* p;
     void* m;
     void* v;
@@ -128,10 +142,8 @@ struct MultiAdamLaunch {
     float* vs;
     int32_t n_tiles;
     int32_t gdtype, pdtype, bits;
-    uint32_t flags, seed;
     float b1, c1, b2, c2, eps;
-    double lr, wd, beta1, beta2, max_norm;
-    zero_step_state_t* st;
+    const MultiScalars* scalars;
 };
 int launch_multi_adamw(const MultiAdamLaunch& a, void* stream);
 

@@ -10,7 +10,7 @@ import torch
 
 from . import (_DTYPE_CODES, _FLOATS, ZERO_NONE, ZERO_ROW, StepState, _check, _current_raw_stream,
                _dev, _dtype_name, _lib, zero_adamw_hparams_t, zero_multi_adamw_step,
-               zero_multi_plan_t, zero_multi_unscale_norm)
+               zero_multi_plan_t)
 
 
 def _doubles(x, n, name):
@@ -172,9 +172,6 @@ class TensorListOptimizer:
         """Statistics over the bound gradients, then the step."""
         if stream is None:
             stream = _current_raw_stream()
-        h = self._hparams()
-        if self.statistics:
-            zero_multi_unscale_norm(self.plan, self.state, stream=stream)
-        zero_multi_adamw_step(self.plan, self.master, self.exp_avg, self.exp_avg_sq, h, self.state,
-                              self.exp_avg_scale, self.exp_avg_sq_scale, seed=self.seed,
-                              stream=stream)
+        zero_multi_adamw_step(self.plan, self.master, self.exp_avg, self.exp_avg_sq, self._hparams(),
+                              self.state, self.exp_avg_scale, self.exp_avg_sq_scale, seed=self.seed,
+                              statistics=self.statistics, stream=stream)

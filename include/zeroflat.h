@@ -470,7 +470,7 @@ typedef struct {
     int64_t bind_bytes;  /* its first part, rewritten by zero_multi_bind */
     int64_t sumsq_off;   /* byte offset of the per-tensor sums, double[n_tensors] */
     /* internal: the other parts of the buffer and the launch shapes */
-    int64_t tiles_off, spans_off, partials_off, counters_off;
+    int64_t tiles_off, spans_off, partials_off, scalars_off;
     int64_t span;        /* elements one block of the statistics pass reads */
     int32_t n_tensors, grad_dtype, param_dtype, state_bits;
     int32_t n_tiles, n_spans;
@@ -499,13 +499,16 @@ int zero_multi_bind(const zero_multi_plan_t* plan, const void* const* grads, voi
  * overflow are set instead (statistics outside a step; the scaler and
  * counters are not touched). */
 #define ZERO_MULTI_RESET 2u
+#define ZERO_MULTI_STATISTICS 4u
 int zero_multi_unscale_norm(const zero_multi_plan_t* plan, void* d_plan, uint32_t flags,
                             zero_step_state_t* d_state, void* stream);
 
 /* One AdamW step over the list: skip, clip, update, 16-bit copy and (flags &
  * ZERO_STEP_FINALIZE) the loss-scaler / counter update, as section 3 has them,
  * with the step state's statistics and, per tensor, lr_k = lr * lr_mult[k] and
- * wd_k = weight_decay * decay_mult[k].  Per element, each a separately rounded
+ * wd_k = weight_decay * decay_mult[k].  ZERO_MULTI_STATISTICS takes this list's
+ * statistics first, as zero_multi_unscale_norm does, in a launch less than two
+ * calls need.  Per element, each a separately rounded
  * fp32 operation unless said otherwise:
  *     u = f32(grad) * (1/loss_scale);  g = u * coef
  *     m = b1*m + c1*g;  v = b2*v + c2*(g*g)
@@ -515,7 +518,9 @@ int zero_multi_unscale_norm(const zero_multi_plan_t* plan, void* d_plan, uint32_
  *   per row each; a value is code * scale):
  *     p = p*keep_k - (rate_k * m) / (sqrtf(v) * rs + eps)
  *     rate_k = f32(lr_k / (1 - beta1^t)), rs = f32(1 / sqrt(1 - beta2^t))
- *     (square root and quotient to about 2 units in the last place)
+ *     (products and sums fused where that helps, square root and reciprocals
+ *     to 1 unit in the last place, the root of a second moment below 2^-126
+ *     possibly 0; eps >= 2^-126)
  *   with keep_k = f32(1 - lr_k * wd_k).
  * The 8-bit states are then written back per row: top = min(max|x|, FLT_MAX),
  * scale = max(top * f32(1/most), 2^-126) (0 for a row of zeros), y =

@@ -30,14 +30,14 @@ def make(zf, numels, grad=1, param=2, bits=8, image=True):
     return rc, plan, host
 
 
-@pytest.mark.parametrize("bits,rows_per_tile", [(32, 4), (8, 8)])
+@pytest.mark.parametrize("bits,rows_per_tile", [(32, 4), (8, 4), (0, 0)])
 @pytest.mark.parametrize("numels", [[1], [0], [256, 257, 0, 255], [4096, 1, 5000, 1 << 20], [],
                                     [7] * 900])
 def test_plan_tables(zf, numels, bits, rows_per_tile):
     rc, plan, host = make(zf, numels, bits=bits)
     assert rc == 0
     rows = [-(-n // 256) for n in numels]
-    tiles = [-(-r // rows_per_tile) for r in rows]
+    tiles = [-(-r // rows_per_tile) if bits else 0 for r in rows]
     spans = [-(-n // plan.span) for n in numels]
     assert (plan.total, plan.rows, plan.n_tiles, plan.n_spans) == \
         (sum(numels), sum(rows), sum(tiles), sum(spans))
@@ -47,8 +47,7 @@ def test_plan_tables(zf, numels, bits, rows_per_tile):
     assert np.array_equal(table, np.repeat(np.arange(len(numels)), spans))
     assert plan.sumsq_off + 8 * len(numels) <= plan.image_bytes
     assert plan.bind_bytes == 64 * len(numels)
-    # counters and workspace start at zero
-    assert not host[plan.counters_off:plan.tiles_off].any()
+    assert not host[plan.sumsq_off:plan.image_bytes].any()
 
 
 def test_plan_refusals(zf):
@@ -115,13 +114,14 @@ def test_calls_validate_before_launch(zf):
                                            None if hp is None else C.byref(hp), 0, flags, st, None)
 
         assert step(ref=None) == -1 and step(d=None) == -1 and step(st=None) == -1
-        assert step(hp=None) == -1 and step(flags=4) == -1 and step(flags=2) == -1
+        assert step(hp=None) == -1 and step(flags=8) == -1 and step(flags=2) == -1
         assert step(d=C.c_void_p(0x1010)) == -2 and step(st=C.c_void_p(0x10004)) == -2
         assert step(p=None) == -1 and step(m=None) == -1 and step(v=None) == -1
         assert step(p=C.c_void_p(0x1008)) == -2 and step(m=C.c_void_p(0x1002)) == -2
         if bits == 8:
             assert step(ms=None) == -1 and step(vs=None) == -1
             assert step(vs=C.c_void_p(0x1002)) == -2
+            assert step(hp=zf.zero_adamw_hparams_t(**dict(HP, eps=1e-40))) == -1
         bad = zf.zero_adamw_hparams_t(**dict(HP, beta2=1.0))
         assert step(hp=bad) == -1
         assert b"zero_multi_adamw_step" in L.zero_last_error()
