@@ -70,7 +70,8 @@ class zero_multi_plan_t(C.Structure):
                 ("total", "rows", "image_bytes", "bind_bytes", "sumsq_off", "tiles_off",
                  "spans_off", "partials_off", "scalars_off", "span")] + \
                [(f, C.c_int32) for f in
-                ("n_tensors", "grad_dtype", "param_dtype", "state_bits", "n_tiles", "n_spans")]
+                ("n_tensors", "grad_dtype", "param_dtype", "state_bits", "n_tiles", "n_spans",
+                 "short_tiles", "reserved")]
 
 
 def _load():

@@ -554,6 +554,8 @@ int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
 // elements one block of the statistics pass reads: the smallest power of two
 // from kMinSpan on that leaves at most kMaxSpans full spans
 constexpr int64_t kMinSpan = 4096, kMaxSpans = 4096;
+// bytes from the step's scalars to the copy of the state in a plan's image
+constexpr int64_t kSnapshotAt = 256;
 
 int check_plan(const char* fn, const zero_multi_plan_t* plan) {
     if (!plan) return fail(ZERO_EINVAL, "%s: NULL plan", fn);
@@ -572,6 +574,7 @@ zf::MultiNormLaunch norm_launch(const zero_multi_plan_t* plan, void* d_plan, int
     a.span_tensor = reinterpret_cast<const int32_t*>(base + plan->spans_off);
     a.tensor_sumsq = reinterpret_cast<double*>(base + plan->sumsq_off);
     a.partials = reinterpret_cast<double*>(base + plan->partials_off);
+    a.snapshot = reinterpret_cast<zf::MultiState*>(base + plan->scalars_off + kSnapshotAt);
     a.span = plan->span;
     a.n_tensors = plan->n_tensors;
     a.n_spans = plan->n_spans;
@@ -596,22 +599,24 @@ int zero_multi_plan_init(const int64_t* numels, int32_t n_tensors, int32_t grad_
         return fail(ZERO_EINVAL, "%s: param_dtype must be fp16, bf16 or none", fn);
     if (state_bits != 0 && state_bits != 8 && state_bits != 32)
         return fail(ZERO_EINVAL, "%s: state_bits must be 32, 8 or 0", fn);
-    int64_t total = 0, rows = 0, tiles = 0;
+    int64_t total = 0, rows = 0;
     for (int32_t k = 0; k < n_tensors; ++k) {
         if (numels[k] < 0) return fail(ZERO_EINVAL, "%s: numel[%d] < 0", fn, k);
         // 4-byte elements: byte counts stay far from int64's end
         if (numels[k] > ((int64_t)1 << 56) || !add_ok(total, numels[k], &total) ||
             total > ((int64_t)1 << 56))
             return fail(ZERO_ERANGE, "%s: total overflows", fn);
-        const int64_t r = ceil_div(numels[k], ZERO_ROW);
-        rows += r;
-        tiles += ceil_div(r, zf::kMultiRows);
+        rows += ceil_div(numels[k], ZERO_ROW);
     }
     int64_t span = kMinSpan;
     while (ceil_div(total, span) > kMaxSpans) span *= 2;
     int64_t spans = 0;
     for (int32_t k = 0; k < n_tensors; ++k) spans += ceil_div(numels[k], span);
-    if (state_bits == 0) tiles = 0;
+    const bool is_short = spans <= zf::kMultiShortSpans;
+    const int64_t tile_elems = ZERO_ROW * (is_short ? zf::kMultiRowsShort : zf::kMultiRows);
+    int64_t tiles = 0;
+    if (state_bits)
+        for (int32_t k = 0; k < n_tensors; ++k) tiles += ceil_div(numels[k], tile_elems);
     // tile and row indices are 32-bit in the kernels
     if (tiles > 0x3fffffff || rows > 0x7fffffff)
         return fail(ZERO_ERANGE, "%s: the list is too long", fn);
@@ -631,7 +636,9 @@ int zero_multi_plan_init(const int64_t* numels, int32_t n_tensors, int32_t grad_
     auto part = [&](int64_t bytes) { const int64_t at = off; off = round_up(off + bytes, 256); return at; };
     P.bind_bytes = (int64_t)n_tensors * (int64_t)sizeof(zf::MultiEntry);
     part(P.bind_bytes);
-    P.scalars_off = part(sizeof(zf::MultiScalars));
+    P.short_tiles = is_short ? 1 : 0;
+    static_assert(sizeof(zf::MultiScalars) <= kSnapshotAt, "the scalars precede the snapshot");
+    P.scalars_off = part(kSnapshotAt + (int64_t)sizeof(zf::MultiState));
     P.tiles_off = part(tiles * 4);
     P.spans_off = part(spans * 4);
     P.sumsq_off = part((int64_t)n_tensors * 8);
@@ -650,7 +657,7 @@ int zero_multi_plan_init(const int64_t* numels, int32_t n_tensors, int32_t grad_
         int64_t row = 0, tile = 0, sp = 0;
         for (int32_t k = 0; k < n_tensors; ++k) {
             const int64_t r = ceil_div(numels[k], ZERO_ROW);
-            const int64_t nt = state_bits ? ceil_div(r, zf::kMultiRows) : 0;
+            const int64_t nt = state_bits ? ceil_div(numels[k], tile_elems) : 0;
             const int64_t ns = ceil_div(numels[k], span);
             e[k].numel = numels[k];
             e[k].row0 = row;
@@ -709,10 +716,9 @@ int zero_multi_unscale_norm(const zero_multi_plan_t* plan, void* d_plan, uint32_
     if (!aligned(d_plan, 256)) return fail(ZERO_EALIGN, "%s: plan buffer not 256-byte aligned", fn);
     if (!aligned(d_state, 8)) return fail(ZERO_EALIGN, "%s: state not 8-byte aligned", fn);
     if (flags & ~ZERO_MULTI_RESET) return fail(ZERO_EINVAL, "%s: unknown flags 0x%x", fn, flags);
-    const zf::MultiNormLaunch a = norm_launch(plan, d_plan, flags & ZERO_MULTI_RESET ? 1 : 0, d_state);
-    zf::MultiStep none;
-    memset(&none, 0, sizeof none);
-    const int e = zf::launch_multi_norm(a, none, stream);
+    zf::MultiNormLaunch a = norm_launch(plan, d_plan, flags & ZERO_MULTI_RESET ? 1 : 0, d_state);
+    a.snapshot = nullptr;
+    const int e = zf::launch_multi_norm(a, stream);
     if (e) return hip_fail(e, fn);
     return ok();
 }
@@ -754,6 +760,7 @@ int zero_multi_adamw_step(const zero_multi_plan_t* plan, void* d_plan, float* ma
     a.ms = m_scale;
     a.vs = v_scale;
     a.n_tiles = plan->n_tiles;
+    a.short_tiles = plan->short_tiles;
     a.gdtype = plan->grad_dtype;
     a.pdtype = plan->param_dtype;
     a.bits = plan->state_bits;
@@ -774,11 +781,9 @@ int zero_multi_adamw_step(const zero_multi_plan_t* plan, void* d_plan, float* ma
     step.seed = seed;
     step.advance = flags & ZERO_STEP_FINALIZE ? 1 : 0;
     a.scalars = step.scalars;
-    int e = flags & ZERO_MULTI_STATISTICS
-                ? zf::launch_multi_norm(norm_launch(plan, d_plan, 0, d_state), step, stream)
-                : zf::launch_multi_prepare(step, stream);
-    if (e) return hip_fail(e, fn);
-    e = zf::launch_multi_adamw(a, stream);
+    const bool stats = (flags & ZERO_MULTI_STATISTICS) != 0;
+    const zf::MultiNormLaunch norm = norm_launch(plan, d_plan, 0, d_state);
+    const int e = zf::launch_multi_step(a, stats ? &norm : nullptr, step, stream);
     if (e) return hip_fail(e, fn);
     return ok();
 }

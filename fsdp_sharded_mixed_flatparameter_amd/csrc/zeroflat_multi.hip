@@ -138,6 +138,79 @@ __device__ __forceinline__ double block_sum(double x) {
     return t;
 }
 
+// ---------------------------------------------------------------- step scalars
+__device__ __forceinline__ uint32_t mix(uint32_t h) {
+    h = (h ^ (h >> 16)) * 0x7FEB352Du;
+    h = (h ^ (h >> 15)) * 0x846CA68Bu;
+    return h ^ (h >> 16);
+}
+// The scalars of the step state.
+__device__ __forceinline__ MultiState read_state(const zero_step_state_t* st) {
+    return {st->sumsq, st->remote_sumsq, st->beta1_pow, st->beta2_pow, st->loss_scale, st->min_scale,
+            st->overflow, st->remote_overflow, st->dynamic, st->window, st->good_steps, st->step};
+}
+__device__ __forceinline__ void add_sum(MultiState& st, double sum, int reset) {
+    const int bad = !isfinite(sum);
+    st.sumsq = reset ? sum : st.sumsq + sum;
+    st.overflow = reset ? bad : st.overflow | bad;
+}
+// What the update needs of them: skip, clip, unscale and bias corrections with
+// t = step + 1 as the flat step has them, the 8-bit form's factors and the key
+// of its random numbers.
+__device__ __forceinline__ MultiScalars step_scalars(const MultiStep& p, const MultiState& st) {
+    MultiScalars r;
+    r.skip = (st.overflow | st.remote_overflow) != 0;
+    r.norm = sqrt(st.sumsq + st.remote_sumsq);
+    r.coef = 1.0f;
+    if (p.max_norm > 0.0) {
+        const double c = p.max_norm / (r.norm + 1e-6);
+        r.coef = (float)(c < 1.0 ? c : 1.0);
+    }
+    r.inv = (float)(1.0 / (double)st.loss_scale);
+    r.inv_coef = r.inv * r.coef;
+    const double bc1 = 1.0 - st.beta1_pow * p.beta1, bc2 = 1.0 - st.beta2_pow * p.beta2;
+    r.bc1 = (float)bc1;
+    r.bc2 = (float)bc2;
+    r.rs = (float)(1.0 / sqrt(bc2));
+    r.lr = p.lr;
+    r.lr_bc1 = p.lr / bc1;
+    r.wd = p.wd;
+    r.key = mix((uint32_t)st.step + 1u + p.seed);
+    return r;
+}
+// The state after the step: the loss scaler and the counters as the flat step
+// moves them; without p.advance only the statistics of `old`.  One thread.
+__device__ __forceinline__ void write_state(const MultiStep& p, const MultiState& old,
+                                            const MultiScalars& r) {
+    zero_step_state_t* st = p.st;
+    if (!p.advance) {
+        st->sumsq = old.sumsq;
+        st->overflow = old.overflow;
+        return;
+    }
+    st->last_norm = r.norm;
+    st->last_skipped = r.skip;
+    st->last_coef = r.skip ? 0.0f : r.coef;
+    if (r.skip) {
+        if (old.dynamic) {
+            const float h = old.loss_scale / 2.0f;
+            st->loss_scale = h > old.min_scale ? h : old.min_scale;
+        }
+        st->good_steps = 0;
+    } else {
+        st->step = old.step + 1;
+        st->beta1_pow = old.beta1_pow * p.beta1;
+        st->beta2_pow = old.beta2_pow * p.beta2;
+        if (old.dynamic) {
+            const bool grow = old.good_steps + 1 == old.window;
+            if (grow && old.loss_scale < 0x1p127f) st->loss_scale = old.loss_scale * 2.0f;
+            st->good_steps = grow ? 0 : old.good_steps + 1;
+        }
+    }
+    st->sumsq = 0.0;
+    st->overflow = 0;
+}
+
 // ---------------------------------------------------------------- statistics
 // One block per span: E consecutive elements of one tensor, from the tensor's
 // first 16-byte boundary on (the first span also takes the elements before it,
@@ -236,81 +309,11 @@ __global__ void __launch_bounds__(kThreads) multi_stats_kernel(MultiNormLaunch a
         // to every element
         const double inv = 1.0 / (double)a.st->loss_scale;
         a.partials[s] = sum * inv * inv;
+        if (s == 0 && a.snapshot) *a.snapshot = read_state(a.st);
     }
 }
 
-// ---------------------------------------------------------------- step scalars
-__device__ __forceinline__ uint32_t mix(uint32_t h) {
-    h = (h ^ (h >> 16)) * 0x7FEB352Du;
-    h = (h ^ (h >> 15)) * 0x846CA68Bu;
-    return h ^ (h >> 16);
-}
-// What the update needs of the step state, formed once per step: skip, clip,
-// unscale and bias corrections with t = step + 1 as the flat step has them, the
-// 8-bit form's factors and the key of its random numbers.  Then, with advance,
-// the loss scaler and the counters move on as after the flat step: the update
-// reads only the record.  One thread; old is the state as the launch found it,
-// with this launch's statistics in it.
-struct StateScalars {
-    double sumsq, remote_sumsq, beta1_pow, beta2_pow;
-    float loss_scale, min_scale;
-    int32_t overflow, remote_overflow, dynamic, window, good_steps, step;
-};
-__device__ __forceinline__ StateScalars read_state(const zero_step_state_t* st) {
-    return {st->sumsq, st->remote_sumsq, st->beta1_pow, st->beta2_pow, st->loss_scale, st->min_scale,
-            st->overflow, st->remote_overflow, st->dynamic, st->window, st->good_steps, st->step};
-}
-__device__ __forceinline__ void prepare(const MultiStep& p, const StateScalars& old) {
-    zero_step_state_t* st = p.st;
-    MultiScalars r;
-    r.skip = (old.overflow | old.remote_overflow) != 0;
-    const double total = old.sumsq + old.remote_sumsq;
-    const double norm = sqrt(total);
-    r.coef = 1.0f;
-    if (p.max_norm > 0.0) {
-        const double c = p.max_norm / (norm + 1e-6);
-        r.coef = (float)(c < 1.0 ? c : 1.0);
-    }
-    r.inv = (float)(1.0 / (double)old.loss_scale);
-    r.inv_coef = r.inv * r.coef;
-    const double b1p = old.beta1_pow * p.beta1, b2p = old.beta2_pow * p.beta2;
-    const double bc1 = 1.0 - b1p, bc2 = 1.0 - b2p;
-    r.bc1 = (float)bc1;
-    r.bc2 = (float)bc2;
-    r.rs = (float)(1.0 / sqrt(bc2));
-    r.lr = p.lr;
-    r.lr_bc1 = p.lr / bc1;
-    r.wd = p.wd;
-    r.key = mix((uint32_t)old.step + 1u + p.seed);
-    *p.scalars = r;
-    if (!p.advance) {
-        st->sumsq = old.sumsq;
-        st->overflow = old.overflow;
-        return;
-    }
-    st->last_norm = norm;
-    st->last_skipped = r.skip;
-    st->last_coef = r.skip ? 0.0f : r.coef;
-    if (r.skip) {
-        if (old.dynamic) {
-            const float h = old.loss_scale / 2.0f;
-            st->loss_scale = h > old.min_scale ? h : old.min_scale;
-        }
-        st->good_steps = 0;
-    } else {
-        st->step = old.step + 1;
-        st->beta1_pow = b1p;
-        st->beta2_pow = b2p;
-        if (old.dynamic) {
-            const bool grow = old.good_steps + 1 == old.window;
-            if (grow && old.loss_scale < 0x1p127f) st->loss_scale = old.loss_scale * 2.0f;
-            st->good_steps = grow ? 0 : old.good_steps + 1;
-        }
-    }
-    st->sumsq = 0.0;
-    st->overflow = 0;
-}
-
+// ---------------------------------------------------------------- folds
 // Block 0: the total, and with `step` what the update needs of it; the other
 // blocks: a tensor's sum each.  A launch of its own: folding in the block that
 // finishes last instead (stores and a count at device scope) made the small
@@ -321,7 +324,7 @@ constexpr int kFoldThreads = 512;
 __global__ void __launch_bounds__(kFoldThreads) multi_fold_kernel(MultiNormLaunch a, MultiStep step) {
     int p0 = 0, np = a.n_spans;
     // read first: thread 0's chain is the whole launch
-    StateScalars st = {};
+    MultiState st = {};
     if (blockIdx.x == 0 && threadIdx.x == 0) st = read_state(a.st);
     if (blockIdx.x > 0) {
         p0 = a.entries[blockIdx.x - 1].span0;
@@ -344,28 +347,35 @@ __global__ void __launch_bounds__(kFoldThreads) multi_fold_kernel(MultiNormLaunc
         a.tensor_sumsq[blockIdx.x - 1] = x;
         return;
     }
-    const int bad = !isfinite(x);
-    st.sumsq = a.reset ? x : st.sumsq + x;
-    st.overflow = a.reset ? bad : st.overflow | bad;
+    add_sum(st, x, a.reset);
     if (step.scalars) {
-        prepare(step, st);
+        const MultiScalars r = step_scalars(step, st);
+        *step.scalars = r;
+        write_state(step, st, r);
     } else {
         a.st->sumsq = st.sumsq;
         a.st->overflow = st.overflow;
     }
 }
 __global__ void multi_prepare_kernel(MultiStep step) {
-    if (threadIdx.x == 0) prepare(step, read_state(step.st));
+    if (threadIdx.x != 0) return;
+    const MultiState st = read_state(step.st);
+    const MultiScalars r = step_scalars(step, st);
+    *step.scalars = r;
+    write_state(step, st, r);
 }
 
-__device__ __forceinline__ MultiScalars load_scalars(const MultiScalars* p) {
-    const ZF_CONST MultiScalars* c = as_const(p);
-    MultiScalars s;
-    s.lr = c->lr; s.lr_bc1 = c->lr_bc1; s.wd = c->wd;
-    s.inv = c->inv; s.coef = c->coef; s.inv_coef = c->inv_coef;
-    s.bc1 = c->bc1; s.bc2 = c->bc2; s.rs = c->rs;
-    s.key = c->key; s.skip = c->skip;
-    return s;
+// the record of an earlier launch, by scalar loads
+template <typename T>
+__device__ __forceinline__ T load_record(const T* p) {
+    static_assert(sizeof(T) % 8 == 0, "read in 8-byte pieces");
+    uint64_t w[sizeof(T) / 8];
+#pragma unroll
+    for (int i = 0; i < (int)(sizeof(T) / 8); ++i)
+        w[i] = as_const(reinterpret_cast<const uint64_t*>(p))[i];
+    T t;
+    __builtin_memcpy(&t, w, sizeof t);
+    return t;
 }
 struct TensorScalars {
     float rate, keep;
@@ -576,91 +586,113 @@ struct CopyTile {
     }
 };
 
-// A tile of R whole rows: every load is issued before any arithmetic, and
-// before the step's scalars are looked at.
-template <int GT, int PT, int BITS, int R>
-__device__ __forceinline__ void tile_full(const MultiAdamLaunch& a, const MultiScalars& s,
-                                          const ZF_CONST MultiEntry* e, const char* g, uint16_t* lp,
-                                          int64_t row, int lane) {
-    GradTile<GT, R> gt;
-    Quad<BITS> q[R];
-    gt.load(g, lane);
-#pragma unroll
-    for (int u = 0; u < R; ++u) load_state<BITS>(a, (row + u) * kRow + 4 * lane, q[u]);
-    uint32_t scales = 0;   // lane u: the m scale of row u, lane R + u: its v scale
-    if constexpr (BITS == 8)
-        if (lane < 2 * R)
-            scales = __float_as_uint(lane < R ? a.ms[row + lane] : a.vs[row + lane - R]);
-    if (s.skip) return;
-    const TensorScalars t = tensor_scalars<BITS>(s, e);
-    CopyTile<R> copy(lp);
-    uint32_t out = 0;
-#pragma unroll
-    for (int u = 0; u < R; ++u) {
-        float gv[4];
-        gt.quad(u, gv);
-        float ms = 0.0f, vs = 0.0f;
-        uint32_t key = 0;
-        if constexpr (BITS == 8) {
-            ms = __uint_as_float(lane_value(scales, u));
-            vs = __uint_as_float(lane_value(scales, R + u));
-            key = mix(s.key + (uint32_t)(row + u));
-        }
-        update_quad<BITS>(a, s, t, gv, q[u], ms, vs, key, lane);
-        store_state<BITS>(a, (row + u) * kRow + 4 * lane, q[u]);
-        if constexpr (PT != ZERO_NONE) {
-            uint32_t h[4];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) h[c] = round16<PT>(q[u].p[c]);
-            copy.store(u, h, lane);
-        }
-        if constexpr (BITS == 8) {
-            if (lane == u) out = __float_as_uint(ms);
-            if (lane == R + u) out = __float_as_uint(vs);
-        }
+// Where a tile of R rows lies.
+template <int GT, int R>
+struct Place {
+    const ZF_CONST MultiEntry* e;
+    const char* g;
+    uint16_t* lp;
+    int64_t row, left;   // first arena row, elements from the tile's first on
+    __device__ __forceinline__ Place(const MultiAdamLaunch& a, int tile) {
+        e = as_const(a.entries) + as_const(a.tile_tensor)[tile];
+        const int64_t row_in = (int64_t)(tile - e->tile0) * R;
+        const int64_t at = row_in * kRow;
+        row = e->row0 + row_in;
+        left = e->numel - at;
+        g = static_cast<const char*>(e->grad) + at * (GT == ZERO_F32 ? 4 : 2);
+        lp = static_cast<uint16_t*>(e->param) + at;
     }
-    if constexpr (BITS == 8)
-        if (lane < 2 * R)
-            (lane < R ? a.ms : a.vs - R)[row + lane] = __uint_as_float(out);
-}
+    __device__ __forceinline__ bool whole() const { return left >= R * kRow; }
+};
 
-// A tensor's last tile: its rows one at a time, the last row of n % 256
-// elements; gradient and copy element-wise.
-template <int GT, int PT, int BITS>
-__device__ __forceinline__ void tile_part(const MultiAdamLaunch& a, const MultiScalars& s,
-                                          const ZF_CONST MultiEntry* e, const char* g, uint16_t* lp,
-                                          int64_t row, int64_t left, int lane) {
-    if (s.skip) return;
-    const TensorScalars t = tensor_scalars<BITS>(s, e);
-#pragma unroll 1
-    for (; left > 0; left -= kRow, row += 1, lp += kRow, g += kRow * (GT == ZERO_F32 ? 4 : 2)) {
-        Quad<BITS> q;
-        load_state<BITS>(a, row * kRow + 4 * lane, q);
-        float gv[4];
+// A tile on its way: load() issues every load, update() waits for them.  Rows
+// of the tile are WHOLE, or end after p.left elements (a tensor's last tile):
+// then gradient and copy go element-wise.
+template <int GT, int PT, int BITS, int R, bool WHOLE>
+struct Tile {
+    GradTile<GT, R> gt;
+    uint32_t ge[WHOLE ? 1 : R][4];   // gradient elements as stored
+    Quad<BITS> q[R];
+    uint32_t scales;                 // lane u: the m scale of row u, lane R + u: its v scale
+
+    __device__ __forceinline__ static int rows(const Place<GT, R>& p) {
+        return WHOLE ? R : (int)((p.left + kRow - 1) / kRow);
+    }
+    __device__ __forceinline__ void load(const MultiAdamLaunch& a, const Place<GT, R>& p, int lane) {
+        if constexpr (WHOLE) gt.load(p.g, lane);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) gv[c] = 4 * lane + c < left ? load_one<GT>(g, 4 * lane + c) : 0.0f;
-        float ms = 0.0f, vs = 0.0f;
-        uint32_t key = 0;
-        if constexpr (BITS == 8) {
-            ms = a.ms[row];
-            vs = a.vs[row];
-            key = mix(s.key + (uint32_t)row);
-        }
-        update_quad<BITS>(a, s, t, gv, q, ms, vs, key, lane);
-        store_state<BITS>(a, row * kRow + 4 * lane, q);
-        if constexpr (PT != ZERO_NONE) {
+        for (int u = 0; u < R; ++u) {
+            if (!WHOLE && u * kRow >= p.left) break;
+            load_state<BITS>(a, (p.row + u) * kRow + 4 * lane, q[u]);
+            if constexpr (!WHOLE) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
-                if (4 * lane + c < left) lp[4 * lane + c] = (uint16_t)round16<PT>(q.p[c]);
-        }
-        if constexpr (BITS == 8) {
-            if (lane == 0) {
-                a.ms[row] = ms;
-                a.vs[row] = vs;
+                for (int c = 0; c < 4; ++c) {
+                    const int i = u * kRow + 4 * lane + c;
+                    ge[u][c] = 0;
+                    if (i < p.left) {
+                        if constexpr (GT == ZERO_F32) ge[u][c] = reinterpret_cast<const uint32_t*>(p.g)[i];
+                        else ge[u][c] = reinterpret_cast<const uint16_t*>(p.g)[i];
+                    }
+                }
             }
         }
+        if constexpr (BITS == 8) {
+            const int n = rows(p), r = lane < R ? lane : lane - R;
+            scales = 0;
+            if (r < n) scales = __float_as_uint((lane < R ? a.ms : a.vs)[p.row + r]);
+        }
     }
-}
+    __device__ __forceinline__ void update(const MultiAdamLaunch& a, const MultiScalars& s,
+                                           const Place<GT, R>& p, int lane) {
+        if (s.skip) return;
+        const TensorScalars t = tensor_scalars<BITS>(s, p.e);
+        CopyTile<R> copy(p.lp);
+        uint32_t out = 0;
+#pragma unroll
+        for (int u = 0; u < R; ++u) {
+            if (!WHOLE && u * kRow >= p.left) break;
+            float gv[4];
+            if constexpr (WHOLE) {
+                gt.quad(u, gv);
+            } else {
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    gv[c] = GT == ZERO_F32 ? __uint_as_float(ge[u][c]) : cvt16<GT>(ge[u][c]);
+            }
+            float ms = 0.0f, vs = 0.0f;
+            uint32_t key = 0;
+            if constexpr (BITS == 8) {
+                ms = __uint_as_float(lane_value(scales, u));
+                vs = __uint_as_float(lane_value(scales, R + u));
+                key = mix(s.key + (uint32_t)(p.row + u));
+            }
+            update_quad<BITS>(a, s, t, gv, q[u], ms, vs, key, lane);
+            store_state<BITS>(a, (p.row + u) * kRow + 4 * lane, q[u]);
+            if constexpr (PT != ZERO_NONE) {
+                uint32_t h[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) h[c] = round16<PT>(q[u].p[c]);
+                if constexpr (WHOLE) {
+                    copy.store(u, h, lane);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const int i = u * kRow + 4 * lane + c;
+                        if (i < p.left) p.lp[i] = (uint16_t)h[c];
+                    }
+                }
+            }
+            if constexpr (BITS == 8) {
+                if (lane == u) out = __float_as_uint(ms);
+                if (lane == R + u) out = __float_as_uint(vs);
+            }
+        }
+        if constexpr (BITS == 8) {
+            const int n = rows(p), r = lane < R ? lane : lane - R;
+            if (r < n) (lane < R ? a.ms : a.vs)[p.row + r] = __uint_as_float(out);
+        }
+    }
+};
 
 // One wave per tile, in launches of at most kSliceTiles tiles over consecutive
 // ranges, at most kBlocksPerCu blocks per compute unit (a dynamic LDS
@@ -677,82 +709,155 @@ __device__ __forceinline__ void tile_part(const MultiAdamLaunch& a, const MultiS
 // request, about 12 ns one after the other, must not cover more than 100 KB.
 constexpr int kSliceTiles = 131072;
 constexpr unsigned kLdsFourBlocks = 40 * 1024;
-template <int GT, int PT, int BITS>
+template <int GT, int PT, int BITS, int R>
 __global__ void __launch_bounds__(kThreads) multi_adamw_kernel(MultiAdamLaunch a, int tile0) {
-    constexpr int R = kMultiRows;
-    constexpr int kGs = GT == ZERO_F32 ? 4 : 2;
     const int lane = threadIdx.x & 63;
     const int tile = tile0 + (int)blockIdx.x * kWaves +
                      __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     if (tile >= a.n_tiles) return;
-    const MultiScalars s = load_scalars(a.scalars);
-    const ZF_CONST MultiEntry* e = as_const(a.entries) + as_const(a.tile_tensor)[tile];
-    const int64_t row_in = (int64_t)(tile - e->tile0) * R;
-    const int64_t at = row_in * kRow;
-    const int64_t left = e->numel - at;
-    const int64_t row = e->row0 + row_in;
-    const char* g = static_cast<const char*>(e->grad) + at * kGs;
-    uint16_t* lp = PT == ZERO_NONE ? nullptr : static_cast<uint16_t*>(e->param) + at;
-    if (left >= R * kRow) tile_full<GT, PT, BITS, R>(a, s, e, g, lp, row, lane);
-    else tile_part<GT, PT, BITS>(a, s, e, g, lp, row, left, lane);
+    const MultiScalars s = load_record(a.scalars);
+    const Place<GT, R> p(a, tile);
+    if (p.whole()) {
+        Tile<GT, PT, BITS, R, true> t;
+        t.load(a, p, lane);
+        t.update(a, s, p, lane);
+    } else {
+        Tile<GT, PT, BITS, R, false> t;
+        t.load(a, p, lane);
+        t.update(a, s, p, lane);
+    }
 }
 
+// A short list's update with statistics, the second of two launches: every
+// block folds the spans' sums itself while its tile is on the way, forms the
+// step's scalars, and updates; block 0 then writes the state, which the blocks
+// read from the copy that the statistics pass took.  The tensors' sums are a
+// wave's each.  Saves the fold's launch and its time, 2.8 us of the small MLP's
+// 13.4; every block reads all partial sums, so a list of more than
+// kMultiShortSpans spans takes the fold.
+static_assert(kMultiShortSpans <= 2 * kThreads, "two partial sums per thread");
 template <int GT, int PT, int BITS>
-int launch_update(const MultiAdamLaunch& a, hipStream_t s) {
+__global__ void __launch_bounds__(kThreads) multi_adamw_short_kernel(MultiAdamLaunch a,
+                                                                     MultiNormLaunch n,
+                                                                     MultiStep step) {
+    constexpr int R = kMultiRowsShort;
+    __shared__ double sums[kWaves];
+    const int lane = threadIdx.x & 63;
+    const int w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    const int wave = (int)blockIdx.x * kWaves + w;
+    const int i0 = threadIdx.x, i1 = threadIdx.x + kThreads;
+    double x = i0 < n.n_spans ? n.partials[i0] : 0.0;
+    const double y = i1 < n.n_spans ? n.partials[i1] : 0.0;
+    const bool live = wave < a.n_tiles;
+    const Place<GT, R> p(a, live ? wave : 0);
+    const bool whole = live && p.whole();
+    Tile<GT, PT, BITS, R, true> t;
+    Tile<GT, PT, BITS, R, false> tp;
+    if (whole) t.load(a, p, lane);
+    else if (live) tp.load(a, p, lane);
+    x = wave_sum(x + y);
+    if (lane == 0) sums[w] = x;
+    __syncthreads();
+    double total = 0.0;
+#pragma unroll
+    for (int j = 0; j < kWaves; ++j) total += sums[j];
+    MultiState st = load_record(n.snapshot);
+    add_sum(st, total, 0);
+    const MultiScalars s = step_scalars(step, st);
+    if (whole) t.update(a, s, p, lane);
+    else if (live) tp.update(a, s, p, lane);
+    if (blockIdx.x == 0 && threadIdx.x == 0) write_state(step, st, s);
+    for (int k = wave; k < n.n_tensors; k += (int)gridDim.x * kWaves) {
+        const int p0 = as_const(a.entries)[k].span0, np = as_const(a.entries)[k].n_spans;
+        double z = 0.0;
+        for (int i = lane; i < np; i += 64) z += n.partials[p0 + i];
+        z = wave_sum(z);
+        if (lane == 0) n.tensor_sumsq[k] = z;
+    }
+}
+
+// short_n, short_step: of multi_adamw_short_kernel, or null
+template <int GT, int PT, int BITS>
+int launch_update(const MultiAdamLaunch& a, const MultiNormLaunch* short_n, const MultiStep* short_step,
+                  hipStream_t s) {
+    if (short_n) {
+        hipLaunchKernelGGL((multi_adamw_short_kernel<GT, PT, BITS>),
+                           dim3((unsigned)((a.n_tiles + kWaves - 1) / kWaves)), dim3(kThreads), 0, s,
+                           a, *short_n, *short_step);
+        return (int)hipGetLastError();
+    }
+    if (a.short_tiles) {           // without statistics
+        if (a.n_tiles > 0)
+            hipLaunchKernelGGL((multi_adamw_kernel<GT, PT, BITS, kMultiRowsShort>),
+                               dim3((unsigned)((a.n_tiles + kWaves - 1) / kWaves)), dim3(kThreads), 0,
+                               s, a, 0);
+        return (int)hipGetLastError();
+    }
     for (int t0 = 0; t0 < a.n_tiles; t0 += kSliceTiles) {
         const int n = a.n_tiles - t0 < kSliceTiles ? a.n_tiles - t0 : kSliceTiles;
-        hipLaunchKernelGGL((multi_adamw_kernel<GT, PT, BITS>),
+        hipLaunchKernelGGL((multi_adamw_kernel<GT, PT, BITS, kMultiRows>),
                            dim3((unsigned)((n + kWaves - 1) / kWaves)), dim3(kThreads),
                            kLdsFourBlocks, s, a, t0);
     }
     return (int)hipGetLastError();
 }
 template <int GT, int PT>
-int launch_update(const MultiAdamLaunch& a, hipStream_t s) {
-    return a.bits == 8 ? launch_update<GT, PT, 8>(a, s) : launch_update<GT, PT, 32>(a, s);
+int launch_update(const MultiAdamLaunch& a, const MultiNormLaunch* n, const MultiStep* p, hipStream_t s) {
+    return a.bits == 8 ? launch_update<GT, PT, 8>(a, n, p, s) : launch_update<GT, PT, 32>(a, n, p, s);
 }
 template <int GT>
-int launch_update(const MultiAdamLaunch& a, hipStream_t s) {
-    if (a.pdtype == ZERO_F16) return launch_update<GT, ZERO_F16>(a, s);
-    if (a.pdtype == ZERO_BF16) return launch_update<GT, ZERO_BF16>(a, s);
-    return launch_update<GT, ZERO_NONE>(a, s);
+int launch_update(const MultiAdamLaunch& a, const MultiNormLaunch* n, const MultiStep* p, hipStream_t s) {
+    if (a.pdtype == ZERO_F16) return launch_update<GT, ZERO_F16>(a, n, p, s);
+    if (a.pdtype == ZERO_BF16) return launch_update<GT, ZERO_BF16>(a, n, p, s);
+    return launch_update<GT, ZERO_NONE>(a, n, p, s);
+}
+int launch_update(const MultiAdamLaunch& a, const MultiNormLaunch* n, const MultiStep* p, hipStream_t s) {
+    if (a.gdtype == ZERO_F32) return launch_update<ZERO_F32>(a, n, p, s);
+    if (a.gdtype == ZERO_F16) return launch_update<ZERO_F16>(a, n, p, s);
+    return launch_update<ZERO_BF16>(a, n, p, s);
 }
 
-}  // namespace
-
-int launch_multi_norm(MultiNormLaunch a, const MultiStep& step, void* stream) {
-    hipStream_t s = (hipStream_t)stream;
-    if (step.scalars) {
-        const int64_t keep = kKeepBytes / (a.span * (a.dtype == ZERO_F32 ? 4 : 2));
-        a.keep_spans = keep < a.n_spans ? (int32_t)keep : a.n_spans;
-    }
-    if (a.n_spans > 0) {
-        const dim3 grid((unsigned)a.n_spans), block(kThreads);
-        if (a.dtype == ZERO_F32)
-            hipLaunchKernelGGL((multi_stats_kernel<ZERO_F32>), grid, block, 0, s, a);
-        else if (a.dtype == ZERO_F16)
-            hipLaunchKernelGGL((multi_stats_kernel<ZERO_F16>), grid, block, 0, s, a);
-        else
-            hipLaunchKernelGGL((multi_stats_kernel<ZERO_BF16>), grid, block, 0, s, a);
-        const int e = (int)hipGetLastError();
-        if (e) return e;
-    }
+int launch_stats(const MultiNormLaunch& a, hipStream_t s) {
+    if (a.n_spans == 0) return 0;
+    const dim3 grid((unsigned)a.n_spans), block(kThreads);
+    if (a.dtype == ZERO_F32)
+        hipLaunchKernelGGL((multi_stats_kernel<ZERO_F32>), grid, block, 0, s, a);
+    else if (a.dtype == ZERO_F16)
+        hipLaunchKernelGGL((multi_stats_kernel<ZERO_F16>), grid, block, 0, s, a);
+    else
+        hipLaunchKernelGGL((multi_stats_kernel<ZERO_BF16>), grid, block, 0, s, a);
+    return (int)hipGetLastError();
+}
+int launch_fold(const MultiNormLaunch& a, const MultiStep& step, hipStream_t s) {
     hipLaunchKernelGGL(multi_fold_kernel, dim3(1 + (unsigned)a.n_tensors), dim3(kFoldThreads), 0, s,
                        a, step);
     return (int)hipGetLastError();
 }
 
-int launch_multi_prepare(const MultiStep& step, void* stream) {
-    hipLaunchKernelGGL(multi_prepare_kernel, dim3(1), dim3(64), 0, (hipStream_t)stream, step);
-    return (int)hipGetLastError();
+}  // namespace
+
+int launch_multi_norm(const MultiNormLaunch& a, void* stream) {
+    if (const int e = launch_stats(a, (hipStream_t)stream)) return e;
+    return launch_fold(a, MultiStep{}, (hipStream_t)stream);
 }
 
-int launch_multi_adamw(const MultiAdamLaunch& a, void* stream) {
+int launch_multi_step(const MultiAdamLaunch& a, const MultiNormLaunch* norm, const MultiStep& step,
+                      void* stream) {
     hipStream_t s = (hipStream_t)stream;
-    if (a.n_tiles == 0) return 0;
-    if (a.gdtype == ZERO_F32) return launch_update<ZERO_F32>(a, s);
-    if (a.gdtype == ZERO_F16) return launch_update<ZERO_F16>(a, s);
-    return launch_update<ZERO_BF16>(a, s);
+    if (!norm) {
+        hipLaunchKernelGGL(multi_prepare_kernel, dim3(1), dim3(64), 0, s, step);
+        if (const int e = (int)hipGetLastError()) return e;
+        return launch_update(a, nullptr, nullptr, s);
+    }
+    MultiNormLaunch n = *norm;
+    const int64_t keep = kKeepBytes / (n.span * (n.dtype == ZERO_F32 ? 4 : 2));
+    n.keep_spans = keep < n.n_spans ? (int32_t)keep : n.n_spans;
+    const bool fold_in_update = a.short_tiles && a.n_tiles > 0;
+    if (!fold_in_update) n.snapshot = nullptr;
+    if (const int e = launch_stats(n, s)) return e;
+    if (fold_in_update) return launch_update(a, &n, &step, s);
+    if (const int e = launch_fold(n, step, s)) return e;
+    return launch_update(a, nullptr, nullptr, s);
 }
 
 }  // namespace zf

@@ -98,54 +98,66 @@ struct MultiEntry {
 };
 static_assert(sizeof(MultiEntry) == 64, "the table's entries are 64 bytes");
 
-// rows of one wave's tile of the update
-constexpr int kMultiRows = 4;
-// a step's scalars, formed once and read by every block of the update
+// Rows of one wave's tile of the update: two where the list is short, which
+// halves a wave's chain of arithmetic (the small MLP's 32-bit step 13.5 to 12.5
+// us) and costs up to 3% on long lists.  A list is short up to
+// kMultiShortSpans spans of its statistics.
+constexpr int kMultiRows = 4, kMultiRowsShort = 2;
+constexpr int64_t kMultiShortSpans = 512;
+
+// the scalars of a step state
+struct MultiState {
+    double sumsq, remote_sumsq, beta1_pow, beta2_pow;
+    float loss_scale, min_scale;
+    int32_t overflow, remote_overflow, dynamic, window, good_steps, step;
+};
+// a step's scalars, formed from them
 struct MultiScalars {
-    double lr, lr_bc1, wd;      // lr, lr / (1 - beta1^t), weight decay
+    double lr, lr_bc1, wd, norm;    // lr, lr / (1 - beta1^t), weight decay
     float inv, coef, inv_coef, bc1, bc2, rs;
     uint32_t key;
     int32_t skip;
 };
-
-struct MultiStep {
-    MultiScalars* scalars;      // null: statistics alone
-    zero_step_state_t* st;
-    double lr, wd, beta1, beta2, max_norm;
-    uint32_t seed;
-    int32_t advance;            // 1: the loss scaler and the counters move on
-};
-int launch_multi_prepare(const MultiStep& step, void* stream);
 
 struct MultiNormLaunch {
     const MultiEntry* entries;
     const int32_t* span_tensor;
     double* tensor_sumsq;
     double* partials;
+    MultiState* snapshot;   // null, or where the pass leaves the state's scalars
+    zero_step_state_t* st;
     int64_t span;
     int32_t n_tensors, n_spans;
-    int32_t keep_spans;  // the first spans, read again by the update: kept in the caches
+    int32_t keep_spans;     // the first spans, read again by the update: kept in the caches
     int32_t dtype;
     int32_t reset;
-    zero_step_state_t* st;
 };
-// step.scalars set: the fold also prepares the step
-int launch_multi_norm(MultiNormLaunch a, const MultiStep& step, void* stream);
+int launch_multi_norm(const MultiNormLaunch& a, void* stream);
 
+struct MultiStep {
+    MultiScalars* scalars;      // where the step's scalars go; null: statistics alone
+    zero_step_state_t* st;
+    double lr, wd, beta1, beta2, max_norm;
+    uint32_t seed;
+    int32_t advance;            // 1: the loss scaler and the counters move on
+};
 struct MultiAdamLaunch {
     const MultiEntry* entries;
     const int32_t* tile_tensor;
+    const MultiScalars* scalars;
     float* p;
     void* m;
     void* v;
     float* ms;
     float* vs;
     int32_t n_tiles;
+    int32_t short_tiles;        // 1: tiles of kMultiRowsShort rows
     int32_t gdtype, pdtype, bits;
     float b1, c1, b2, c2, eps;
-    const MultiScalars* scalars;
 };
-int launch_multi_adamw(const MultiAdamLaunch& a, void* stream);
+// norm: null, or the list's statistics, taken first
+int launch_multi_step(const MultiAdamLaunch& a, const MultiNormLaunch* norm, const MultiStep& step,
+                      void* stream);
 
 // ZeRO-Offload (zeroflat_offload.cpp).  The host update over host arrays:
 // *skipped = 1 (and nothing written) when the state says overflow.

@@ -8,9 +8,9 @@ import itertools
 
 import torch
 
-from . import (_DTYPE_CODES, _FLOATS, ZERO_NONE, ZERO_ROW, StepState, _check, _current_raw_stream,
-               _dev, _dtype_name, _lib, zero_adamw_hparams_t, zero_multi_adamw_step,
-               zero_multi_plan_t)
+from . import (_DTYPE_CODES, _FLOATS, ZERO_MULTI_STATISTICS, ZERO_NONE, ZERO_ROW,
+               ZERO_STEP_FINALIZE, StepState, _check, _dev, _dtype_name, _lib, _stream,
+               zero_adamw_hparams_t, zero_multi_plan_t)
 
 
 def _doubles(x, n, name):
@@ -111,7 +111,9 @@ class TensorListOptimizer:
     from row first_row[k] on (views() gives the tensors inside one); the
     constructor copies `masters` into the first.  With state_bits 8, exp_avg is
     e4m3 and exp_avg_sq e5m2, with one scale per row in exp_avg_scale and
-    exp_avg_sq_scale, and `seed` fixes the second moment's random rounding.
+    exp_avg_sq_scale (None otherwise), and `seed` fixes the second moment's
+    random rounding.  The arenas stay where they are: load a state by copying
+    into them.
     bind() names the gradients and the 16-bit parameters that step() reads and
     writes; without a param_dtype the fp32 master is all there is.  With
     statistics=False a step neither clips nor looks for an overflow."""
@@ -134,14 +136,15 @@ class TensorListOptimizer:
         rows = [-(-x // ZERO_ROW) for x in n]
         self.first_row = [0] + list(itertools.accumulate(rows))[:-1]
         size = self.plan.rows * ZERO_ROW
-        self.master = torch.zeros(size, device=dev)
         kinds = (torch.float8_e4m3fn, torch.float8_e5m2) if state_bits == 8 else (torch.float32,) * 2
-        self.exp_avg, self.exp_avg_sq = (
-            torch.zeros(size * k.itemsize, dtype=torch.uint8, device=dev).view(k) for k in kinds)
-        self.exp_avg_scale = self.exp_avg_sq_scale = None
-        if state_bits == 8:
-            self.exp_avg_scale = torch.zeros(self.plan.rows, device=dev)
-            self.exp_avg_sq_scale = torch.zeros(self.plan.rows, device=dev)
+        arenas = [torch.zeros(size, device=dev)]
+        arenas += [torch.zeros(size * k.itemsize, dtype=torch.uint8, device=dev).view(k) for k in kinds]
+        for _ in range(2):
+            arenas.append(torch.zeros(self.plan.rows, device=dev) if state_bits == 8 else None)
+        self._arenas = tuple(arenas)
+        # the call's arguments that never change
+        self._fixed = (self.plan._ref, self.plan._image_ptr) + tuple(
+            None if t is None else C.c_void_p(t.data_ptr()) for t in arenas)
         for v, t in zip(self.views(self.master), masters):
             v.copy_(t.view(-1))
         self.hp = dict(hp)
@@ -149,6 +152,12 @@ class TensorListOptimizer:
         self.lr_mult, self.decay_mult = lr_mult, decay_mult
         self.state = StepState(loss_scale, dynamic, window, min_scale, device=dev)
         self._h = (None, None)   # (hp items, their C struct)
+
+    master = property(lambda self: self._arenas[0])
+    exp_avg = property(lambda self: self._arenas[1])
+    exp_avg_sq = property(lambda self: self._arenas[2])
+    exp_avg_scale = property(lambda self: self._arenas[3])
+    exp_avg_sq_scale = property(lambda self: self._arenas[4])
 
     def views(self, arena):
         """The tensors inside an arena (flat views, without the rows' padding)."""
@@ -160,18 +169,20 @@ class TensorListOptimizer:
         self.plan.bind(grads, params, self.lr_mult, self.decay_mult)
 
     def _hparams(self):
-        """The C hyper-parameter struct, rebuilt only when self.hp changed."""
+        """The C hyper-parameters, rebuilt only when self.hp changed."""
         key = tuple(self.hp.items())
         if self._h[0] != key:
             if not self.statistics and self.hp.get("max_grad_norm", 0.0) > 0.0:
                 raise ValueError("clipping needs the statistics: max_grad_norm must be 0 without them")
-            self._h = (key, zero_adamw_hparams_t(**self.hp))
+            self._h = (key, C.byref(zero_adamw_hparams_t(**self.hp)))
         return self._h[1]
 
     def step(self, stream=None):
-        """Statistics over the bound gradients, then the step."""
-        if stream is None:
-            stream = _current_raw_stream()
-        zero_multi_adamw_step(self.plan, self.master, self.exp_avg, self.exp_avg_sq, self._hparams(),
-                              self.state, self.exp_avg_scale, self.exp_avg_sq_scale, seed=self.seed,
-                              statistics=self.statistics, stream=stream)
+        """Statistics over the bound gradients, then the step (one library call,
+        as zero_multi_adamw_step with the arguments prepared)."""
+        self.plan._require_bound()
+        flags = ZERO_STEP_FINALIZE | (ZERO_MULTI_STATISTICS if self.statistics else 0)
+        rc = _lib.zero_multi_adamw_step(*self._fixed, self._hparams(), self.seed & 0xffffffff, flags,
+                                        self.state.ptr(), _stream(stream))
+        if rc:
+            _check(rc)

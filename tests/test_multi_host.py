@@ -30,12 +30,14 @@ def make(zf, numels, grad=1, param=2, bits=8, image=True):
     return rc, plan, host
 
 
-@pytest.mark.parametrize("bits,rows_per_tile", [(32, 4), (8, 4), (0, 0)])
+@pytest.mark.parametrize("bits", [32, 8, 0])
 @pytest.mark.parametrize("numels", [[1], [0], [256, 257, 0, 255], [4096, 1, 5000, 1 << 20], [],
                                     [7] * 900])
-def test_plan_tables(zf, numels, bits, rows_per_tile):
+def test_plan_tables(zf, numels, bits):
     rc, plan, host = make(zf, numels, bits=bits)
     assert rc == 0
+    rows_per_tile = 2 if plan.short_tiles else 4
+    assert plan.short_tiles == (plan.n_spans <= 512)
     rows = [-(-n // 256) for n in numels]
     tiles = [-(-r // rows_per_tile) if bits else 0 for r in rows]
     spans = [-(-n // plan.span) for n in numels]
