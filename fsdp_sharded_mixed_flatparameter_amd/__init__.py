@@ -498,10 +498,13 @@ def zero_multi_unscale_norm(plan, state, reset=False, stream=None):
     """Statistics over the tensors bound to `plan` (a MultiPlan): the sum of
     squares of each unscaled gradient into plan.tensor_sumsq, their sum and the
     overflow flag into `state` (added to it, or set with `reset`)."""
-    plan._require_bound()
-    _check(_lib.zero_multi_unscale_norm(plan._ref, plan._image_ptr,
-                                        ZERO_MULTI_RESET if reset else 0, _state_ptr(state),
-                                        _stream(stream)))
+    if not plan._bound:
+        plan._require_bound()
+    rc = _lib.zero_multi_unscale_norm(plan._ref, plan._image_ptr, ZERO_MULTI_RESET if reset else 0,
+                                      _state_ptr(state),
+                                      _current_raw_stream() if stream is None else _stream(stream))
+    if rc:
+        _check(rc)
 
 
 def zero_multi_adamw_step(plan, master, exp_avg, exp_avg_sq, hp, state, exp_avg_scale=None,

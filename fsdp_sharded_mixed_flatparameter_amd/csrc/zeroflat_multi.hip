@@ -275,6 +275,8 @@ __global__ void __launch_bounds__(kThreads) multi_stats_kernel(MultiNormLaunch a
     constexpr int kEs = DT == ZERO_F32 ? 4 : 2;
     constexpr int kV = 16 / kEs;   // elements per 16-byte load
     const int s = blockIdx.x;
+    if (s == 0 && threadIdx.x == 0 && a.snapshot) *a.snapshot = read_state(a.st);
+    const double inv = 1.0 / (double)as_const(a.st)->loss_scale;
     const int k = as_const(a.span_tensor)[s];
     const ZF_CONST MultiEntry* e = as_const(a.entries) + k;
     const char* g = static_cast<const char*>(e->grad);
@@ -304,28 +306,37 @@ __global__ void __launch_bounds__(kThreads) multi_stats_kernel(MultiNormLaunch a
         s1 = __builtin_fma(d, d, s1);
     }
     const double sum = block_sum<kWaves>(s0 + s1);
-    if (tid == 0) {
-        // the loss scale is a power of two: applied to the sum as exactly as
-        // to every element
-        const double inv = 1.0 / (double)a.st->loss_scale;
-        a.partials[s] = sum * inv * inv;
-        if (s == 0 && a.snapshot) *a.snapshot = read_state(a.st);
-    }
+    // the loss scale is a power of two: applied to the sum as exactly as to
+    // every element
+    if (tid == 0) a.partials[s] = sum * inv * inv;
 }
 
 // ---------------------------------------------------------------- folds
 // Block 0: the total, and with `step` what the update needs of it; the other
-// blocks: a tensor's sum each.  A launch of its own: folding in the block that
+// blocks: a tensor's sum each, or (per_wave) a tensor's sum per wave.  A launch of its own: folding in the block that
 // finishes last instead (stores and a count at device scope) made the small
 // MLP's statistics 8.3 us against 6.0 and the 2.02e8-element block's 70 against
 // 66, and a count per block of the update costs about 12 ns each, one after
 // the other.
 constexpr int kFoldThreads = 512;
-__global__ void __launch_bounds__(kFoldThreads) multi_fold_kernel(MultiNormLaunch a, MultiStep step) {
+__global__ void __launch_bounds__(kFoldThreads) multi_fold_kernel(MultiNormLaunch a, MultiStep step,
+                                                                  int per_wave) {
     int p0 = 0, np = a.n_spans;
     // read first: thread 0's chain is the whole launch
     MultiState st = {};
     if (blockIdx.x == 0 && threadIdx.x == 0) st = read_state(a.st);
+    if (per_wave && blockIdx.x > 0) {
+        const int k = (int)(blockIdx.x - 1) * (kFoldThreads / 64) +
+                      __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+        if (k >= a.n_tensors) return;
+        p0 = as_const(a.entries)[k].span0;
+        np = as_const(a.entries)[k].n_spans;
+        double x = 0.0;
+        for (int i = threadIdx.x & 63; i < np; i += 64) x += a.partials[p0 + i];
+        x = wave_sum(x);
+        if ((threadIdx.x & 63) == 0) a.tensor_sumsq[k] = x;
+        return;
+    }
     if (blockIdx.x > 0) {
         p0 = a.entries[blockIdx.x - 1].span0;
         np = a.entries[blockIdx.x - 1].n_spans;
@@ -730,26 +741,27 @@ __global__ void __launch_bounds__(kThreads) multi_adamw_kernel(MultiAdamLaunch a
 
 // A short list's update with statistics, the second of two launches: every
 // block folds the spans' sums itself while its tile is on the way, forms the
-// step's scalars, and updates; block 0 then writes the state, which the blocks
-// read from the copy that the statistics pass took.  The tensors' sums are a
-// wave's each.  Saves the fold's launch and its time, 2.8 us of the small MLP's
+// step's scalars, and updates.  The first sum_blocks blocks have no tiles:
+// block 0 writes the state, which the others read from the copy that the
+// statistics pass took, and each of their waves adds one tensor's sums.  Saves the fold's launch and its time, 2.8 us of the small MLP's
 // 13.4; every block reads all partial sums, so a list of more than
 // kMultiShortSpans spans takes the fold.
 static_assert(kMultiShortSpans <= 2 * kThreads, "two partial sums per thread");
 template <int GT, int PT, int BITS>
 __global__ void __launch_bounds__(kThreads) multi_adamw_short_kernel(MultiAdamLaunch a,
                                                                      MultiNormLaunch n,
-                                                                     MultiStep step) {
+                                                                     MultiStep step,
+                                                                     int sum_blocks) {
     constexpr int R = kMultiRowsShort;
     __shared__ double sums[kWaves];
     const int lane = threadIdx.x & 63;
     const int w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-    const int wave = (int)blockIdx.x * kWaves + w;
     const int i0 = threadIdx.x, i1 = threadIdx.x + kThreads;
     double x = i0 < n.n_spans ? n.partials[i0] : 0.0;
     const double y = i1 < n.n_spans ? n.partials[i1] : 0.0;
-    const bool live = wave < a.n_tiles;
-    const Place<GT, R> p(a, live ? wave : 0);
+    const int tile = ((int)blockIdx.x - sum_blocks) * kWaves + w;
+    const bool live = tile >= 0 && tile < a.n_tiles;
+    const Place<GT, R> p(a, live ? tile : 0);
     const bool whole = live && p.whole();
     Tile<GT, PT, BITS, R, true> t;
     Tile<GT, PT, BITS, R, false> tp;
@@ -766,14 +778,15 @@ __global__ void __launch_bounds__(kThreads) multi_adamw_short_kernel(MultiAdamLa
     const MultiScalars s = step_scalars(step, st);
     if (whole) t.update(a, s, p, lane);
     else if (live) tp.update(a, s, p, lane);
+    if (tile >= 0) return;
     if (blockIdx.x == 0 && threadIdx.x == 0) write_state(step, st, s);
-    for (int k = wave; k < n.n_tensors; k += (int)gridDim.x * kWaves) {
-        const int p0 = as_const(a.entries)[k].span0, np = as_const(a.entries)[k].n_spans;
-        double z = 0.0;
-        for (int i = lane; i < np; i += 64) z += n.partials[p0 + i];
-        z = wave_sum(z);
-        if (lane == 0) n.tensor_sumsq[k] = z;
-    }
+    const int k = (int)blockIdx.x * kWaves + w;
+    if (k >= n.n_tensors) return;
+    const int p0 = as_const(a.entries)[k].span0, np = as_const(a.entries)[k].n_spans;
+    double z = 0.0;
+    for (int i = lane; i < np; i += 64) z += n.partials[p0 + i];
+    z = wave_sum(z);
+    if (lane == 0) n.tensor_sumsq[k] = z;
 }
 
 // short_n, short_step: of multi_adamw_short_kernel, or null
@@ -781,9 +794,11 @@ template <int GT, int PT, int BITS>
 int launch_update(const MultiAdamLaunch& a, const MultiNormLaunch* short_n, const MultiStep* short_step,
                   hipStream_t s) {
     if (short_n) {
+        const int sum_blocks = (short_n->n_tensors + kWaves - 1) / kWaves;
+        const int tile_blocks = (a.n_tiles + kWaves - 1) / kWaves;
         hipLaunchKernelGGL((multi_adamw_short_kernel<GT, PT, BITS>),
-                           dim3((unsigned)((a.n_tiles + kWaves - 1) / kWaves)), dim3(kThreads), 0, s,
-                           a, *short_n, *short_step);
+                           dim3((unsigned)(sum_blocks + tile_blocks)), dim3(kThreads), 0, s, a,
+                           *short_n, *short_step, sum_blocks);
         return (int)hipGetLastError();
     }
     if (a.short_tiles) {           // without statistics
@@ -829,8 +844,11 @@ int launch_stats(const MultiNormLaunch& a, hipStream_t s) {
     return (int)hipGetLastError();
 }
 int launch_fold(const MultiNormLaunch& a, const MultiStep& step, hipStream_t s) {
-    hipLaunchKernelGGL(multi_fold_kernel, dim3(1 + (unsigned)a.n_tensors), dim3(kFoldThreads), 0, s,
-                       a, step);
+    // a wave per tensor where the tensors have few spans each on average
+    const int per_wave = a.n_spans <= 64 * (int64_t)a.n_tensors;
+    const unsigned per = per_wave ? kFoldThreads / 64 : 1;
+    hipLaunchKernelGGL(multi_fold_kernel, dim3(1 + ((unsigned)a.n_tensors + per - 1) / per),
+                       dim3(kFoldThreads), 0, s, a, step, per_wave);
     return (int)hipGetLastError();
 }
 

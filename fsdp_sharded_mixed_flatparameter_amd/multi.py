@@ -9,7 +9,7 @@ import itertools
 import torch
 
 from . import (_DTYPE_CODES, _FLOATS, ZERO_MULTI_STATISTICS, ZERO_NONE, ZERO_ROW,
-               ZERO_STEP_FINALIZE, StepState, _check, _dev, _dtype_name, _lib, _stream,
+               ZERO_STEP_FINALIZE, StepState, _check, _current_raw_stream, _dev, _dtype_name, _lib, _stream,
                zero_adamw_hparams_t, zero_multi_plan_t)
 
 
@@ -180,9 +180,11 @@ class TensorListOptimizer:
     def step(self, stream=None):
         """Statistics over the bound gradients, then the step (one library call,
         as zero_multi_adamw_step with the arguments prepared)."""
-        self.plan._require_bound()
+        if not self.plan._bound:
+            self.plan._require_bound()
         flags = ZERO_STEP_FINALIZE | (ZERO_MULTI_STATISTICS if self.statistics else 0)
         rc = _lib.zero_multi_adamw_step(*self._fixed, self._hparams(), self.seed & 0xffffffff, flags,
-                                        self.state.ptr(), _stream(stream))
+                                        self.state.ptr(),
+                                        _current_raw_stream() if stream is None else _stream(stream))
         if rc:
             _check(rc)

@@ -300,6 +300,112 @@ def test_extreme_gradients(zf, bits, value):
             assert torch.all(torch.isfinite(opt.views(opt.exp_avg_sq)[1].float()))
 
 
+def rounding_corners():
+    """fp32 patterns where a 16-bit rounding decides: every binary16 value of
+    the exponents' ends, the midpoints between neighbours and one fp32 step to
+    either side, the borders of overflow and underflow, and what is no number."""
+    h = np.arange(0x7C00, dtype=np.uint16)                 # every finite binary16 >= 0
+    f = h.view(np.float16).astype(np.float32)
+    mid = (f[:-1].astype(np.float64) + f[1:].astype(np.float64)) / 2
+    b = (np.arange(0x0000, 0x7F80, 7, dtype=np.uint32) << 16)    # bfloat16 values and midpoints
+    x = np.concatenate((f, mid.astype(np.float32), b.view(np.float32),
+                        (b + 0x8000).view(np.float32),
+                        np.array([65519.996, 65520.0, 65504.0, 2.0 ** -25, 2.0 ** -24, 2.0 ** -26,
+                                  1e-45, 3.4e38, 0.0, np.inf], np.float32)))
+    bits = np.concatenate([x.view(np.uint32) + d for d in (0, 1)] + [x.view(np.uint32)[1:] - 1])
+    bits = bits[bits <= 0x7F800000]
+    bits = np.concatenate((bits, bits | 0x80000000,
+                           np.array([0x7FC00000, 0xFFC00000, 0x7F800001], np.uint32)))
+    return bits.astype(np.uint32).view(np.float32)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("param", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("shift", [0, 1])
+def test_copies_round_to_nearest(zf, bits, param, shift):
+    """No rate and no decay: the master stays, and its copy is the nearest
+    16-bit value, ties to even (numpy's and torch's casts on the host)."""
+    x = rounding_corners()
+    hp = dict(HP, lr=0.0, weight_decay=0.0, max_grad_norm=0.0)
+    opt = zf.TensorListOptimizer([torch.from_numpy(x).cuda()], hp, state_bits=bits, statistics=False,
+                                 loss_scale=1.0, grad_dtype=torch.float32, param_dtype=param)
+    buf = torch.zeros(len(x) + 4, dtype=param, device="cuda")
+    opt.bind([torch.zeros(len(x), device="cuda")], [buf[shift:shift + len(x)]])
+    opt.step()
+    assert_bitwise(to_host(opt.master[:len(x)])[~np.isnan(x)], x[~np.isnan(x)], "master")
+    got = to_host(buf[shift:shift + len(x)])
+    if param == torch.float16:
+        with np.errstate(over="ignore"):
+            want = x.astype(np.float16).view(np.uint16)
+        quiet = 0x7E00
+    else:
+        want = torch.from_numpy(x).to(torch.bfloat16).view(torch.int16).numpy().view(np.uint16)
+        quiet = 0x7FC0
+    nan = np.isnan(x)
+    assert np.all(got[nan] & 0x7FFF == quiet)
+    assert_bitwise(got[~nan], want[~nan], "copy")
+
+
+def test_first_moment_ties_go_to_even(zf):
+    """beta1 = 0 and a row whose largest gradient is 448: the scale is one, and
+    every value halfway between two e4m3 codes is held as the even one."""
+    assert np.float32(448) * np.float32(1 / 448) == 1
+    code = np.arange(1, 0x7E, dtype=np.uint8)
+    vals = torch.from_numpy(code).view(torch.float8_e4m3fn).float().numpy()   # up to 416
+    mid = ((vals[:-1].astype(np.float64) + vals[1:]) / 2).astype(np.float32)
+    g = np.zeros(512, np.float32)
+    g[0] = g[256] = 448.0
+    g[1:1 + len(mid)] = mid
+    g[257:257 + len(mid)] = -mid
+    hp = dict(HP, beta1=0.0, max_grad_norm=0.0)
+    opt = zf.TensorListOptimizer([torch.zeros(512, device="cuda")], hp, state_bits=8, loss_scale=1.0,
+                                 grad_dtype=torch.float32, param_dtype=None)
+    opt.bind([torch.from_numpy(g).cuda()])
+    opt.step()
+    assert opt.exp_avg_scale.tolist() == [1.0, 1.0]
+    from list_reference import nearest_e4m3
+    assert np.array_equal(f64(opt.exp_avg), nearest_e4m3(g.astype(np.float64)))
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_a_tensor_past_two_to_the_31(zf, bits):
+    """Elements, bytes and rows past 32 bits: the ends and the border of one
+    long tensor behind another, against the same elements on their own."""
+    n = [700, (1 << 31) + 1027]
+    hp = dict(HP, max_grad_norm=0.0)
+    def packed(dtype):
+        t = torch.zeros(n[0] + n[1] + 1, dtype=dtype, device="cuda")
+        return t, [t[1:1 + n[0]], t[1 + n[0]:]]
+    gbuf, grads = packed(torch.bfloat16)
+    cbuf, copies = packed(torch.bfloat16)
+    cuts = [slice(0, 2048), slice((1 << 31) - 2048, (1 << 31) + 512), slice(n[1] - 1027, n[1])]
+    torch.manual_seed(3)
+    for c in cuts:
+        grads[1][c] = torch.randn(c.stop - c.start, device="cuda").to(torch.bfloat16)
+    grads[0].normal_()
+    masters = [torch.zeros(x, device="cuda") for x in n]
+    opt = zf.TensorListOptimizer(masters, hp, state_bits=bits, loss_scale=1.0)
+    del masters
+    opt.bind(grads, copies)
+    opt.step()
+    want = sum(float(grads[1][c].double().square().sum()) for c in (cuts[0], cuts[1], cuts[2])) - \
+        float(grads[1][slice(max(cuts[1].start, cuts[2].start), cuts[1].stop)].double().square().sum())
+    got = opt.plan.tensor_sumsq.tolist()
+    assert abs(got[1] - want) <= 1e-9 * want
+    first = float(grads[0].double().square().sum())
+    assert abs(got[0] - first) <= 1e-9 * first
+    p = opt.views(opt.master)[1]
+    for c in cuts:
+        ref = ListReference([c.stop - c.start], hp)
+        z = np.zeros(ref.row0[-1] * ROW)
+        sc = (np.zeros(ref.row0[-1], np.float32),) * 2 if bits == 8 else ()
+        w = ref.step([f64(grads[1][c])], z, z, z, 1, 1.0, bits, *sc)
+        k = c.stop - c.start
+        assert np.all(np.abs(f64(p[c]) - w["p"][:k]) <= w["p_err"][:k])
+        assert torch.equal(copies[1][c], p[c].to(torch.bfloat16))
+    assert not p[4096:1 << 20].any() and float(cbuf[0]) == 0.0
+
+
 def test_second_moment_rounding_is_unbiased(zf):
     """From one state the rounded second moments of many seeds have its mean:
     256 * 64 elements and 32 seeds; a code's step is at most a quarter of its
