@@ -405,6 +405,13 @@ constexpr float kMost4 = 448.0f, kMost5 = 57344.0f;
 __device__ __forceinline__ float row_scale(float top, float most_inv) {
     return top > 0.0f ? fmaxf(fminf(top, 0x1.fffffep127f) * most_inv, 0x1p-126f) : 0.0f;
 }
+// 1/x to the nearest, for a scale (2^-126 to 2^120, so x and 1/x are normal):
+// one step of Newton's method from the 1-ulp instruction, checked for every
+// mantissa against the IEEE quotient; a quarter of the division's instructions.
+__device__ __forceinline__ float reciprocal(float x) {
+    const float r = __builtin_amdgcn_rcpf(x);
+    return __builtin_fmaf(__builtin_fmaf(-x, r, 1.0f), r, r);
+}
 // Four second moments (times 1/scale) as e5m2, rounded with the row's numbers.
 // e5m2's exponent is fp32's less 112; the difference, modulo the 6 exponent
 // bits that are kept, is added before the cut.  The largest, 57344, has no bit
@@ -490,14 +497,18 @@ __device__ __forceinline__ void update_quad(const MultiAdamLaunch& a, const Mult
         const v2f v01 = __builtin_amdgcn_cvt_pk_f32_bf8((int)q.v.x, false);
         const v2f v23 = __builtin_amdgcn_cvt_pk_f32_bf8((int)q.v.x, true);
         float m[4] = {m01.x, m01.y, m23.x, m23.y}, v[4] = {v01.x, v01.y, v23.x, v23.y};
-        // one product of the row's scale and the decay, one fused multiply-add
-        const float bm = a.b1 * ms, bv = a.b2 * vs;
         float tm = 0.0f, tv = 0.0f;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
+            // the states' operations are rounded one by one, so that they are
+            // the same on any machine: a random rounding that falls the other
+            // way is a whole code off
             const float g = gv[c] * s.inv_coef;
-            m[c] = __builtin_fmaf(bm, m[c], a.c1 * g);
-            v[c] = __builtin_fmaf(bv, v[c], (a.c2 * g) * g);
+            m[c] = a.b1 * (m[c] * ms) + a.c1 * g;
+            v[c] = a.b2 * (v[c] * vs) + a.c2 * (g * g);
+            // the parameter's are not held in 8 bits: fused, and by the root
+            // and the reciprocal instructions (1 unit in the last place each
+            // of a step that is far smaller than the parameter)
             const float d = __builtin_fmaf(__builtin_amdgcn_sqrtf(v[c]), s.rs, a.eps);
             q.p[c] = __builtin_fmaf(q.p[c], t.keep, -((t.rate * m[c]) * __builtin_amdgcn_rcpf(d)));
             tm = fmaxf(tm, fabsf(m[c]));
@@ -505,9 +516,8 @@ __device__ __forceinline__ void update_quad(const MultiAdamLaunch& a, const Mult
         }
         ms = row_scale(wave_max(tm), 1.0f / kMost4);
         vs = row_scale(wave_max(tv), 1.0f / kMost5);
-        // scales lie well inside the range where the reciprocal is normal
-        const float mi = ms > 0.0f ? __builtin_amdgcn_rcpf(ms) : 0.0f;
-        const float vi = vs > 0.0f ? __builtin_amdgcn_rcpf(vs) : 0.0f;
+        const float mi = ms > 0.0f ? reciprocal(ms) : 0.0f;
+        const float vi = vs > 0.0f ? reciprocal(vs) : 0.0f;
         int w = __builtin_amdgcn_cvt_pk_fp8_f32(m[0] * mi, m[1] * mi, 0, false);
         q.m.x = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(m[2] * mi, m[3] * mi, w, true);
         q.v.x = round_e5m2(v, vi, key, lane);

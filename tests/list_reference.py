@@ -137,3 +137,29 @@ class ListReference:
             assert np.all(ok), "%s codes: %d off, first %s" % (
                 name, int(np.sum(~ok)), [(y[i], code[i], lo[i], hi[i]) for i in
                                          [tuple(np.argwhere(~ok)[0])]])
+
+
+def hold_in_fp32(g, m, v, m_scale, v_scale, hp, inv_coef, t, seed):
+    """The 8-bit states after step t by fp32 operations rounded one by one, on
+    arenas of gradients and codes: (m codes, v codes, m scales, v scales)."""
+    f = np.float32
+    R = len(m_scale)
+    g = g.astype(f).reshape(R, ROW) * f(inv_coef)
+    m, v = m.astype(f).reshape(R, ROW), v.astype(f).reshape(R, ROW)
+    m = f(hp["beta1"]) * (m * m_scale[:, None]) + f(1 - hp["beta1"]) * g
+    v = f(hp["beta2"]) * (v * v_scale[:, None]) + f(1 - hp["beta2"]) * (g * g)
+
+    def scaled(x, most):
+        top = np.minimum(np.abs(x).max(1), np.finfo(f).max)
+        sc = np.where(top > 0, np.maximum(top * f(1.0 / most), f(SCALE_MIN)), f(0))
+        inv = np.where(sc > 0, f(1) / np.where(sc > 0, sc, f(1)), f(0))
+        return x * inv[:, None], sc
+    ym, ms = scaled(m, MOST4)
+    yv, vs = scaled(v, MOST5)
+    assert ym.dtype == yv.dtype == ms.dtype == vs.dtype == f
+    y = np.maximum(yv, f(2.0 ** -14)).view(np.uint32).astype(np.int64)
+    code = np.minimum(((y + 32 * random16(R, t, seed).astype(np.int64)) >> 21) - 448, 0x7B)
+    code = np.where(v > 0, code, 0)
+    val = np.ldexp(np.where(code >> 2, 4 + (code & 3), code & 3).astype(np.float64),
+                   np.maximum(code >> 2, 1) - 17)
+    return nearest_e4m3(ym.astype(np.float64)).reshape(-1), val.reshape(-1), ms, vs

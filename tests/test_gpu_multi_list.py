@@ -10,7 +10,7 @@ import pytest
 import torch
 
 from harness import assert_bitwise, to_host
-from list_reference import ROW, ListReference
+from list_reference import ROW, ListReference, hold_in_fp32
 
 pytestmark = pytest.mark.gpu
 
@@ -165,6 +165,26 @@ def test_steps(zf, sizes, layout, dtype, param, bits):
         check_step(opt, ref, grads, before, t, scale, copies, bits)
         if buf is not None:                                # nothing around the copies
             assert float(buf[0]) == 7.0 and torch.all(buf[1 + sum(n):] == 7.0)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("sizes", ["spans", "large"])
+def test_states_in_8_bits_are_fp32_operations_one_by_one(zf, sizes, dtype):
+    """Every code and scale of five steps, bit for bit: a rounding that fell the
+    other way would be a whole code off."""
+    n = SIZES[sizes]
+    opt, ref, _ = make(zf, n, 8, dtype, None, "own", 256.0)
+    for t in range(1, 6):
+        _, grads = lay_out(values(n, 60 + t, 0.3), "packed", dtype)
+        opt.bind(grads)
+        before = snapshot(opt)
+        opt.step()
+        coef = opt.state.read().last_coef
+        want = hold_in_fp32(ref.arena([f64(x) for x in grads]), *before[1:], HP,
+                            np.float32(1 / 256) * np.float32(coef), t, 11)
+        for name, a, b in zip(("exp_avg", "exp_avg_sq", "exp_avg_scale", "exp_avg_sq_scale"),
+                              snapshot(opt)[1:], want):
+            assert np.array_equal(a, b), (t, name, int(np.sum(a != b)))
 
 
 @pytest.mark.parametrize("bits", [32, 8])
