@@ -71,7 +71,7 @@ class zero_multi_plan_t(C.Structure):
                  "spans_off", "partials_off", "scalars_off", "span")] + \
                [(f, C.c_int32) for f in
                 ("n_tensors", "grad_dtype", "param_dtype", "state_bits", "n_tiles", "n_spans",
-                 "short_tiles", "reserved")]
+                 "tile_rows", "reserved")]
 
 
 def _load():

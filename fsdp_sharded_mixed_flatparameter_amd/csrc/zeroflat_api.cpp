@@ -612,8 +612,10 @@ int zero_multi_plan_init(const int64_t* numels, int32_t n_tensors, int32_t grad_
     while (ceil_div(total, span) > kMaxSpans) span *= 2;
     int64_t spans = 0;
     for (int32_t k = 0; k < n_tensors; ++k) spans += ceil_div(numels[k], span);
-    const bool is_short = spans <= zf::kMultiShortSpans;
-    const int64_t tile_elems = ZERO_ROW * (is_short ? zf::kMultiRowsShort : zf::kMultiRows);
+    const int tile_rows = spans > zf::kMultiShortSpans ? zf::kMultiRowsLong
+                          : rows > zf::kMultiTinyRows  ? zf::kMultiRowsShort
+                                                       : zf::kMultiRowsTiny;
+    const int64_t tile_elems = (int64_t)ZERO_ROW * tile_rows;
     int64_t tiles = 0;
     if (state_bits)
         for (int32_t k = 0; k < n_tensors; ++k) tiles += ceil_div(numels[k], tile_elems);
@@ -636,7 +638,7 @@ int zero_multi_plan_init(const int64_t* numels, int32_t n_tensors, int32_t grad_
     auto part = [&](int64_t bytes) { const int64_t at = off; off = round_up(off + bytes, 256); return at; };
     P.bind_bytes = (int64_t)n_tensors * (int64_t)sizeof(zf::MultiEntry);
     part(P.bind_bytes);
-    P.short_tiles = is_short ? 1 : 0;
+    P.tile_rows = tile_rows;
     static_assert(sizeof(zf::MultiScalars) <= kSnapshotAt, "the scalars precede the snapshot");
     P.scalars_off = part(kSnapshotAt + (int64_t)sizeof(zf::MultiState));
     P.tiles_off = part(tiles * 4);
@@ -760,7 +762,7 @@ int zero_multi_adamw_step(const zero_multi_plan_t* plan, void* d_plan, float* ma
     a.ms = m_scale;
     a.vs = v_scale;
     a.n_tiles = plan->n_tiles;
-    a.short_tiles = plan->short_tiles;
+    a.tile_rows = plan->tile_rows;
     a.gdtype = plan->grad_dtype;
     a.pdtype = plan->param_dtype;
     a.bits = plan->state_bits;

@@ -753,22 +753,26 @@ __global__ void __launch_bounds__(kThreads) multi_adamw_kernel(MultiAdamLaunch a
 // block folds the spans' sums itself while its tile is on the way, forms the
 // step's scalars, and updates.  The first sum_blocks blocks have no tiles:
 // block 0 writes the state, which the others read from the copy that the
-// statistics pass took, and each of their waves adds one tensor's sums.  Saves the fold's launch and its time, 2.8 us of the small MLP's
-// 13.4; every block reads all partial sums, so a list of more than
-// kMultiShortSpans spans takes the fold.
-static_assert(kMultiShortSpans <= 2 * kThreads, "two partial sums per thread");
-template <int GT, int PT, int BITS>
+// statistics pass took, and each of their waves adds one tensor's sums.  Saves
+// the fold's launch and its time, 2.8 us of the small MLP's 13.4; every block
+// reads all partial sums, so a list of more than kMultiShortSpans spans takes
+// the fold.
+static_assert(kMultiShortSpans % kThreads == 0, "whole partial sums per thread");
+template <int GT, int PT, int BITS, int R>
 __global__ void __launch_bounds__(kThreads) multi_adamw_short_kernel(MultiAdamLaunch a,
                                                                      MultiNormLaunch n,
                                                                      MultiStep step,
                                                                      int sum_blocks) {
-    constexpr int R = kMultiRowsShort;
     __shared__ double sums[kWaves];
     const int lane = threadIdx.x & 63;
     const int w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-    const int i0 = threadIdx.x, i1 = threadIdx.x + kThreads;
-    double x = i0 < n.n_spans ? n.partials[i0] : 0.0;
-    const double y = i1 < n.n_spans ? n.partials[i1] : 0.0;
+    constexpr int kMine = (int)(kMultiShortSpans / kThreads);   // partial sums per thread
+    double part[kMine];
+#pragma unroll
+    for (int j = 0; j < kMine; ++j) {
+        const int i = threadIdx.x + j * kThreads;
+        part[j] = i < n.n_spans ? n.partials[i] : 0.0;
+    }
     const int tile = ((int)blockIdx.x - sum_blocks) * kWaves + w;
     const bool live = tile >= 0 && tile < a.n_tiles;
     const Place<GT, R> p(a, live ? tile : 0);
@@ -777,7 +781,10 @@ __global__ void __launch_bounds__(kThreads) multi_adamw_short_kernel(MultiAdamLa
     Tile<GT, PT, BITS, R, false> tp;
     if (whole) t.load(a, p, lane);
     else if (live) tp.load(a, p, lane);
-    x = wave_sum(x + y);
+    double x = part[0];
+#pragma unroll
+    for (int j = 1; j < kMine; ++j) x += part[j];
+    x = wave_sum(x);
     if (lane == 0) sums[w] = x;
     __syncthreads();
     double total = 0.0;
@@ -799,29 +806,34 @@ __global__ void __launch_bounds__(kThreads) multi_adamw_short_kernel(MultiAdamLa
     if (lane == 0) n.tensor_sumsq[k] = z;
 }
 
-// short_n, short_step: of multi_adamw_short_kernel, or null
+// n, step: for multi_adamw_short_kernel, or null
+template <int GT, int PT, int BITS, int R>
+int launch_short(const MultiAdamLaunch& a, const MultiNormLaunch* n, const MultiStep* step,
+                 hipStream_t s) {
+    const int tile_blocks = (a.n_tiles + kWaves - 1) / kWaves;
+    if (n) {
+        const int sum_blocks = (n->n_tensors + kWaves - 1) / kWaves;
+        hipLaunchKernelGGL((multi_adamw_short_kernel<GT, PT, BITS, R>),
+                           dim3((unsigned)(sum_blocks + tile_blocks)), dim3(kThreads), 0, s, a, *n,
+                           *step, sum_blocks);
+    } else {
+        hipLaunchKernelGGL((multi_adamw_kernel<GT, PT, BITS, R>), dim3((unsigned)tile_blocks),
+                           dim3(kThreads), 0, s, a, 0);
+    }
+    return (int)hipGetLastError();
+}
 template <int GT, int PT, int BITS>
-int launch_update(const MultiAdamLaunch& a, const MultiNormLaunch* short_n, const MultiStep* short_step,
+int launch_update(const MultiAdamLaunch& a, const MultiNormLaunch* n, const MultiStep* step,
                   hipStream_t s) {
-    if (short_n) {
-        const int sum_blocks = (short_n->n_tensors + kWaves - 1) / kWaves;
-        const int tile_blocks = (a.n_tiles + kWaves - 1) / kWaves;
-        hipLaunchKernelGGL((multi_adamw_short_kernel<GT, PT, BITS>),
-                           dim3((unsigned)(sum_blocks + tile_blocks)), dim3(kThreads), 0, s, a,
-                           *short_n, *short_step, sum_blocks);
-        return (int)hipGetLastError();
-    }
-    if (a.short_tiles) {           // without statistics
-        if (a.n_tiles > 0)
-            hipLaunchKernelGGL((multi_adamw_kernel<GT, PT, BITS, kMultiRowsShort>),
-                               dim3((unsigned)((a.n_tiles + kWaves - 1) / kWaves)), dim3(kThreads), 0,
-                               s, a, 0);
-        return (int)hipGetLastError();
-    }
+    if (a.n_tiles == 0) return 0;
+    if (a.tile_rows == kMultiRowsTiny)
+        return launch_short<GT, PT, BITS, kMultiRowsTiny>(a, n, step, s);
+    if (a.tile_rows == kMultiRowsShort)
+        return launch_short<GT, PT, BITS, kMultiRowsShort>(a, n, step, s);
     for (int t0 = 0; t0 < a.n_tiles; t0 += kSliceTiles) {
-        const int n = a.n_tiles - t0 < kSliceTiles ? a.n_tiles - t0 : kSliceTiles;
-        hipLaunchKernelGGL((multi_adamw_kernel<GT, PT, BITS, kMultiRows>),
-                           dim3((unsigned)((n + kWaves - 1) / kWaves)), dim3(kThreads),
+        const int tiles = a.n_tiles - t0 < kSliceTiles ? a.n_tiles - t0 : kSliceTiles;
+        hipLaunchKernelGGL((multi_adamw_kernel<GT, PT, BITS, kMultiRowsLong>),
+                           dim3((unsigned)((tiles + kWaves - 1) / kWaves)), dim3(kThreads),
                            kLdsFourBlocks, s, a, t0);
     }
     return (int)hipGetLastError();
@@ -880,7 +892,7 @@ int launch_multi_step(const MultiAdamLaunch& a, const MultiNormLaunch* norm, con
     MultiNormLaunch n = *norm;
     const int64_t keep = kKeepBytes / (n.span * (n.dtype == ZERO_F32 ? 4 : 2));
     n.keep_spans = keep < n.n_spans ? (int32_t)keep : n.n_spans;
-    const bool fold_in_update = a.short_tiles && a.n_tiles > 0;
+    const bool fold_in_update = a.tile_rows != kMultiRowsLong && a.n_tiles > 0;
     if (!fold_in_update) n.snapshot = nullptr;
     if (const int e = launch_stats(n, s)) return e;
     if (fold_in_update) return launch_update(a, &n, &step, s);

@@ -98,12 +98,18 @@ struct MultiEntry {
 };
 static_assert(sizeof(MultiEntry) == 64, "the table's entries are 64 bytes");
 
-// Rows of one wave's tile of the update: two where the list is short, which
-// halves a wave's chain of arithmetic (the small MLP's 32-bit step 13.5 to 12.5
-// us) and costs up to 3% on long lists.  A list is short up to
-// kMultiShortSpans spans of its statistics.
-constexpr int kMultiRows = 4, kMultiRowsShort = 2;
-constexpr int64_t kMultiShortSpans = 512;
+// A list is short up to kMultiShortSpans spans of its statistics: its update
+// folds them itself, which takes a launch less.  Whole steps with the limit at
+// 512, 1024 and 2048 spans, us: 10 tensors of 8e6 elements in all, 32-bit
+// states 52, 52, 48, 8-bit 35, 35, 33; 700 of 4e6 34, 34, 28 and 23, 23, 22.
+constexpr int64_t kMultiShortSpans = 2048;
+// Rows of one wave's tile of the update.  Fewer rows shorten a wave's chain of
+// loads and arithmetic; more keep more bytes in flight per wave.  1, 2 and 4
+// rows, us: 20,000 elements 7.5, 8.1, 9.2 (32-bit states) and 7.4, 7.9, 8.7
+// (8-bit); 1.05e6 10.3, 10.7, 11.8 and 9.7, 9.5, 10.4; 4e6 25.9, 26.1, 29.2
+// and 22.3, 20.0, 20.6; 3e7 144, 139, 139 and 88, 81, 82.
+constexpr int kMultiRowsLong = 4, kMultiRowsShort = 2, kMultiRowsTiny = 1;
+constexpr int64_t kMultiTinyRows = 2048;   // a short list of at most so many rows is tiny
 
 // the scalars of a step state
 struct MultiState {
@@ -151,7 +157,7 @@ struct MultiAdamLaunch {
     float* ms;
     float* vs;
     int32_t n_tiles;
-    int32_t short_tiles;        // 1: tiles of kMultiRowsShort rows
+    int32_t tile_rows;          // kMultiRowsLong, -Short or -Tiny
     int32_t gdtype, pdtype, bits;
     float b1, c1, b2, c2, eps;
 };

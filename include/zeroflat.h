@@ -473,7 +473,7 @@ typedef struct {
     int64_t tiles_off, spans_off, partials_off, scalars_off;
     int64_t span;        /* elements one block of the statistics pass reads */
     int32_t n_tensors, grad_dtype, param_dtype, state_bits;
-    int32_t n_tiles, n_spans, short_tiles, reserved;
+    int32_t n_tiles, n_spans, tile_rows, reserved;
 } zero_multi_plan_t;
 
 /* numels: HOST int64[n_tensors], each >= 0, 0 <= n_tensors <=

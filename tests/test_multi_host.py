@@ -31,15 +31,14 @@ def make(zf, numels, grad=1, param=2, bits=8, image=True):
 
 
 @pytest.mark.parametrize("bits", [32, 8, 0])
-@pytest.mark.parametrize("numels", [[1], [0], [256, 257, 0, 255], [4096, 1, 5000, 1 << 20], [],
+@pytest.mark.parametrize("numels", [[1], [0], [256, 257, 0, 255], [4096, 1, 5000, 1 << 20], [], [9_000_001, 3],
                                     [7] * 900])
 def test_plan_tables(zf, numels, bits):
     rc, plan, host = make(zf, numels, bits=bits)
     assert rc == 0
-    rows_per_tile = 2 if plan.short_tiles else 4
-    assert plan.short_tiles == (plan.n_spans <= 512)
+    assert plan.tile_rows == (4 if plan.n_spans > 2048 else 2 if plan.rows > 2048 else 1)
     rows = [-(-n // 256) for n in numels]
-    tiles = [-(-r // rows_per_tile) if bits else 0 for r in rows]
+    tiles = [-(-r // plan.tile_rows) if bits else 0 for r in rows]
     spans = [-(-n // plan.span) for n in numels]
     assert (plan.total, plan.rows, plan.n_tiles, plan.n_spans) == \
         (sum(numels), sum(rows), sum(tiles), sum(spans))
