@@ -573,18 +573,24 @@ struct GradTile {
 // A full tile's 16-bit parameters at any element offset: whole aligned words,
 // each joined from a lane's values and the top of the lane below; the words
 // shared with the tiles before and after are written element by element.
-template <int R>
+// KEEP: by plain stores, which leave the copy in the memory-side cache for the
+// forward pass that reads it.
+template <int R, bool KEEP>
 struct CopyTile {
     uint16_t* lp;
     int ms;
     uint32_t carry_lo, carry_hi;
     __device__ __forceinline__ explicit CopyTile(uint16_t* at)
         : lp(at), ms((int)((uintptr_t)at >> 1) & 3), carry_lo(0), carry_hi(0) {}
+    __device__ __forceinline__ static void put(uint16_t* p, v2u x) {
+        if constexpr (KEEP) *reinterpret_cast<v2u*>(p) = x;
+        else stnt<v2u>(p, x);
+    }
     __device__ __forceinline__ void store(int u, const uint32_t h[4], int lane) {
         const int e = u * kRow + 4 * lane;
         const uint32_t lo = h[0] | h[1] << 16, hi = h[2] | h[3] << 16;
         if (ms == 0) {
-            stnt<v2u>(lp + e, v2u{lo, hi});
+            put(lp + e, v2u{lo, hi});
             return;
         }
         const uint32_t blo = from_below(lo, carry_lo), bhi = from_below(hi, carry_hi);
@@ -597,7 +603,7 @@ struct CopyTile {
             for (int c = 0; c < 4; ++c)
                 if (c < 4 - ms) lp[c] = (uint16_t)h[c];
         } else {
-            stnt<v2u>(lp + e - ms, v2u{(uint32_t)x, (uint32_t)(x >> 32)});
+            put(lp + e - ms, v2u{(uint32_t)x, (uint32_t)(x >> 32)});
         }
         if (u == R - 1 && lane == 63) {
 #pragma unroll
@@ -629,7 +635,7 @@ struct Place {
 // A tile on its way: load() issues every load, update() waits for them.  Rows
 // of the tile are WHOLE, or end after p.left elements (a tensor's last tile):
 // then gradient and copy go element-wise.
-template <int GT, int PT, int BITS, int R, bool WHOLE>
+template <int GT, int PT, int BITS, int R, bool WHOLE, bool KEEP>
 struct Tile {
     GradTile<GT, R> gt;
     uint32_t ge[WHOLE ? 1 : R][4];   // gradient elements as stored
@@ -667,7 +673,7 @@ struct Tile {
                                            const Place<GT, R>& p, int lane) {
         if (s.skip) return;
         const TensorScalars t = tensor_scalars<BITS>(s, p.e);
-        CopyTile<R> copy(p.lp);
+        CopyTile<R, KEEP> copy(p.lp);
         uint32_t out = 0;
 #pragma unroll
         for (int u = 0; u < R; ++u) {
@@ -729,8 +735,14 @@ struct Tile {
 // ask (the flat step's form for large shards): 8-10% slower here, since a
 // request, about 12 ns one after the other, must not cover more than 100 KB.
 constexpr int kSliceTiles = 131072;
+// A copy of at most this size is left in the memory-side cache (KEEP).  Steps
+// without and with, us: 3e7 elements 151 and 138 (32-bit states), 87 and 79
+// (8-bit); 1e8 503 and 445, 280 and 243; with statistics, whose kept gradients
+// compete for the cache, 518 and 486, 294 and 289, but 1.3e8 674 and 655, 379
+// and 386, and 2.02e8 1000 and 1034, 572 and 624.
+constexpr int64_t kKeepCopyBytes = (int64_t)192 << 20;
 constexpr unsigned kLdsFourBlocks = 40 * 1024;
-template <int GT, int PT, int BITS, int R>
+template <int GT, int PT, int BITS, int R, bool KEEP>
 __global__ void __launch_bounds__(kThreads) multi_adamw_kernel(MultiAdamLaunch a, int tile0) {
     const int lane = threadIdx.x & 63;
     const int tile = tile0 + (int)blockIdx.x * kWaves +
@@ -739,11 +751,11 @@ __global__ void __launch_bounds__(kThreads) multi_adamw_kernel(MultiAdamLaunch a
     const MultiScalars s = load_record(a.scalars);
     const Place<GT, R> p(a, tile);
     if (p.whole()) {
-        Tile<GT, PT, BITS, R, true> t;
+        Tile<GT, PT, BITS, R, true, KEEP> t;
         t.load(a, p, lane);
         t.update(a, s, p, lane);
     } else {
-        Tile<GT, PT, BITS, R, false> t;
+        Tile<GT, PT, BITS, R, false, KEEP> t;
         t.load(a, p, lane);
         t.update(a, s, p, lane);
     }
@@ -777,8 +789,8 @@ __global__ void __launch_bounds__(kThreads) multi_adamw_short_kernel(MultiAdamLa
     const bool live = tile >= 0 && tile < a.n_tiles;
     const Place<GT, R> p(a, live ? tile : 0);
     const bool whole = live && p.whole();
-    Tile<GT, PT, BITS, R, true> t;
-    Tile<GT, PT, BITS, R, false> tp;
+    Tile<GT, PT, BITS, R, true, true> t;
+    Tile<GT, PT, BITS, R, false, true> tp;
     if (whole) t.load(a, p, lane);
     else if (live) tp.load(a, p, lane);
     double x = part[0];
@@ -817,8 +829,18 @@ int launch_short(const MultiAdamLaunch& a, const MultiNormLaunch* n, const Multi
                            dim3((unsigned)(sum_blocks + tile_blocks)), dim3(kThreads), 0, s, a, *n,
                            *step, sum_blocks);
     } else {
-        hipLaunchKernelGGL((multi_adamw_kernel<GT, PT, BITS, R>), dim3((unsigned)tile_blocks),
+        hipLaunchKernelGGL((multi_adamw_kernel<GT, PT, BITS, R, true>), dim3((unsigned)tile_blocks),
                            dim3(kThreads), 0, s, a, 0);
+    }
+    return (int)hipGetLastError();
+}
+template <int GT, int PT, int BITS, bool KEEP>
+int launch_long(const MultiAdamLaunch& a, hipStream_t s) {
+    for (int t0 = 0; t0 < a.n_tiles; t0 += kSliceTiles) {
+        const int tiles = a.n_tiles - t0 < kSliceTiles ? a.n_tiles - t0 : kSliceTiles;
+        hipLaunchKernelGGL((multi_adamw_kernel<GT, PT, BITS, kMultiRowsLong, KEEP>),
+                           dim3((unsigned)((tiles + kWaves - 1) / kWaves)), dim3(kThreads),
+                           kLdsFourBlocks, s, a, t0);
     }
     return (int)hipGetLastError();
 }
@@ -830,13 +852,11 @@ int launch_update(const MultiAdamLaunch& a, const MultiNormLaunch* n, const Mult
         return launch_short<GT, PT, BITS, kMultiRowsTiny>(a, n, step, s);
     if (a.tile_rows == kMultiRowsShort)
         return launch_short<GT, PT, BITS, kMultiRowsShort>(a, n, step, s);
-    for (int t0 = 0; t0 < a.n_tiles; t0 += kSliceTiles) {
-        const int tiles = a.n_tiles - t0 < kSliceTiles ? a.n_tiles - t0 : kSliceTiles;
-        hipLaunchKernelGGL((multi_adamw_kernel<GT, PT, BITS, kMultiRowsLong>),
-                           dim3((unsigned)((tiles + kWaves - 1) / kWaves)), dim3(kThreads),
-                           kLdsFourBlocks, s, a, t0);
+    if constexpr (PT != ZERO_NONE) {
+        const int64_t copy_bytes = (int64_t)a.n_tiles * kMultiRowsLong * kRow * 2;
+        if (copy_bytes <= kKeepCopyBytes) return launch_long<GT, PT, BITS, true>(a, s);
     }
-    return (int)hipGetLastError();
+    return launch_long<GT, PT, BITS, false>(a, s);
 }
 template <int GT, int PT>
 int launch_update(const MultiAdamLaunch& a, const MultiNormLaunch* n, const MultiStep* p, hipStream_t s) {
