@@ -243,13 +243,14 @@ class StepState:
 
     def upload(self, host_state):
         import torch
-        raw = bytes(bytearray(host_state))
-        self.buf.copy_(torch.frombuffer(bytearray(raw), dtype=torch.uint8))
+        self.buf.copy_(torch.frombuffer(host_state, dtype=torch.uint8))
 
     def read(self):
         """Host copy of the state (synchronizes with the current stream)."""
-        raw = self.buf.cpu().numpy().tobytes()
-        return zero_step_state_t.from_buffer_copy(raw)
+        import torch
+        host_state = zero_step_state_t()
+        torch.frombuffer(host_state, dtype=torch.uint8).copy_(self.buf)
+        return host_state
 
     def set_remote(self, sumsq=0.0, overflow=0):
         st = self.read()

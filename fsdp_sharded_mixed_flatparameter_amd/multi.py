@@ -68,14 +68,16 @@ class MultiPlan:
         tensors = list(tensors)
         if len(tensors) != len(self):
             raise ValueError("%s must have one entry per tensor (%d)" % (name, len(self)))
+        dev, ptrs = self._image.device, []
         for k, (t, n) in enumerate(zip(tensors, self.numels)):
-            _dev(t, "%s[%d]" % (name, k), (_dtype_name(dtype),))
-            if t.numel() != n:
-                raise ValueError("%s[%d] has %d elements, the plan says %d" % (name, k, t.numel(), n))
-            if t.device != self._image.device:
-                raise ValueError("%s[%d] is on %s, the plan on %s" % (name, k, t.device,
-                                                                     self._image.device))
-        return tensors, (C.c_void_p * max(len(self), 1))(*[t.data_ptr() or None for t in tensors])
+            if not (t.dtype == dtype and t.numel() == n and t.is_cuda and t.device == dev
+                    and t.is_contiguous()):
+                _dev(t, "%s[%d]" % (name, k), (_dtype_name(dtype),))
+                if t.numel() != n:
+                    raise ValueError("%s[%d] has %d elements, the plan says %d" % (name, k, t.numel(), n))
+                raise ValueError("%s[%d] is on %s, the plan on %s" % (name, k, t.device, dev))
+            ptrs.append(t.data_ptr() or None)
+        return tensors, (C.c_void_p * max(len(self), 1))(*ptrs)
 
     def bind(self, grads, params=None, lr_mult=None, decay_mult=None):
         """Name the gradients, and the 16-bit parameters if the plan has them,
@@ -137,7 +139,8 @@ class TensorListOptimizer:
         self.first_row = [0] + list(itertools.accumulate(rows))[:-1]
         size = self.plan.rows * ZERO_ROW
         kinds = (torch.float8_e4m3fn, torch.float8_e5m2) if state_bits == 8 else (torch.float32,) * 2
-        arenas = [torch.zeros(size, device=dev)]
+        # rows without padding are filled by the copy below
+        arenas = [(torch.zeros if any(x % ZERO_ROW for x in n) else torch.empty)(size, device=dev)]
         arenas += [torch.zeros(size * k.itemsize, dtype=torch.uint8, device=dev).view(k) for k in kinds]
         for _ in range(2):
             arenas.append(torch.zeros(self.plan.rows, device=dev) if state_bits == 8 else None)
@@ -145,8 +148,8 @@ class TensorListOptimizer:
         # the call's arguments that never change
         self._fixed = (self.plan._ref, self.plan._image_ptr) + tuple(
             None if t is None else C.c_void_p(t.data_ptr()) for t in arenas)
-        for v, t in zip(self.views(self.master), masters):
-            v.copy_(t.view(-1))
+        if size:
+            torch._foreach_copy_(self.views(self.master), [t.view(-1) for t in masters])
         self.hp = dict(hp)
         self.statistics, self.seed = bool(statistics), int(seed)
         self.lr_mult, self.decay_mult = lr_mult, decay_mult

@@ -559,3 +559,19 @@ def test_bind_refusals(zf):
         opt.plan.bind([g], [g.clone()], lr_mult=[-1.0])
     opt.bind([g], [g.clone()])
     opt.step()
+
+
+def test_example_trains(zf):
+    """The example's MLP learns with 8-bit states as with 32-bit ones."""
+    import os
+    import sys
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
+                                    "examples"))
+    import list_adamw
+    final = {}
+    for bits in (32, 8):
+        losses, opt = list_adamw.train(bits, 150)
+        assert opt.state.read().step == 150
+        assert losses[-1] < 0.2 * losses[0], (bits, losses[0], losses[-1])
+        final[bits] = losses[-1]
+    assert final[8] < 2 * final[32] + 0.01, final
