@@ -722,18 +722,21 @@ struct Tile {
 };
 
 // One wave per tile, in launches of at most kSliceTiles tiles over consecutive
-// ranges, at most kBlocksPerCu blocks per compute unit (a dynamic LDS
+// ranges, with at most two blocks per compute unit for 32-bit states and four
+// for 8-bit ones, which have half the bytes in flight per wave (a dynamic LDS
 // reservation that the kernel does not use): both keep the addresses in flight
-// in one window of every array.  Whole steps, us, same allocation:
+// in one window of every array.  Whole steps, us, each line on one allocation:
 //                       one launch, full   slices, full   slices, 4 per CU   2 per CU
-//   2.02e8, 32-bit            976               944              929            931
-//   2.02e8, 8-bit             575               565              563            577
-//   1.25e9, 8-bit            3700              3545             3518           3524
-//   3e7, 8-bit                 83                83               82             86
-// Half the slice: 941, 572 and 3546.  Tiles of two rows run within 2% of tiles
-// of four.  A resident grid taking tiles from a counter in the order its blocks
-// ask (the flat step's form for large shards): 8-10% slower here, since a
-// request, about 12 ns one after the other, must not cover more than 100 KB.
+//   2.02e8, 32-bit            991               984              991            974
+//   3e7, 32-bit               141               141              137            136
+//   2.02e8, 8-bit             569               567              572            579
+//   3e7, 8-bit                 81                81               78             87
+//   1.25e9, 8-bit            3941              3633             3609           3552
+// Slices of half and twice the size are within 2%.  A resident grid taking
+// tiles from a counter in the order its blocks ask (the flat step's form for
+// large shards) took 1008 against 1016 us on the first line's list, 613
+// against 604 on the third's and 162 against 147 on the second's (before
+// gradients were kept).
 constexpr int kSliceTiles = 131072;
 // A copy of at most this size is left in the memory-side cache (KEEP).  Steps
 // without and with, us: 3e7 elements 151 and 138 (32-bit states), 87 and 79
@@ -741,7 +744,7 @@ constexpr int kSliceTiles = 131072;
 // compete for the cache, 518 and 486, 294 and 289, but 1.3e8 674 and 655, 379
 // and 386, and 2.02e8 1000 and 1034, 572 and 624.
 constexpr int64_t kKeepCopyBytes = (int64_t)192 << 20;
-constexpr unsigned kLdsFourBlocks = 40 * 1024;
+constexpr unsigned kLdsTwoBlocks = 56 * 1024, kLdsFourBlocks = 40 * 1024;
 template <int GT, int PT, int BITS, int R, bool KEEP>
 __global__ void __launch_bounds__(kThreads) multi_adamw_kernel(MultiAdamLaunch a, int tile0) {
     const int lane = threadIdx.x & 63;
@@ -840,7 +843,7 @@ int launch_long(const MultiAdamLaunch& a, hipStream_t s) {
         const int tiles = a.n_tiles - t0 < kSliceTiles ? a.n_tiles - t0 : kSliceTiles;
         hipLaunchKernelGGL((multi_adamw_kernel<GT, PT, BITS, kMultiRowsLong, KEEP>),
                            dim3((unsigned)((tiles + kWaves - 1) / kWaves)), dim3(kThreads),
-                           kLdsFourBlocks, s, a, t0);
+                           BITS == 32 ? kLdsTwoBlocks : kLdsFourBlocks, s, a, t0);
     }
     return (int)hipGetLastError();
 }
