@@ -683,7 +683,7 @@ int zero_multi_bind(const zero_multi_plan_t* plan, const void* const* grads, voi
                     const double* lr_mult, const double* decay_mult, void* image) {
     const char* fn = "zero_multi_bind";
     if (int e = check_plan(fn, plan)) return e;
-    if (!image) return fail(ZERO_EINVAL, "%s: NULL image", fn);
+    if (!image && plan->n_tensors > 0) return fail(ZERO_EINVAL, "%s: NULL image", fn);
     if (!aligned(image, 8)) return fail(ZERO_EALIGN, "%s: image not 8-byte aligned", fn);
     const bool copy = plan->param_dtype != ZERO_NONE;
     const int32_t n = plan->n_tensors;

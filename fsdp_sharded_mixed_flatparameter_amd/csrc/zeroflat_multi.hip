@@ -6,8 +6,10 @@
 //                       scalars, loss scaler and counters (multi_prepare_kernel
 //                       does only that)
 //   multi_adamw_kernel  AdamW with 32-bit or 8-bit states, 16-bit copy
+//   multi_adamw_short_kernel  the same for short lists, with the fold inside
 //
-// Everything here streams HBM once; none of it is a contraction.  The state
+// A step reads the gradients twice and everything else once; none of it is a
+// contraction.  The state
 // arenas are rows of 256 elements, so a wave owns whole rows: in a row lane l
 // holds elements 4l .. 4l+3 (16 bytes of each fp32 array, 8 of a 16-bit one,
 // 4 of an 8-bit one per lane).  Only the gradients and the 16-bit parameters
@@ -313,11 +315,11 @@ __global__ void __launch_bounds__(kThreads) multi_stats_kernel(MultiNormLaunch a
 
 // ---------------------------------------------------------------- folds
 // Block 0: the total, and with `step` what the update needs of it; the other
-// blocks: a tensor's sum each, or (per_wave) a tensor's sum per wave.  A launch of its own: folding in the block that
-// finishes last instead (stores and a count at device scope) made the small
-// MLP's statistics 8.3 us against 6.0 and the 2.02e8-element block's 70 against
-// 66, and a count per block of the update costs about 12 ns each, one after
-// the other.
+// blocks: a tensor's sum each, or (per_wave) a tensor's sum per wave.  A launch
+// of its own: folding in the block that finishes last instead (stores and a
+// count at device scope) made the small MLP's statistics 8.3 us against 6.0 and
+// the 2.02e8-element block's 70 against 66, and a count per block of the update
+// costs about 12 ns each, one after the other.
 constexpr int kFoldThreads = 512;
 __global__ void __launch_bounds__(kFoldThreads) multi_fold_kernel(MultiNormLaunch a, MultiStep step,
                                                                   int per_wave) {

@@ -27,7 +27,8 @@ class MultiPlan:
 
     `numels` and the dtypes are fixed; bind() names the tensors and may be called
     again whenever they move.  The plan keeps the tensors alive.  A plan is used
-    by one stream at a time."""
+    by one stream at a time.  tensor_sumsq is a device view (fp64, one entry per
+    tensor) of what the latest statistics wrote."""
 
     def __init__(self, numels, grad_dtype, param_dtype=None, state_bits=0, device="cuda"):
         numels = [int(x) for x in numels]

@@ -538,6 +538,14 @@ def test_an_empty_list_still_advances_the_state(zf):
     st = opt.state.read()
     assert (st.step, st.last_norm, st.last_skipped) == (1, 0.0, 0)
     assert opt.plan.tensor_sumsq.tolist() == [0.0]
+    plan = zf.MultiPlan([], torch.float32)
+    plan.bind([])
+    state = zf.StepState(1.0, False)
+    state.field("sumsq").fill_(3.0)
+    zf.zero_multi_unscale_norm(plan, state)
+    assert state.read().sumsq == 3.0
+    zf.zero_multi_unscale_norm(plan, state, reset=True)
+    assert (state.read().sumsq, state.read().overflow) == (0.0, 0)
 
 
 def test_bind_refusals(zf):

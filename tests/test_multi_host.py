@@ -95,6 +95,8 @@ def test_bind_refusals(zf):
     assert L.zero_multi_bind(None, None, None, None, None, image) == -1
     assert np.array_equal(host, before)                    # nothing written on error
     assert bind(lr=(1.0, 2.0, 0.5)) == 0                   # an empty tensor has no address
+    empty = make(zf, [])[1]
+    assert L.zero_multi_bind(C.byref(empty), None, None, None, None, None) == 0
     rc, plan32, host32 = make(zf, [4], param=-1)
     one = (C.c_void_p * 1)(0x1000)
     assert L.zero_multi_bind(C.byref(plan32), one, one, None, None,
