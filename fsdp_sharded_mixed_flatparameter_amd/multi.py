@@ -183,7 +183,9 @@ class TensorListOptimizer:
 
     def step(self, stream=None):
         """Statistics over the bound gradients, then the step (one library call,
-        as zero_multi_adamw_step with the arguments prepared)."""
+        as zero_multi_adamw_step with the arguments prepared).  On a stream
+        other than the tensors' own, the caller orders the two, and keeps the
+        optimizer until the step is done."""
         if not self.plan._bound:
             self.plan._require_bound()
         flags = ZERO_STEP_FINALIZE | (ZERO_MULTI_STATISTICS if self.statistics else 0)
