@@ -29,7 +29,7 @@ EXPORTS = ("zero_last_error", "zero_flat_layout", "zero_step_state_init",
            "zero_quant_allgather_slot", "zero_dequant_allgather", "zero_grad_accumulate_shard",
            "zero_grad_reduce_shard_int8", "zero_offload_adamw_host", "zero_offload_step",
            "zero_grad_reduce_shard_noalloc", "zero_multi_plan_init", "zero_multi_bind",
-           "zero_multi_unscale_norm", "zero_multi_adamw_step")
+           "zero_multi_unscale_norm", "zero_multi_adamw_step", "zero_multi_adamw_step_args")
 
 
 class zero_span_t(C.Structure):
@@ -74,6 +74,13 @@ class zero_multi_plan_t(C.Structure):
                  "tile_rows", "reserved")]
 
 
+class zero_multi_step_args_t(C.Structure):
+    _fields_ = [(f, C.c_void_p) for f in
+                ("plan", "d_plan", "master", "exp_avg", "exp_avg_sq", "m_scale", "v_scale",
+                 "d_state")] + \
+               [("hp", zero_adamw_hparams_t), ("seed", C.c_uint32), ("flags", C.c_uint32)]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError("libzeroflat.so is not built (%s); run __graft_entry__.build()" % LIB_PATH)
@@ -115,6 +122,8 @@ def _load():
     L.zero_multi_unscale_norm.argtypes = [vp, vp, u32, vp, vp]
     L.zero_multi_adamw_step.restype = C.c_int
     L.zero_multi_adamw_step.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, u32, u32, vp, vp]
+    L.zero_multi_adamw_step_args.restype = C.c_int
+    L.zero_multi_adamw_step_args.argtypes = [vp, vp]
     return L
 
 
@@ -150,15 +159,21 @@ def _ptr(t):
     return None if t is None else C.c_void_p(t.data_ptr())
 
 
+_raw_stream = None
+
+
 def _current_raw_stream():
     """torch's current HIP stream on the current device, as an integer handle
     (the raw-stream query torch's own generated code uses; the public
     torch.cuda.current_stream() costs several microseconds per call)."""
-    import torch
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    if raw is None:
-        return torch.cuda.current_stream().cuda_stream
-    return raw(torch._C._cuda_getDevice())
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is None:
+            return torch.cuda.current_stream().cuda_stream
+        _raw_stream = (raw, torch._C._cuda_getDevice)
+    return _raw_stream[0](_raw_stream[1]())
 
 
 def _stream(stream):
@@ -502,7 +517,8 @@ def zero_multi_unscale_norm(plan, state, reset=False, stream=None):
     if not plan._bound:
         plan._require_bound()
     rc = _lib.zero_multi_unscale_norm(plan._ref, plan._image_ptr, ZERO_MULTI_RESET if reset else 0,
-                                      _state_ptr(state),
+                                      state.buf.data_ptr() if type(state) is StepState
+                                      else _state_ptr(state),
                                       _current_raw_stream() if stream is None else _stream(stream))
     if rc:
         _check(rc)

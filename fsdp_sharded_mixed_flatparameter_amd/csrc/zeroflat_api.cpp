@@ -790,4 +790,11 @@ int zero_multi_adamw_step(const zero_multi_plan_t* plan, void* d_plan, float* ma
     return ok();
 }
 
+int zero_multi_adamw_step_args(const zero_multi_step_args_t* args, void* stream) {
+    if (!args) return fail(ZERO_EINVAL, "zero_multi_adamw_step_args: NULL args");
+    return zero_multi_adamw_step(args->plan, args->d_plan, args->master, args->exp_avg,
+                                 args->exp_avg_sq, args->m_scale, args->v_scale, &args->hp,
+                                 args->seed, args->flags, args->d_state, stream);
+}
+
 }  // extern "C"

@@ -22,6 +22,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "zf_launch.h"
 
 namespace zf {
@@ -321,8 +323,7 @@ __global__ void __launch_bounds__(kThreads) multi_stats_kernel(MultiNormLaunch a
 // the 2.02e8-element block's 70 against 66, and a count per block of the update
 // costs about 12 ns each, one after the other.
 constexpr int kFoldThreads = 512;
-__global__ void __launch_bounds__(kFoldThreads) multi_fold_kernel(MultiNormLaunch a, MultiStep step,
-                                                                  int per_wave) {
+__device__ __forceinline__ void fold(const MultiNormLaunch& a, const MultiStep* step, int per_wave) {
     int p0 = 0, np = a.n_spans;
     // read first: thread 0's chain is the whole launch
     MultiState st = {};
@@ -361,14 +362,21 @@ __global__ void __launch_bounds__(kFoldThreads) multi_fold_kernel(MultiNormLaunc
         return;
     }
     add_sum(st, x, a.reset);
-    if (step.scalars) {
-        const MultiScalars r = step_scalars(step, st);
-        *step.scalars = r;
-        write_state(step, st, r);
+    if (step) {
+        const MultiScalars r = step_scalars(*step, st);
+        *step->scalars = r;
+        write_state(*step, st, r);
     } else {
         a.st->sumsq = st.sumsq;
         a.st->overflow = st.overflow;
     }
+}
+__global__ void __launch_bounds__(kFoldThreads) multi_fold_kernel(MultiNormLaunch a, int per_wave) {
+    fold(a, nullptr, per_wave);
+}
+__global__ void __launch_bounds__(kFoldThreads) multi_fold_step_kernel(MultiNormLaunch a,
+                                                                       MultiStep step, int per_wave) {
+    fold(a, &step, per_wave);
 }
 __global__ void multi_prepare_kernel(MultiStep step) {
     if (threadIdx.x != 0) return;
@@ -823,31 +831,41 @@ __global__ void __launch_bounds__(kThreads) multi_adamw_short_kernel(MultiAdamLa
     if (lane == 0) n.tensor_sumsq[k] = z;
 }
 
+// A launch by the runtime's plain entry point, 0.15 us less of the host's time
+// than the launch syntax, which passes the shape through a second call.
+template <typename... P, typename... A>
+int launch(void (*kernel)(P...), unsigned grid, unsigned block, unsigned lds, hipStream_t s,
+           const A&... args) {
+    static_assert((std::is_same<P, A>::value && ...), "arguments of the kernel's own types");
+    void* p[] = {const_cast<void*>(static_cast<const void*>(&args))...};
+    const int e = (int)hipLaunchKernel(reinterpret_cast<const void*>(kernel), dim3(grid), dim3(block),
+                                       p, lds, s);
+    if (e) (void)hipGetLastError();   // reported here, not by the next call
+    return e;
+}
+
 // n, step: for multi_adamw_short_kernel, or null
 template <int GT, int PT, int BITS, int R>
 int launch_short(const MultiAdamLaunch& a, const MultiNormLaunch* n, const MultiStep* step,
                  hipStream_t s) {
     const int tile_blocks = (a.n_tiles + kWaves - 1) / kWaves;
-    if (n) {
-        const int sum_blocks = (n->n_tensors + kWaves - 1) / kWaves;
-        hipLaunchKernelGGL((multi_adamw_short_kernel<GT, PT, BITS, R>),
-                           dim3((unsigned)(sum_blocks + tile_blocks)), dim3(kThreads), 0, s, a, *n,
-                           *step, sum_blocks);
-    } else {
-        hipLaunchKernelGGL((multi_adamw_kernel<GT, PT, BITS, R, true>), dim3((unsigned)tile_blocks),
-                           dim3(kThreads), 0, s, a, 0);
-    }
-    return (int)hipGetLastError();
+    if (!n)
+        return launch(multi_adamw_kernel<GT, PT, BITS, R, true>, (unsigned)tile_blocks, kThreads, 0, s,
+                      a, 0);
+    const int sum_blocks = (n->n_tensors + kWaves - 1) / kWaves;
+    return launch(multi_adamw_short_kernel<GT, PT, BITS, R>, (unsigned)(sum_blocks + tile_blocks),
+                  kThreads, 0, s, a, *n, *step, sum_blocks);
 }
 template <int GT, int PT, int BITS, bool KEEP>
 int launch_long(const MultiAdamLaunch& a, hipStream_t s) {
     for (int t0 = 0; t0 < a.n_tiles; t0 += kSliceTiles) {
         const int tiles = a.n_tiles - t0 < kSliceTiles ? a.n_tiles - t0 : kSliceTiles;
-        hipLaunchKernelGGL((multi_adamw_kernel<GT, PT, BITS, kMultiRowsLong, KEEP>),
-                           dim3((unsigned)((tiles + kWaves - 1) / kWaves)), dim3(kThreads),
-                           BITS == 32 ? kLdsTwoBlocks : kLdsFourBlocks, s, a, t0);
+        const int e = launch(multi_adamw_kernel<GT, PT, BITS, kMultiRowsLong, KEEP>,
+                             (unsigned)((tiles + kWaves - 1) / kWaves), kThreads,
+                             BITS == 32 ? kLdsTwoBlocks : kLdsFourBlocks, s, a, t0);
+        if (e) return e;
     }
-    return (int)hipGetLastError();
+    return 0;
 }
 template <int GT, int PT, int BITS>
 int launch_update(const MultiAdamLaunch& a, const MultiNormLaunch* n, const MultiStep* step,
@@ -881,37 +899,32 @@ int launch_update(const MultiAdamLaunch& a, const MultiNormLaunch* n, const Mult
 
 int launch_stats(const MultiNormLaunch& a, hipStream_t s) {
     if (a.n_spans == 0) return 0;
-    const dim3 grid((unsigned)a.n_spans), block(kThreads);
-    if (a.dtype == ZERO_F32)
-        hipLaunchKernelGGL((multi_stats_kernel<ZERO_F32>), grid, block, 0, s, a);
-    else if (a.dtype == ZERO_F16)
-        hipLaunchKernelGGL((multi_stats_kernel<ZERO_F16>), grid, block, 0, s, a);
-    else
-        hipLaunchKernelGGL((multi_stats_kernel<ZERO_BF16>), grid, block, 0, s, a);
-    return (int)hipGetLastError();
+    const unsigned grid = (unsigned)a.n_spans;
+    if (a.dtype == ZERO_F32) return launch(multi_stats_kernel<ZERO_F32>, grid, kThreads, 0, s, a);
+    if (a.dtype == ZERO_F16) return launch(multi_stats_kernel<ZERO_F16>, grid, kThreads, 0, s, a);
+    return launch(multi_stats_kernel<ZERO_BF16>, grid, kThreads, 0, s, a);
 }
-int launch_fold(const MultiNormLaunch& a, const MultiStep& step, hipStream_t s) {
+int launch_fold(const MultiNormLaunch& a, const MultiStep* step, hipStream_t s) {
     // a wave per tensor where the tensors have few spans each on average
     const int per_wave = a.n_spans <= 64 * (int64_t)a.n_tensors;
     const unsigned per = per_wave ? kFoldThreads / 64 : 1;
-    hipLaunchKernelGGL(multi_fold_kernel, dim3(1 + ((unsigned)a.n_tensors + per - 1) / per),
-                       dim3(kFoldThreads), 0, s, a, step, per_wave);
-    return (int)hipGetLastError();
+    const unsigned grid = 1 + ((unsigned)a.n_tensors + per - 1) / per;
+    return step ? launch(multi_fold_step_kernel, grid, kFoldThreads, 0, s, a, *step, per_wave)
+                : launch(multi_fold_kernel, grid, kFoldThreads, 0, s, a, per_wave);
 }
 
 }  // namespace
 
 int launch_multi_norm(const MultiNormLaunch& a, void* stream) {
     if (const int e = launch_stats(a, (hipStream_t)stream)) return e;
-    return launch_fold(a, MultiStep{}, (hipStream_t)stream);
+    return launch_fold(a, nullptr, (hipStream_t)stream);
 }
 
 int launch_multi_step(const MultiAdamLaunch& a, const MultiNormLaunch* norm, const MultiStep& step,
                       void* stream) {
     hipStream_t s = (hipStream_t)stream;
     if (!norm) {
-        hipLaunchKernelGGL(multi_prepare_kernel, dim3(1), dim3(64), 0, s, step);
-        if (const int e = (int)hipGetLastError()) return e;
+        if (const int e = launch(multi_prepare_kernel, 1, 64, 0, s, step)) return e;
         return launch_update(a, nullptr, nullptr, s);
     }
     MultiNormLaunch n = *norm;
@@ -921,7 +934,7 @@ int launch_multi_step(const MultiAdamLaunch& a, const MultiNormLaunch* norm, con
     if (!fold_in_update) n.snapshot = nullptr;
     if (const int e = launch_stats(n, s)) return e;
     if (fold_in_update) return launch_update(a, &n, &step, s);
-    if (const int e = launch_fold(n, step, s)) return e;
+    if (const int e = launch_fold(n, &step, s)) return e;
     return launch_update(a, nullptr, nullptr, s);
 }
 

@@ -10,7 +10,7 @@ import torch
 
 from . import (_DTYPE_CODES, _FLOATS, ZERO_MULTI_STATISTICS, ZERO_NONE, ZERO_ROW,
                ZERO_STEP_FINALIZE, StepState, _check, _current_raw_stream, _dev, _dtype_name, _lib, _stream,
-               zero_adamw_hparams_t, zero_multi_plan_t)
+               zero_adamw_hparams_t, zero_multi_plan_t, zero_multi_step_args_t)
 
 
 def _doubles(x, n, name):
@@ -146,22 +146,25 @@ class TensorListOptimizer:
         for _ in range(2):
             arenas.append(torch.zeros(self.plan.rows, device=dev) if state_bits == 8 else None)
         self._arenas = tuple(arenas)
-        # the call's arguments that never change
-        self._fixed = (self.plan._ref, self.plan._image_ptr) + tuple(
-            None if t is None else C.c_void_p(t.data_ptr()) for t in arenas)
         if size:
             torch._foreach_copy_(self.views(self.master), [t.view(-1) for t in masters])
         self.hp = dict(hp)
         self.statistics, self.seed = bool(statistics), int(seed)
         self.lr_mult, self.decay_mult = lr_mult, decay_mult
-        self.state = StepState(loss_scale, dynamic, window, min_scale, device=dev)
-        self._h = (None, None)   # (hp items, their C struct)
+        self._state = StepState(loss_scale, dynamic, window, min_scale, device=dev)
+        # the library call's arguments, of which only hp, seed and flags change
+        self._args = zero_multi_step_args_t(
+            C.addressof(self.plan._plan), self.plan._image_ptr,
+            *[None if t is None else t.data_ptr() for t in arenas], self._state.ptr())
+        self._ref = C.byref(self._args)
+        self._args_of = None
 
     master = property(lambda self: self._arenas[0])
     exp_avg = property(lambda self: self._arenas[1])
     exp_avg_sq = property(lambda self: self._arenas[2])
     exp_avg_scale = property(lambda self: self._arenas[3])
     exp_avg_sq_scale = property(lambda self: self._arenas[4])
+    state = property(lambda self: self._state)
 
     def views(self, arena):
         """The tensors inside an arena (flat views, without the rows' padding)."""
@@ -172,25 +175,25 @@ class TensorListOptimizer:
         """Name the gradients and the 16-bit parameters; again when they move."""
         self.plan.bind(grads, params, self.lr_mult, self.decay_mult)
 
-    def _hparams(self):
-        """The C hyper-parameters, rebuilt only when self.hp changed."""
-        key = tuple(self.hp.items())
-        if self._h[0] != key:
-            if not self.statistics and self.hp.get("max_grad_norm", 0.0) > 0.0:
-                raise ValueError("clipping needs the statistics: max_grad_norm must be 0 without them")
-            self._h = (key, C.byref(zero_adamw_hparams_t(**self.hp)))
-        return self._h[1]
+    def _refresh(self):
+        """The arguments that the attributes hp, seed and statistics set."""
+        if not self.statistics and self.hp.get("max_grad_norm", 0.0) > 0.0:
+            raise ValueError("clipping needs the statistics: max_grad_norm must be 0 without them")
+        self._args.hp = zero_adamw_hparams_t(**self.hp)
+        self._args.seed = self.seed & 0xffffffff
+        self._args.flags = ZERO_STEP_FINALIZE | (ZERO_MULTI_STATISTICS if self.statistics else 0)
+        self._args_of = (dict(self.hp), self.seed, self.statistics)
 
     def step(self, stream=None):
         """Statistics over the bound gradients, then the step (one library call,
-        as zero_multi_adamw_step with the arguments prepared).  On a stream
+        as zero_multi_adamw_step with its arguments prepared).  On a stream
         other than the tensors' own, the caller orders the two, and keeps the
         optimizer until the step is done."""
         if not self.plan._bound:
             self.plan._require_bound()
-        flags = ZERO_STEP_FINALIZE | (ZERO_MULTI_STATISTICS if self.statistics else 0)
-        rc = _lib.zero_multi_adamw_step(*self._fixed, self._hparams(), self.seed & 0xffffffff, flags,
-                                        self.state.ptr(),
-                                        _current_raw_stream() if stream is None else _stream(stream))
+        if self._args_of != (self.hp, self.seed, self.statistics):
+            self._refresh()
+        rc = _lib.zero_multi_adamw_step_args(
+            self._ref, _current_raw_stream() if stream is None else _stream(stream))
         if rc:
             _check(rc)

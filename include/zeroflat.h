@@ -545,6 +545,23 @@ int zero_multi_adamw_step(const zero_multi_plan_t* plan, void* d_plan, float* ma
                           void* exp_avg, void* exp_avg_sq, float* m_scale, float* v_scale,
                           const zero_adamw_hparams_t* hp, uint32_t seed, uint32_t flags,
                           zero_step_state_t* d_state, void* stream);
+
+/* The same call with its arguments in a HOST struct, for a caller that fills it
+ * once and steps many times: passing them one by one through a foreign-function
+ * interface takes as long as a small kernel. */
+typedef struct {
+    const zero_multi_plan_t* plan;
+    void* d_plan;
+    float* master;
+    void* exp_avg;
+    void* exp_avg_sq;
+    float* m_scale;
+    float* v_scale;
+    zero_step_state_t* d_state;
+    zero_adamw_hparams_t hp;
+    uint32_t seed, flags;
+} zero_multi_step_args_t;
+int zero_multi_adamw_step_args(const zero_multi_step_args_t* args, void* stream);
 #ifdef __cplusplus
 }
 #endif

@@ -128,6 +128,13 @@ def test_calls_validate_before_launch(zf):
         bad = zf.zero_adamw_hparams_t(**dict(HP, beta2=1.0))
         assert step(hp=bad) == -1
         assert b"zero_multi_adamw_step" in L.zero_last_error()
+        # the same call through the struct of its arguments
+        assert L.zero_multi_adamw_step_args(None, None) == -1
+        args = zf.zero_multi_step_args_t(C.addressof(plan), 0x1000, 0x1000, 0x1000, 0x1000,
+                                         *[0x1000 if bits == 8 else None] * 2, None, hp, 0, 1)
+        assert L.zero_multi_adamw_step_args(C.byref(args), None) == -1      # no state
+        args.d_state, args.master = 0x10000, 0x1008
+        assert L.zero_multi_adamw_step_args(C.byref(args), None) == -2
     assert L.zero_multi_unscale_norm(ref, None, 0, st, None) == -1
     assert L.zero_multi_unscale_norm(ref, P, 0, None, None) == -1
     assert L.zero_multi_unscale_norm(ref, P, 1, st, None) == -1
