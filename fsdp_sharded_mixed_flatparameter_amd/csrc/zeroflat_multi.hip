@@ -102,28 +102,40 @@ __device__ __forceinline__ uint32_t from_below(uint32_t x, uint32_t edge) {
 __device__ __forceinline__ uint32_t lane_value(uint32_t x, int lane) {
     return (uint32_t)__builtin_amdgcn_readlane((int)x, lane);
 }
+// Reductions over a wave: DPP shifts within rows of 16 lanes, then the row
+// broadcasts (gfx9-family controls, 0 where there is no source); lane 63 ends
+// with all of it.  A butterfly through LDS permutes takes three times as long,
+// 0.3 us of a small kernel.
+#define ZF_WAVE_STEPS(STEP)                                                          \
+    STEP(0x111, 0xf) /* row_shr:1 */ STEP(0x112, 0xf) /* row_shr:2 */                \
+    STEP(0x114, 0xf) /* row_shr:4 */ STEP(0x118, 0xf) /* row_shr:8 */                \
+    STEP(0x142, 0xa) /* row_bcast:15 */ STEP(0x143, 0xc) /* row_bcast:31 */
+#define ZF_DPP(x, ctrl, rows) __builtin_amdgcn_update_dpp(0, (int)(x), ctrl, rows, 0xf, false)
+// The sum in a fixed order, in every lane.
 __device__ __forceinline__ double wave_sum(double x) {
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) x += __shfl_xor(x, off, 64);
-    return x;
+#define ZF_SUM_STEP(ctrl, rows)                                                      \
+    {                                                                                \
+        const uint64_t b = __builtin_bit_cast(uint64_t, x);                          \
+        const uint64_t o = (uint64_t)(uint32_t)ZF_DPP((uint32_t)b, ctrl, rows) |     \
+                           (uint64_t)(uint32_t)ZF_DPP(b >> 32, ctrl, rows) << 32;    \
+        x += __builtin_bit_cast(double, o);                                          \
+    }
+    ZF_WAVE_STEPS(ZF_SUM_STEP)
+#undef ZF_SUM_STEP
+    const uint64_t b = __builtin_bit_cast(uint64_t, x);
+    return __builtin_bit_cast(double, (uint64_t)lane_value((uint32_t)b, 63) |
+                                          (uint64_t)lane_value((uint32_t)(b >> 32), 63) << 32);
 }
-// The largest of the lanes' values, none of them negative or NaN, as a scalar:
-// DPP shifts within rows of 16 lanes, then the row broadcasts (gfx9-family
-// controls); lane 63 ends with all of it.  Patterns of floats >= 0 are ordered
-// as integers.
+// The largest of values that are neither negative nor NaN (whose patterns are
+// ordered as integers), as a scalar.
 __device__ __forceinline__ float wave_max(float x) {
     uint32_t u = __float_as_uint(x);
-#define ZF_MAX_STEP(ctrl, rows)                                                                 \
-    {                                                                                           \
-        const uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)u, ctrl, rows, 0xf, false); \
-        u = u > o ? u : o;                                                                      \
+#define ZF_MAX_STEP(ctrl, rows)                            \
+    {                                                      \
+        const uint32_t o = (uint32_t)ZF_DPP(u, ctrl, rows); \
+        u = u > o ? u : o;                                 \
     }
-    ZF_MAX_STEP(0x111, 0xf)   // row_shr:1
-    ZF_MAX_STEP(0x112, 0xf)   // row_shr:2
-    ZF_MAX_STEP(0x114, 0xf)   // row_shr:4
-    ZF_MAX_STEP(0x118, 0xf)   // row_shr:8
-    ZF_MAX_STEP(0x142, 0xa)   // row_bcast:15
-    ZF_MAX_STEP(0x143, 0xc)   // row_bcast:31
+    ZF_WAVE_STEPS(ZF_MAX_STEP)
 #undef ZF_MAX_STEP
     return __uint_as_float(lane_value(u, 63));
 }
