@@ -322,7 +322,7 @@ __global__ void __launch_bounds__(kThreads) multi_stats_kernel(MultiNormLaunch a
         s1 = __builtin_fma(d, d, s1);
     }
     const double sum = block_sum<kWaves>(s0 + s1);
-    // the loss scale is a power of two: applied to the sum as exactly as to
+    // the loss scale, a power of two, is applied to the sum as exactly as to
     // every element
     if (tid == 0) a.partials[s] = sum * inv * inv;
 }

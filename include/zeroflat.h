@@ -495,7 +495,9 @@ int zero_multi_bind(const zero_multi_plan_t* plan, const void* const* grads, voi
  *   tensor_sumsq[k] = sum of (double)u^2 over tensor k (plan->sumsq_off)
  *   sumsq += their sum;  overflow |= (that sum is not finite)
  * as zero_unscale_norm takes them over a shard, in an order fixed by the list's
- * sizes and its gradients' alignment.  With ZERO_MULTI_RESET sumsq and
+ * sizes and its gradients' alignment.  The loss scale is applied to the sums, in
+ * fp64: exactly so while it is a power of two (it always is unless min_scale is
+ * not one).  With ZERO_MULTI_RESET sumsq and
  * overflow are set instead (statistics outside a step; the scaler and
  * counters are not touched). */
 #define ZERO_MULTI_RESET 2u
