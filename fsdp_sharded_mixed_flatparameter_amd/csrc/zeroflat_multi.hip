@@ -183,7 +183,6 @@ __device__ __forceinline__ MultiScalars step_scalars(const MultiStep& p, const M
         r.coef = (float)(c < 1.0 ? c : 1.0);
     }
     r.inv = (float)(1.0 / (double)st.loss_scale);
-    r.inv_coef = r.inv * r.coef;
     const double bc1 = 1.0 - st.beta1_pow * p.beta1, bc2 = 1.0 - st.beta2_pow * p.beta2;
     r.bc1 = (float)bc1;
     r.bc2 = (float)bc2;
@@ -524,8 +523,11 @@ __device__ __forceinline__ void update_quad(const MultiAdamLaunch& a, const Mult
         for (int c = 0; c < 4; ++c) {
             // the states' operations are rounded one by one, so that they are
             // the same on any machine: a random rounding that falls the other
-            // way is a whole code off
-            const float g = gv[c] * s.inv_coef;
+            // way is a whole code off.  Two products for g: the factors' own may
+            // be below fp32's normal numbers (a scale near 2^127 with a clip
+            // below one) and lose the gradient
+            const float u = gv[c] * s.inv;
+            const float g = u * s.coef;
             m[c] = a.b1 * (m[c] * ms) + a.c1 * g;
             v[c] = a.b2 * (v[c] * vs) + a.c2 * (g * g);
             // the parameter's are not held in 8 bits: fused, and by the root

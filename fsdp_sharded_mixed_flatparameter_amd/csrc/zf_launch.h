@@ -120,7 +120,7 @@ struct MultiState {
 // a step's scalars, formed from them
 struct MultiScalars {
     double lr, lr_bc1, wd, norm;    // lr, lr / (1 - beta1^t), weight decay
-    float inv, coef, inv_coef, bc1, bc2, rs;
+    float inv, coef, bc1, bc2, rs;
     uint32_t key;
     int32_t skip;
 };

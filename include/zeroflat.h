@@ -522,7 +522,7 @@ int zero_multi_unscale_norm(const zero_multi_plan_t* plan, void* d_plan, uint32_
  *     rate_k = f32(lr_k / (1 - beta1^t)), rs = f32(1 / sqrt(1 - beta2^t))
  *     (p alone with fused multiply-adds, and the square root and 1/d to 1 unit
  *     in the last place, the root of a second moment below 2^-126 possibly 0;
- *     eps >= 2^-126); u and g by one product with (1/loss_scale) * coef
+ *     eps >= 2^-126)
  *   with keep_k = f32(1 - lr_k * wd_k).
  * The 8-bit states are then written back per row: top = min(max|x|, FLT_MAX),
  * scale = max(top * f32(1/most), 2^-126) (0 for a row of zeros), y =
