@@ -147,7 +147,8 @@ class TensorListOptimizer:
             arenas.append(torch.zeros(self.plan.rows, device=dev) if state_bits == 8 else None)
         self._arenas = tuple(arenas)
         if size:
-            torch._foreach_copy_(self.views(self.master), [t.view(-1) for t in masters])
+            # detached: a model's own parameters would make the arena part of a graph
+            torch._foreach_copy_(self.views(self.master), [t.detach().view(-1) for t in masters])
         self.hp = dict(hp)
         self.statistics, self.seed = bool(statistics), int(seed)
         self.lr_mult, self.decay_mult = lr_mult, decay_mult
