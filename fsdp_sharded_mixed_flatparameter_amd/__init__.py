@@ -257,7 +257,10 @@ class StepState:
         self.upload(zero_step_state_init(loss_scale, dynamic, window, min_scale))
 
     def upload(self, host_state):
+        """A zero_step_state_t, or its bytes as they were saved."""
         import torch
+        if not isinstance(host_state, zero_step_state_t):
+            host_state = bytearray(host_state)     # bytes are read-only
         self.buf.copy_(torch.frombuffer(host_state, dtype=torch.uint8))
 
     def read(self):
