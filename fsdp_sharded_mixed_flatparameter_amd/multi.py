@@ -119,7 +119,13 @@ class TensorListOptimizer:
     into them.
     bind() names the gradients and the 16-bit parameters that step() reads and
     writes; without a param_dtype the fp32 master is all there is.  With
-    statistics=False a step neither clips nor looks for an overflow."""
+    statistics=False a step neither clips nor looks for an overflow.
+
+    On one of several ranks the norm, the clip and the skip cover all of them:
+    take the statistics first (zero_multi_unscale_norm on plan and state),
+    exchange state.field("sumsq") and state.field("overflow"), put the others'
+    into state.field("remote_sumsq") and state.field("remote_overflow"), and
+    step with zero_multi_adamw_step on the arenas."""
 
     def __init__(self, masters, hp, state_bits=32, loss_scale=65536.0, dynamic=False, window=1000,
                  min_scale=1.0, lr_mult=None, decay_mult=None, statistics=True, seed=0,
