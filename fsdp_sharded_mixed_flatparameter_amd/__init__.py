@@ -516,7 +516,10 @@ def unflatten(flat, shapes, n_ranks=1, align=1):
 def zero_multi_unscale_norm(plan, state, reset=False, stream=None):
     """Statistics over the tensors bound to `plan` (a MultiPlan): the sum of
     squares of each unscaled gradient into plan.tensor_sumsq, their sum and the
-    overflow flag into `state` (added to it, or set with `reset`)."""
+    overflow flag into `state` (added to it, or set with `reset`).  A step adds
+    its own statistics to what its state holds: to look at them between steps,
+    give a StepState of their own, or zero state.field("sumsq") and
+    state.field("overflow") before the next step."""
     if not plan._bound:
         plan._require_bound()
     rc = _lib.zero_multi_unscale_norm(plan._ref, plan._image_ptr, ZERO_MULTI_RESET if reset else 0,

@@ -496,10 +496,13 @@ int zero_multi_bind(const zero_multi_plan_t* plan, const void* const* grads, voi
  *   sumsq += their sum;  overflow |= (that sum is not finite)
  * as zero_unscale_norm takes them over a shard, in an order fixed by the list's
  * sizes and its gradients' alignment.  The loss scale is applied to the sums, in
- * fp64: exactly so while it is a power of two (it always is unless min_scale is
- * not one).  With ZERO_MULTI_RESET sumsq and
- * overflow are set instead (statistics outside a step; the scaler and
- * counters are not touched). */
+ * fp64: exactly so while it is a power of two (it always is, unless it has come
+ * down to a min_scale that is none).  With ZERO_MULTI_RESET sumsq and overflow
+ * are set instead, for statistics outside a step; the scaler and counters are
+ * not touched.  A step adds its statistics to what the state holds, so such a
+ * look takes a step state of its own, of the same loss scale, or the caller
+ * zeroes both fields before the next step: left there, the sum counts twice in
+ * its norm and an overflow skips it. */
 #define ZERO_MULTI_RESET 2u
 #define ZERO_MULTI_STATISTICS 4u
 int zero_multi_unscale_norm(const zero_multi_plan_t* plan, void* d_plan, uint32_t flags,

@@ -1,5 +1,5 @@
 """Statistics of a list taken apart from its step: with other ranks' sums between
-the two, on lists of every length."""
+the two, on lists of every length, and as a look between steps."""
 import math
 
 import numpy as np
@@ -60,3 +60,26 @@ def test_a_step_with_other_ranks_sums(zf, sizes, apart, bits):
     opt.step()
     assert opt.state.read().last_skipped == 1
     assert all(np.array_equal(a, b) for a, b in zip(snapshot(opt), before))
+
+@pytest.mark.parametrize("sizes", ["spans", "tensors"])
+def test_statistics_taken_between_steps(zf, sizes):
+    """A look at the statistics takes a state of its own, or clears the step's
+    two fields afterwards: what they hold is added to the next step's."""
+    n = SHORT.get(sizes) or LONG[sizes]
+    opt, _, (_, copies) = make(zf, n, 32, torch.bfloat16, torch.bfloat16, "own", 4.0)
+    _, grads = lay_out(values(n, 9, 0.3), "own", torch.bfloat16)
+    opt.bind(grads, copies)
+    norm = math.sqrt(sum(float((g.double() / 4.0).square().sum()) for g in grads))
+    look = zf.StepState(4.0, False)
+    zf.zero_multi_unscale_norm(opt.plan, look, reset=True)
+    assert abs(look.read().sumsq - norm ** 2) <= 1e-10 * norm ** 2
+    opt.step()
+    assert abs(opt.state.read().last_norm - norm) <= 1e-10 * norm
+    zf.zero_multi_unscale_norm(opt.plan, opt.state, reset=True)
+    opt.state.field("sumsq").zero_()
+    opt.state.field("overflow").zero_()
+    opt.step()
+    assert abs(opt.state.read().last_norm - norm) <= 1e-10 * norm
+    zf.zero_multi_unscale_norm(opt.plan, opt.state, reset=True)
+    opt.step()
+    assert abs(opt.state.read().last_norm - math.sqrt(2) * norm) <= 1e-10 * norm
