@@ -61,6 +61,7 @@ def test_a_step_with_other_ranks_sums(zf, sizes, apart, bits):
     assert opt.state.read().last_skipped == 1
     assert all(np.array_equal(a, b) for a, b in zip(snapshot(opt), before))
 
+
 @pytest.mark.parametrize("sizes", ["spans", "tensors"])
 def test_statistics_taken_between_steps(zf, sizes):
     """A look at the statistics takes a state of its own, or clears the step's
