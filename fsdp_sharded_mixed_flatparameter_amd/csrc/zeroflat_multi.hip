@@ -155,6 +155,9 @@ __device__ __forceinline__ double block_sum(double x) {
 }
 
 // ---------------------------------------------------------------- step scalars
+// A bijection of 32-bit numbers whose output bits depend on every input bit; the
+// shifts and multipliers are C. Wellons' ("Prospecting for Hash Functions",
+// 2018, found by a search for the least bias).
 __device__ __forceinline__ uint32_t mix(uint32_t h) {
     h = (h ^ (h >> 16)) * 0x7FEB352Du;
     h = (h ^ (h >> 15)) * 0x846CA68Bu;
@@ -749,20 +752,29 @@ struct Tile {
 // ranges, with at most two blocks per compute unit for 32-bit states and four
 // for 8-bit ones, which have half the bytes in flight per wave (a dynamic LDS
 // reservation that the kernel does not use): both keep the addresses in flight
-// in one window of every array.  Whole steps, us, each line on one allocation:
-//                       one launch, full   slices, full   slices, 4 per CU   2 per CU
-//   2.02e8, 32-bit            991               984              991            974
-//   3e7, 32-bit               141               141              137            136
-//   2.02e8, 8-bit             569               567              572            579
-//   3e7, 8-bit                 81                81               78             87
-//   1.25e9, 8-bit            3941              3633             3609           3552
-// Slices of half and twice the size are within 2%.  A resident grid taking
+// in one window of every array.  One launch against slices (no limit), us:
+// 1.25e9 elements with 8-bit states 3941 and 3633, 2.02e8 and 3e7 within 1%.
+// Whole steps over slices, in turn on three allocations (medians, us):
+//   blocks per CU             no limit      4        3        2
+//   2.02e8, 32-bit              1004      1007     1004      982
+//   1e8, 32-bit                  487       490      484      484
+//   3e7, 32-bit                  142       139      137      137
+//   2.5e7, 32-bit                132       132      132      133
+//   2.02e8, 8-bit                572       573      565      582
+//   1e8, 8-bit                   294       290      294      307
+//   3e7, 8-bit                    81        79       81       87
+//   2.5e7, 8-bit, no copy         82.5      84       88       84
+//   1.25e9, 8-bit               3660      3648     3594     3578
+// Two for 32-bit states is the best or within 1% of it; four for 8-bit ones is
+// within 2% of the best on every line, which no other is.  Slices of half and
+// twice the size are within 2%.  A resident grid taking
 // tiles from a counter in the order its blocks ask (the flat step's form for
 // large shards) took 1008 against 1016 us on the first line's list, 613
 // against 604 on the third's and 162 against 147 on the second's (before
 // gradients were kept).
 constexpr int kSliceTiles = 131072;
-// A copy of at most this size is left in the memory-side cache (KEEP).  Steps
+// A copy of at most this size, counted in whole tiles, is left in the memory-side
+// cache (KEEP).  Steps
 // without and with, us: 3e7 elements 151 and 138 (32-bit states), 87 and 79
 // (8-bit); 1e8 503 and 445, 280 and 243; with statistics, whose kept gradients
 // compete for the cache, 518 and 486, 294 and 289, but 1.3e8 674 and 655, 379

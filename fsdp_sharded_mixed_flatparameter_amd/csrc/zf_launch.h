@@ -98,10 +98,14 @@ struct MultiEntry {
 };
 static_assert(sizeof(MultiEntry) == 64, "the table's entries are 64 bytes");
 
-// A list is short up to kMultiShortSpans spans of its statistics: its update
-// folds them itself, which takes a launch less.  Whole steps with the limit at
+// A list is short up to kMultiShortSpans spans of its statistics, of which a
+// tensor that is not empty has one at least: its update folds them itself, which
+// takes a launch less.  Whole steps with the limit at
 // 512, 1024 and 2048 spans, us: 10 tensors of 8e6 elements in all, 32-bit
 // states 52, 52, 48, 8-bit 35, 35, 33; 700 of 4e6 34, 34, 28 and 23, 23, 22.
+// Lists on either side of it: 2,000 and 2,100 tensors of 64 elements 12.1 and
+// 14.7, of 900 elements 20.9 and 24.7 (32-bit; 8-bit 12.1 and 13.9, 15.8 and
+// 19.7).
 constexpr int64_t kMultiShortSpans = 2048;
 // Rows of one wave's tile of the update.  Fewer rows shorten a wave's chain of
 // loads and arithmetic; more keep more bytes in flight per wave.  1, 2 and 4
@@ -141,7 +145,7 @@ struct MultiNormLaunch {
 int launch_multi_norm(const MultiNormLaunch& a, void* stream);
 
 struct MultiStep {
-    MultiScalars* scalars;      // where the step's scalars go; null: statistics alone
+    MultiScalars* scalars;      // where the step's scalars go
     zero_step_state_t* st;
     double lr, wd, beta1, beta2, max_norm;
     uint32_t seed;

@@ -440,7 +440,9 @@ int zero_offload_step(const void* d_grad, int32_t grad_dtype, int64_t n, float* 
  * Sections 2 and 3 work on one flat shard.  A rank that keeps its parameters
  * as tensors of their own (per-parameter shards, adapters, the unflattened
  * views of a bucket) has hundreds of them, with a learning-rate and decay
- * factor each; these entry points take the whole list in one launch per pass.
+ * factor each; these entry points take the whole list at once: the statistics
+ * in two launches, a step in two, or in three and more (over slices) where the
+ * list is long.
  *
  * State arenas: master, exp_avg and exp_avg_sq of a list are arrays of rows of
  * ZERO_ROW elements.  Tensor k takes ceil(numel_k / ZERO_ROW) consecutive
@@ -530,16 +532,20 @@ int zero_multi_unscale_norm(const zero_multi_plan_t* plan, void* d_plan, uint32_
  * The 8-bit states are then written back per row: top = min(max|x|, FLT_MAX),
  * scale = max(top * f32(1/most), 2^-126) (0 for a row of zeros), y =
  * x * (1/scale); m (most 448) is rounded to the nearest e4m3, ties to even.
- * v (most 57344) moves in a step by far less than the distance of two codes,
- * so it is rounded at random, up with the probability of the part cut off:
+ * v (most 57344) decays in a step by (1 - beta2) of itself at most and usually
+ * grows by as little, far less than the distance of two codes (14 to 25%), so it
+ * is rounded at random, up with the probability of the part cut off:
  * the 21 low bits of max(y, 2^-14)'s fp32 pattern are cut after adding 32 * r
  * (not past most), r a 16-bit number fixed by (seed, t, row, place):
  *     mix(h): h ^= h>>16; h *= 0x7FEB352D; h ^= h>>15; h *= 0x846CA68B; h ^= h>>16
  *     h = mix(mix(mix(t + seed) + row) + (place/4) * 0x9E3779B9)   (mod 2^32)
  *     k = h * 0x2C1B3C6D;  k ^= k >> 13
  *     r = the low, high half of h, low, high half of k at place%4 = 0, 1, 2, 3
- *   row counts from the arena's start.  A second moment above 0 never becomes
- *   0.  Only a step without statistics meets a gradient that is not finite:
+ *   row counts from the arena's start.  Step t of a seed has the numbers of step
+ *   t - 1 of the next seed, and lists of one seed share them row by row: give
+ *   lists that train together seeds further apart than the steps they make.  A
+ *   second moment above 0 never becomes 0: below 2^-14 of the row's scale it is
+ *   held as that (above it the rounding keeps the mean).  Only a step without statistics meets a gradient that is not finite:
  *   its parameter becomes NaN, its first moment's code NaN, its second
  *   moment's 0 (NaN) or the largest (inf), and a NaN leaves its row's scales
  *   to the other elements.
