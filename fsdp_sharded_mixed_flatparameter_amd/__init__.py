@@ -29,7 +29,9 @@ EXPORTS = ("zero_last_error", "zero_flat_layout", "zero_step_state_init",
            "zero_quant_allgather_slot", "zero_dequant_allgather", "zero_grad_accumulate_shard",
            "zero_grad_reduce_shard_int8", "zero_offload_adamw_host", "zero_offload_step",
            "zero_grad_reduce_shard_noalloc", "zero_multi_plan_init", "zero_multi_bind",
-           "zero_multi_unscale_norm", "zero_multi_adamw_step", "zero_multi_adamw_step_args")
+           "zero_multi_unscale_norm", "zero_multi_adamw_step", "zero_multi_adamw_step_args",
+           "zero_embed_lookup", "zero_embed_lookup_int8", "zero_embed_grad_workspace",
+           "zero_embed_grad")
 
 
 class zero_span_t(C.Structure):
@@ -124,6 +126,16 @@ def _load():
     L.zero_multi_adamw_step.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, u32, u32, vp, vp]
     L.zero_multi_adamw_step_args.restype = C.c_int
     L.zero_multi_adamw_step_args.argtypes = [vp, vp]
+    f32 = C.c_float
+    L.zero_embed_lookup.restype = C.c_int
+    L.zero_embed_lookup.argtypes = [vp, i32, i64, i64, vp, i32, i64, i64, f32, vp, i32, i64, vp]
+    L.zero_embed_lookup_int8.restype = C.c_int
+    L.zero_embed_lookup_int8.argtypes = [vp, i32, i64, i64, vp, vp, i32, i64, i32, i64, i64, i64, f32, vp, i32,
+                                         i64, vp]
+    L.zero_embed_grad_workspace.restype = C.c_int
+    L.zero_embed_grad_workspace.argtypes = [i64, i64, i64, vp]
+    L.zero_embed_grad.restype = C.c_int
+    L.zero_embed_grad.argtypes = [vp, i32, i64, i64, vp, vp, i32, i64, f32, vp, i32, i64, i64, u32, vp, i64, vp]
     return L
 
 
@@ -564,6 +576,8 @@ def zero_multi_adamw_step(plan, master, exp_avg, exp_avg_sq, hp, state, exp_avg_
                                       _state_ptr(state), _stream(stream)))
 
 
-from . import multi, shard  # noqa: E402
+from . import multi, shard, unit  # noqa: E402
 from .multi import MultiPlan, TensorListOptimizer  # noqa: E402,F401
 from .shard import MultiShardOptimizer, OffloadShardOptimizer, ShardOptimizer  # noqa: E402,F401
+from .unit import (ZERO_ACCUMULATE, zero_embed_grad, zero_embed_grad_workspace,  # noqa: E402,F401
+                   zero_embed_lookup, zero_embed_lookup_int8)

@@ -797,4 +797,149 @@ int zero_multi_adamw_step_args(const zero_multi_step_args_t* args, void* stream)
                                  args->seed, args->flags, args->d_state, stream);
 }
 
+// ---------------------------------------------------------------------------
+// 10. Embedding rows and their gradient.
+namespace {
+constexpr int64_t kEmbedMaxTokens = (int64_t)1 << 28, kEmbedMaxVocab = (int64_t)1 << 25;
+constexpr int64_t kMaxCols = (int64_t)1 << 24;
+
+int check_tokens(const char* fn, const void* tokens, int32_t token_bytes, int64_t n_tokens, int64_t first,
+                 int64_t vocab, int64_t dim) {
+    if (token_bytes != 4 && token_bytes != 8)
+        return fail(ZERO_EINVAL, "%s: token_bytes must be 4 or 8", fn);
+    if (n_tokens < 0 || first < 0 || vocab < 0 || dim < 0)
+        return fail(ZERO_EINVAL, "%s: negative size or first token", fn);
+    if (n_tokens > kEmbedMaxTokens || vocab > kEmbedMaxVocab || dim > kMaxCols)
+        return fail(ZERO_ERANGE, "%s: more than 2^28 tokens, 2^25 rows or 2^24 columns", fn);
+    if (n_tokens > 0 && !tokens) return fail(ZERO_EINVAL, "%s: NULL tokens", fn);
+    if (!aligned(tokens, token_bytes)) return fail(ZERO_EALIGN, "%s: tokens not aligned to their size", fn);
+    return ZERO_OK;
+}
+
+// the table's own arguments are checked by the caller
+int embed_lookup(const char* fn, zf::EmbedLookupLaunch& l, const void* tokens, int32_t token_bytes,
+                 int64_t n_tokens, int64_t first, int64_t vocab, int64_t dim, float scale, void* out,
+                 int32_t out_dtype, int64_t out_ld, void* stream) {
+    if (!valid_dtype(out_dtype)) return fail(ZERO_EINVAL, "%s: bad out_dtype %d", fn, out_dtype);
+    if (n_tokens > 1 && out_ld < dim) return fail(ZERO_EINVAL, "%s: out_ld is less than dim", fn);
+    int64_t end;
+    if (n_tokens > 1 && !mul_ok(n_tokens - 1, out_ld, &end))
+        return fail(ZERO_ERANGE, "%s: the output's size overflows", fn);
+    if (n_tokens == 0 || dim == 0) return ok();
+    if (!out) return fail(ZERO_EINVAL, "%s: NULL out", fn);
+    if (!aligned(out, esize(out_dtype))) return fail(ZERO_EALIGN, "%s: out not aligned to its element size", fn);
+    l.args.tokens = tokens;
+    l.args.wide = token_bytes == 8;
+    l.args.out = out;
+    l.args.out_ld = out_ld;
+    l.args.first = first;
+    l.args.vocab = vocab;
+    l.args.scale = scale;
+    l.n_tokens = n_tokens;
+    l.dim = dim;
+    l.out_dtype = out_dtype;
+    const int e = zf::launch_embed_lookup(l, stream);
+    if (e) return hip_fail(e, fn);
+    return ok();
+}
+}  // namespace
+
+int zero_embed_lookup(const void* tokens, int32_t token_bytes, int64_t n_tokens, int64_t first,
+                      const void* table, int32_t table_dtype, int64_t vocab, int64_t dim, float scale,
+                      void* out, int32_t out_dtype, int64_t out_ld, void* stream) {
+    const char* fn = "zero_embed_lookup";
+    if (int e = check_tokens(fn, tokens, token_bytes, n_tokens, first, vocab, dim)) return e;
+    if (!valid_dtype(table_dtype)) return fail(ZERO_EINVAL, "%s: bad table_dtype %d", fn, table_dtype);
+    if (n_tokens > 0 && vocab > 0 && dim > 0 && !table) return fail(ZERO_EINVAL, "%s: NULL table", fn);
+    if (!aligned(table, esize(table_dtype)))
+        return fail(ZERO_EALIGN, "%s: table not aligned to its element size", fn);
+    zf::EmbedLookupLaunch l;
+    memset(&l, 0, sizeof l);
+    l.args.table = table;
+    l.table_dtype = table_dtype;
+    return embed_lookup(fn, l, tokens, token_bytes, n_tokens, first, vocab, dim, scale, out, out_dtype, out_ld,
+                        stream);
+}
+
+int zero_embed_lookup_int8(const void* tokens, int32_t token_bytes, int64_t n_tokens, int64_t first,
+                           const int8_t* q_buf, const float* q_scales, int32_t n_slots,
+                           int64_t slot_numel, int32_t block, int64_t elem_offset, int64_t vocab,
+                           int64_t dim, float scale, void* out, int32_t out_dtype, int64_t out_ld,
+                           void* stream) {
+    const char* fn = "zero_embed_lookup_int8";
+    if (int e = check_tokens(fn, tokens, token_bytes, n_tokens, first, vocab, dim)) return e;
+    if (block != 256) return fail(ZERO_EINVAL, "%s: block must be 256", fn);
+    if (n_slots < 1 || n_slots > 65536) return fail(ZERO_ERANGE, "%s: n_slots out of range", fn);
+    if (slot_numel < 0 || elem_offset < 0) return fail(ZERO_EINVAL, "%s: negative slot size or offset", fn);
+    int64_t held, need;
+    if (!mul_ok(slot_numel, n_slots, &held) || !add_ok(vocab * dim, elem_offset, &need))
+        return fail(ZERO_ERANGE, "%s: the payload's size overflows", fn);
+    if (need > held) return fail(ZERO_EINVAL, "%s: the table exceeds the payload's slots", fn);
+    if (n_tokens > 0 && vocab > 0 && dim > 0 && (!q_buf || !q_scales))
+        return fail(ZERO_EINVAL, "%s: NULL payload", fn);
+    if (!aligned(q_scales, 4)) return fail(ZERO_EALIGN, "%s: q_scales not 4-byte aligned", fn);
+    zf::EmbedLookupLaunch l;
+    memset(&l, 0, sizeof l);
+    l.args.table = q_buf;
+    l.args.scales = q_scales;
+    l.args.elem_offset = elem_offset;
+    l.args.slot_numel = slot_numel > 0 ? slot_numel : 1;
+    l.args.slot_blocks = slot_numel / block + (slot_numel % block ? 1 : 0);
+    l.table_dtype = zf::kEmbedInt8;
+    return embed_lookup(fn, l, tokens, token_bytes, n_tokens, first, vocab, dim, scale, out, out_dtype, out_ld,
+                        stream);
+}
+
+int zero_embed_grad_workspace(int64_t n_tokens, int64_t vocab, int64_t dim, int64_t* bytes) {
+    const char* fn = "zero_embed_grad_workspace";
+    if (!bytes) return fail(ZERO_EINVAL, "%s: NULL bytes", fn);
+    if (int e = check_tokens(fn, &fn, 8, n_tokens, 0, vocab, dim)) return e;
+    *bytes = zf::embed_workspace(n_tokens, vocab, dim).bytes;
+    return ok();
+}
+
+int zero_embed_grad(const void* tokens, int32_t token_bytes, int64_t n_tokens, int64_t first,
+                    const int64_t* padding, const void* dy, int32_t dy_dtype, int64_t dy_ld, float scale,
+                    void* grad, int32_t grad_dtype, int64_t vocab, int64_t dim, uint32_t flags,
+                    void* workspace, int64_t workspace_bytes, void* stream) {
+    const char* fn = "zero_embed_grad";
+    if (int e = check_tokens(fn, tokens, token_bytes, n_tokens, first, vocab, dim)) return e;
+    if (!valid_dtype(dy_dtype) || !valid_dtype(grad_dtype))
+        return fail(ZERO_EINVAL, "%s: bad dy_dtype %d or grad_dtype %d", fn, dy_dtype, grad_dtype);
+    if (flags & ~ZERO_ACCUMULATE) return fail(ZERO_EINVAL, "%s: unknown flags", fn);
+    if (dy_ld < 0) return fail(ZERO_EINVAL, "%s: negative dy_ld", fn);
+    int64_t end;
+    if (!mul_ok(n_tokens, dy_ld, &end)) return fail(ZERO_ERANGE, "%s: dy's size overflows", fn);
+    const bool accumulate = flags & ZERO_ACCUMULATE;
+    if (vocab == 0 || dim == 0 || (n_tokens == 0 && accumulate)) return ok();
+    if (!grad || (n_tokens > 0 && !dy)) return fail(ZERO_EINVAL, "%s: NULL dy or grad", fn);
+    if (!aligned(dy, esize(dy_dtype)) || !aligned(grad, esize(grad_dtype)))
+        return fail(ZERO_EALIGN, "%s: dy or grad not aligned to its element size", fn);
+    const zf::EmbedWorkspace w = zf::embed_workspace(n_tokens, vocab, dim);
+    if (!workspace || workspace_bytes < w.bytes)
+        return fail(ZERO_EINVAL, "%s: the workspace needs %lld bytes", fn, (long long)w.bytes);
+    if (!aligned(workspace, 16)) return fail(ZERO_EALIGN, "%s: workspace not 16-byte aligned", fn);
+    zf::EmbedGradLaunch l;
+    memset(&l, 0, sizeof l);
+    l.sort.tokens = tokens;
+    l.sort.n_tokens = n_tokens;
+    l.sort.first = first;
+    l.sort.padding = padding ? *padding : 0;
+    l.sort.has_padding = padding != nullptr;
+    l.sort.vocab = vocab;
+    l.sort.wide = token_bytes == 8;
+    l.sum.dy = dy;
+    l.sum.grad = grad;
+    l.sum.dim = dim;
+    l.sum.dy_ld = dy_ld;
+    l.sum.accumulate = accumulate;
+    l.sum.scale = scale;
+    l.workspace = workspace;
+    l.dy_dtype = dy_dtype;
+    l.grad_dtype = grad_dtype;
+    const int e = zf::launch_embed_grad(l, stream);
+    if (e) return hip_fail(e, fn);
+    return ok();
+}
+
 }  // extern "C"

@@ -1,0 +1,549 @@
+// zeroflat_embed.hip -- gfx950 (MI355X, CDNA4, wave64) kernels of the embedding:
+//   embed_lookup_kernel   rows of the table by token, scaled; the table a view
+//                         of the flat parameter, or the gathered INT8 payload
+//   embed_sort_kernel, embed_hist_kernel, embed_scan_kernel,
+//   embed_scatter_kernel  the tokens' positions sorted by token, stable
+//   embed_sum_kernel      the gradient's rows summed over runs of equal tokens
+//   embed_join_kernel     the runs that cross tiles
+//
+// The gradient of row v is the sum of dy's rows at the tokens equal to v.  Added
+// by atomics its roundings would depend on the order of arrival, and a frequent
+// token's row would be one address for the whole chip.  Sorted, the positions
+// are cut into tiles of one length whatever the tokens are, so that every wave
+// has the same work; a run inside a tile is summed in registers and written
+// once, and one that crosses tiles leaves an fp32 partial row per tile, which
+// the join adds in order.  Every sum's order is fixed by the tokens alone.
+#include "zf_vec.h"
+
+namespace zf {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWaves = kThreads / 64;
+constexpr int kBins = 256;             // digits of up to 8 bits
+constexpr int kRounds = kEmbedSortTile / kThreads;
+constexpr int kChunk = 512;            // columns of one wave: eight per lane
+
+#define ZF_CONST __attribute__((address_space(4)))
+// Read-only while the kernel runs: wave-uniform reads stay scalar.
+template <typename T>
+__device__ __forceinline__ const ZF_CONST T* as_const(const T* p) {
+    return (const ZF_CONST T*)(uintptr_t)p;
+}
+
+__device__ __forceinline__ int64_t token_at(const void* tokens, int wide, int64_t i) {
+    return wide ? static_cast<const int64_t*>(tokens)[i] : (int64_t)static_cast<const int32_t*>(tokens)[i];
+}
+// The token's row of the table, or `vocab` if it has none here.
+__device__ __forceinline__ uint32_t row_of(int64_t token, int64_t first, uint32_t vocab) {
+    return token >= first && (uint64_t)(token - first) < vocab ? (uint32_t)(token - first) : vocab;
+}
+
+// ---------------------------------------------------------------- lookup
+// One group of eight columns of one token's row per lane.  Bound by memory: the
+// row and the output, once each.
+template <int TT, int TO>
+__global__ __launch_bounds__(kThreads) void embed_lookup_kernel(EmbedLookup a) {
+    const uint32_t g = blockIdx.x * kThreads + threadIdx.x;
+    if (g >= a.groups) return;
+    const uint32_t t = div_by(g, a.per_row);
+    const uint32_t col = (g - t * a.per_row.d) * 8;
+    const int n = (int)min((uint32_t)8, (uint32_t)a.dim - col);
+    const uint32_t row = row_of(token_at(a.tokens, a.wide, t), a.first, (uint32_t)a.vocab);
+    float x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    if (row < (uint32_t)a.vocab) {
+        const int64_t at = (int64_t)row * a.dim + col;
+        if constexpr (TT != kEmbedInt8) {
+            load8<TT>(a.table, at, n, x);
+        } else {
+            // element `at` of the table is code at + elem_offset of the payload:
+            // slot s, place i within it, block i / 256 of the slot's scales
+            const int8_t* q = static_cast<const int8_t*>(a.table);
+            int64_t e = at + a.elem_offset;
+            const int64_t s = e / a.slot_numel, i = e - s * a.slot_numel;
+            const float* sc = a.scales + s * a.slot_blocks;
+            if (n >= 8 && i + 8 <= a.slot_numel) {
+                const v2u c = *reinterpret_cast<const v2u_any*>(q + e);
+                const int64_t b = i >> 8;
+                const int left = 256 - (int)(i & 255);
+                const float s0 = sc[b], s1 = left < 8 ? sc[b + 1] : s0;
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    x[k] = (float)(int8_t)(c[k / 4] >> (8 * (k % 4))) * (k < left ? s0 : s1);
+            } else {
+                for (int k = 0; k < n; ++k, ++e) {
+                    const int64_t sk = e / a.slot_numel;
+                    x[k] = (float)q[e] * a.scales[sk * a.slot_blocks + ((e - sk * a.slot_numel) >> 8)];
+                }
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[k] *= a.scale;
+    }
+    store8<TO>(a.out, (int64_t)t * a.out_ld + col, n, x);
+}
+
+// ---------------------------------------------------------------- sort
+// Exclusive sum over the block's threads of 64-lane waves, in thread order.
+template <int WAVES>
+__device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t* lds, uint32_t* total) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    uint32_t s = x;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+        const uint32_t o = __shfl_up(s, d);
+        if (lane >= d) s += o;
+    }
+    if (lane == 63) lds[wave] = s;
+    __syncthreads();
+    uint32_t before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) {
+        const uint32_t v = lds[w];
+        if (w < wave) before += v;
+        all += v;
+    }
+    __syncthreads();
+    *total = all;
+    return before + s - x;
+}
+
+// The lanes of the wave that hold the same digit as this one.
+__device__ __forceinline__ uint64_t same_digit(uint32_t d, int bits, bool live) {
+    uint64_t m = __ballot(live);
+    for (int b = 0; b < bits; ++b) {
+        const uint64_t v = __ballot((d >> b) & 1);
+        m &= (d >> b) & 1 ? v : ~v;
+    }
+    return m;
+}
+
+__device__ __forceinline__ uint32_t key_at(const EmbedSort& a, int64_t i) {
+    const int64_t token = token_at(a.tokens, a.wide, i);
+    return token == a.padding && a.has_padding ? (uint32_t)a.vocab : row_of(token, a.first, (uint32_t)a.vocab);
+}
+
+// The whole sort in one block's LDS: up to kEmbedSmall tokens, four per thread,
+// in as many stable passes as the vocabulary's digits need.  Item r * 64 + lane
+// of wave w's 256 keeps the order of the input.
+__global__ __launch_bounds__(1024) void embed_sort_kernel(EmbedSort a) {
+    constexpr int kW = 16, kR = kEmbedSmall / 1024;
+    __shared__ uint32_t keys[kEmbedSmall];
+    __shared__ uint16_t places[kEmbedSmall];
+    __shared__ uint32_t count[kW][kBins];
+    __shared__ uint32_t sums[kW];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int n = (int)a.n_tokens;
+    if (a.flags)
+        for (int i = threadIdx.x; i < a.flag_words; i += 1024) a.flags[i] = 0;
+    uint32_t key[kR], place[kR], rank[kR];
+#pragma unroll
+    for (int r = 0; r < kR; ++r) {
+        place[r] = wave * 64 * kR + r * 64 + lane;
+        key[r] = (int)place[r] < n ? key_at(a, place[r]) : (uint32_t)a.vocab;
+    }
+    __syncthreads();
+    if (a.flags) {
+#pragma unroll
+        for (int r = 0; r < kR; ++r)
+            if (key[r] < (uint32_t)a.vocab) reinterpret_cast<uint8_t*>(a.flags)[key[r]] = 1;
+    }
+    for (int p = 0; p < a.passes; ++p) {
+        for (int i = threadIdx.x; i < kW * kBins; i += 1024) (&count[0][0])[i] = 0;
+        __syncthreads();
+        const uint32_t mask = (1u << a.digit_bits) - 1, shift = p * a.digit_bits;
+#pragma unroll
+        for (int r = 0; r < kR; ++r) {
+            const bool live = (int)(wave * 64 * kR + r * 64 + lane) < n;
+            const uint32_t d = (key[r] >> shift) & mask;
+            const uint64_t m = same_digit(d, a.digit_bits, live);
+            const int below = __popcll(m & ((1ull << lane) - 1));
+            const uint32_t had = live ? count[wave][d] : 0;
+            rank[r] = had + below;
+            __syncthreads();
+            if (live && below == 0) count[wave][d] = had + __popcll(m);
+            __syncthreads();
+        }
+        // digits' totals, then each wave's first place of each digit
+        uint32_t mine = 0, all;
+        if (threadIdx.x < kBins)
+            for (int w = 0; w < kW; ++w) mine += count[w][threadIdx.x];
+        uint32_t at = block_scan<kW>(mine, sums, &all);
+        if (threadIdx.x < kBins)
+            for (int w = 0; w < kW; ++w) {
+                const uint32_t c = count[w][threadIdx.x];
+                count[w][threadIdx.x] = at;
+                at += c;
+            }
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < kR; ++r) {
+            if ((int)(wave * 64 * kR + r * 64 + lane) < n) {
+                const uint32_t to = count[wave][(key[r] >> shift) & mask] + rank[r];
+                keys[to] = key[r];
+                places[to] = (uint16_t)place[r];
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < kR; ++r) {
+            const int i = wave * 64 * kR + r * 64 + lane;
+            if (i < n) {
+                key[r] = keys[i];
+                place[r] = places[i];
+            }
+        }
+        __syncthreads();
+    }
+#pragma unroll
+    for (int r = 0; r < kR; ++r) {
+        const int i = wave * 64 * kR + r * 64 + lane;
+        if (i < n) {
+            a.keys_out[i] = key[r];
+            a.places_out[i] = (int32_t)place[r];
+        }
+    }
+}
+
+// One pass over a long list, first half: how many of each digit a block of
+// kEmbedSortTile items holds.  The first pass reads the tokens and clears the
+// rows' marks.
+__global__ __launch_bounds__(kThreads) void embed_hist_kernel(EmbedSort a) {
+    __shared__ uint32_t count[kBins];
+    count[threadIdx.x] = 0;
+    if (a.pass == 0 && a.flags)
+        for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < a.flag_words;
+             i += (int64_t)gridDim.x * kThreads)
+            a.flags[i] = 0;
+    __syncthreads();
+    const uint32_t mask = (1u << a.digit_bits) - 1, shift = a.pass * a.digit_bits;
+#pragma unroll
+    for (int r = 0; r < kRounds; ++r) {
+        const int64_t i = (int64_t)blockIdx.x * kEmbedSortTile + r * kThreads + threadIdx.x;
+        if (i < a.n_tokens) {
+            const uint32_t key = a.pass == 0 ? key_at(a, i) : a.keys_in[i];
+            atomicAdd(&count[(key >> shift) & mask], 1u);      // counts: any order gives the same
+        }
+    }
+    __syncthreads();
+    a.hist[(int64_t)blockIdx.x * kBins + threadIdx.x] = count[threadIdx.x];
+}
+
+// Lists of more than kEmbedScanBlocks blocks: each digit's counts summed over
+// the blocks before, one block per digit, totals behind the table.
+__global__ __launch_bounds__(kThreads) void embed_scan_kernel(EmbedSort a) {
+    __shared__ uint32_t sums[kWaves];
+    const int d = blockIdx.x;
+    uint32_t base = 0;
+    for (int b0 = 0; b0 < a.blocks; b0 += kThreads) {
+        const int b = b0 + (int)threadIdx.x;
+        uint32_t all;
+        const uint32_t c = b < a.blocks ? a.hist[(int64_t)b * kBins + d] : 0;
+        const uint32_t at = block_scan<kWaves>(c, sums, &all);
+        if (b < a.blocks) a.hist[(int64_t)b * kBins + d] = base + at;
+        base += all;
+    }
+    if (threadIdx.x == 0) a.hist[(int64_t)a.blocks * kBins + d] = base;
+}
+
+// Second half of a pass: every item to its place.  Up to kEmbedScanBlocks
+// blocks each block sums the table itself, which saves the launch between.
+__global__ __launch_bounds__(kThreads) void embed_scatter_kernel(EmbedSort a) {
+    __shared__ uint32_t count[kWaves][kBins];
+    __shared__ uint32_t sums[kWaves];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    uint32_t before = 0, total = 0;
+    if (a.scanned) {
+        before = a.hist[(int64_t)blockIdx.x * kBins + threadIdx.x];
+        total = a.hist[(int64_t)a.blocks * kBins + threadIdx.x];
+    } else {
+#pragma unroll 8
+        for (int b = 0; b < a.blocks; ++b) {
+            const uint32_t c = a.hist[(int64_t)b * kBins + threadIdx.x];
+            total += c;
+            if (b < (int)blockIdx.x) before += c;
+        }
+    }
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) count[w][threadIdx.x] = 0;
+    uint32_t all;
+    const uint32_t base = before + block_scan<kWaves>(total, sums, &all);
+    const uint32_t mask = (1u << a.digit_bits) - 1, shift = a.pass * a.digit_bits;
+    uint32_t key[kRounds], place[kRounds], rank[kRounds];
+    const int64_t first = (int64_t)blockIdx.x * kEmbedSortTile + wave * 64 * kRounds + lane;
+#pragma unroll
+    for (int r = 0; r < kRounds; ++r) {
+        const int64_t i = first + r * 64;
+        const bool live = i < a.n_tokens;
+        key[r] = !live ? 0 : a.pass == 0 ? key_at(a, i) : a.keys_in[i];
+        place[r] = !live ? 0 : a.pass == 0 ? (uint32_t)i : (uint32_t)a.places_in[i];
+        if (a.pass == 0 && a.flags && live && key[r] < (uint32_t)a.vocab)
+            reinterpret_cast<uint8_t*>(a.flags)[key[r]] = 1;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < kRounds; ++r) {
+        const bool live = first + r * 64 < a.n_tokens;
+        const uint32_t d = (key[r] >> shift) & mask;
+        const uint64_t m = same_digit(d, a.digit_bits, live);
+        const int below = __popcll(m & ((1ull << lane) - 1));
+        const uint32_t had = live ? count[wave][d] : 0;
+        rank[r] = had + below;
+        __syncthreads();
+        if (live && below == 0) count[wave][d] = had + __popcll(m);
+        __syncthreads();
+    }
+    uint32_t at = base;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+        const uint32_t c = count[w][threadIdx.x];
+        count[w][threadIdx.x] = at;
+        at += c;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < kRounds; ++r) {
+        if (first + r * 64 < a.n_tokens) {
+            const uint32_t to = count[wave][(key[r] >> shift) & mask] + rank[r];
+            a.keys_out[to] = key[r];
+            a.places_out[to] = (int32_t)place[r];
+        }
+    }
+}
+
+// ---------------------------------------------------------------- sums
+template <int TG>
+__device__ __forceinline__ void write_row(const EmbedSum& a, uint32_t row, int64_t col, int n,
+                                          float (&acc)[8]) {
+    const int64_t at = (int64_t)row * a.dim + col;
+    float y[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) y[k] = acc[k] * a.scale;
+    if (a.accumulate) {
+        float old[8];
+        load8<TG>(a.grad, at, n, old);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) y[k] += old[k];
+    }
+    store8<TG>(a.grad, at, n, y);
+}
+
+// A wave takes a tile of a.tile sorted positions and 512 columns; the waves
+// behind them write zeros to the rows that no token names.
+template <int TD, int TG>
+__global__ __launch_bounds__(kThreads) void embed_sum_kernel(EmbedSum a) {
+    const int lane = threadIdx.x & 63;
+    const int64_t unit = (int64_t)blockIdx.x * kWaves + uniform(threadIdx.x >> 6);
+    if (unit >= a.sum_units) {
+        const int64_t v = unit - a.sum_units;
+        if (v >= a.zero_rows || as_const(reinterpret_cast<const uint8_t*>(a.flags))[v]) return;
+        const float zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        for (int64_t col = lane * 8; col < a.dim; col += kChunk)
+            store8<TG>(a.grad, v * a.dim + col, (int)min((int64_t)8, a.dim - col), zero);
+        return;
+    }
+    const int64_t tile = unit / a.chunks;
+    const int64_t col = (unit - tile * a.chunks) * kChunk + lane * 8;
+    const int n = (int)min((int64_t)8, a.dim - col);       // <= 0: the lane has no columns
+    const int64_t base = tile * a.tile;
+    const int len = (int)min((int64_t)a.tile, a.n_tokens - base);
+    const auto* keys = as_const(a.keys) + base;
+    const auto* places = as_const(a.places) + base;
+    const uint32_t none = (uint32_t)a.vocab;
+    uint32_t cur = keys[0];
+    if (cur == none) return;
+    bool before = tile > 0 && keys[-1] == cur;             // the run began in an earlier tile
+    const uint32_t after = base + len < a.n_tokens ? keys[len] : none;
+    float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    auto partial = [&](int which) {
+        if (n > 0) {
+            float* p = a.partials + (tile * 2 + which) * a.pitch + col;
+            *reinterpret_cast<v4f*>(p) = v4f{acc[0], acc[1], acc[2], acc[3]};
+            *reinterpret_cast<v4f*>(p + 4) = v4f{acc[4], acc[5], acc[6], acc[7]};
+        }
+    };
+    for (int j0 = 0; j0 < len; j0 += kEmbedBatch) {
+        float x[kEmbedBatch][8];
+#pragma unroll
+        for (int j = 0; j < kEmbedBatch; ++j) {
+            const bool live = j0 + j < len && keys[j0 + j] != none;
+            if (live && n > 0) load8<TD>(a.dy, (int64_t)places[j0 + j] * a.dy_ld + col, n, x[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < kEmbedBatch; ++j) {
+            if (j0 + j < len && cur != none) {
+                const uint32_t k = keys[j0 + j];
+                if (k != cur) {
+                    if (before) partial(0);
+                    else if (n > 0) write_row<TG>(a, cur, col, n, acc);
+                    before = false;
+                    cur = k;
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) acc[c] = 0.0f;
+                }
+                if (cur != none) {
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) acc[c] += x[j][c];
+                }
+            }
+        }
+    }
+    if (cur == none) return;
+    if (before) partial(0);
+    else if (after == cur) partial(1);
+    else if (n > 0) write_row<TG>(a, cur, col, n, acc);
+}
+
+// The block of tile t and 512 columns, if a run begins in t and ends in a later
+// tile e: tail of t + heads of t+1 .. e.  Its waves take equal shares of the
+// tiles, and the shares are added in order.
+template <int TG>
+__global__ __launch_bounds__(kThreads) void embed_join_kernel(EmbedSum a) {
+    __shared__ float part[kWaves][kChunk];
+    const int64_t tile = blockIdx.x;
+    const int64_t base = tile * a.tile;
+    const auto* keys = as_const(a.keys);
+    const uint32_t k = keys[base + a.tile - 1];            // every tile but the last is full
+    if (k == (uint32_t)a.vocab || keys[base + a.tile] != k) return;
+    if (tile > 0 && keys[base] == k && keys[base - 1] == k) return;
+    int64_t lo = tile + 1, hi = a.tiles - 1;               // the last tile whose first key is k
+    while (lo < hi) {
+        const int64_t mid = (lo + hi + 1) / 2;
+        if (keys[mid * a.tile] == k) lo = mid;
+        else hi = mid - 1;
+    }
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+    const int64_t col = (int64_t)blockIdx.y * kChunk + lane * 8;
+    const int n = (int)min((int64_t)8, a.dim - col);
+    const int64_t many = lo - tile + 1, share = (many + kWaves - 1) / kWaves;
+    const int64_t from = min(many, wave * share), to = min(many, from + share);
+    float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    if (n > 0) {
+#pragma unroll 4
+        for (int64_t j = from; j < to; ++j) {
+            const float* p = a.partials + ((tile + j) * 2 + (j == 0)) * a.pitch + col;
+            const v4f x = *reinterpret_cast<const v4f*>(p), y = *reinterpret_cast<const v4f*>(p + 4);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) { acc[c] += x[c]; acc[4 + c] += y[c]; }
+        }
+    }
+    *reinterpret_cast<v4f*>(&part[wave][lane * 8]) = v4f{acc[0], acc[1], acc[2], acc[3]};
+    *reinterpret_cast<v4f*>(&part[wave][lane * 8 + 4]) = v4f{acc[4], acc[5], acc[6], acc[7]};
+    __syncthreads();
+    if (wave || n <= 0) return;
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w)
+#pragma unroll
+        for (int c = 0; c < 8; ++c) acc[c] += part[w][lane * 8 + c];
+    write_row<TG>(a, k, col, n, acc);
+}
+
+int last_error() { return (int)hipGetLastError(); }
+
+template <int TT>
+void lookup_to(const EmbedLookup& a, int out, dim3 grid, hipStream_t s) {
+    if (out == ZERO_F32) embed_lookup_kernel<TT, ZERO_F32><<<grid, kThreads, 0, s>>>(a);
+    else if (out == ZERO_F16) embed_lookup_kernel<TT, ZERO_F16><<<grid, kThreads, 0, s>>>(a);
+    else embed_lookup_kernel<TT, ZERO_BF16><<<grid, kThreads, 0, s>>>(a);
+}
+
+template <int TD>
+void sum_to(const EmbedSum& a, int grad, dim3 grid, hipStream_t s) {
+    if (grad == ZERO_F32) embed_sum_kernel<TD, ZERO_F32><<<grid, kThreads, 0, s>>>(a);
+    else if (grad == ZERO_F16) embed_sum_kernel<TD, ZERO_F16><<<grid, kThreads, 0, s>>>(a);
+    else embed_sum_kernel<TD, ZERO_BF16><<<grid, kThreads, 0, s>>>(a);
+}
+
+}  // namespace
+
+int launch_embed_lookup(const EmbedLookupLaunch& l, void* stream) {
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    const int64_t per_row = (l.dim + 7) / 8;
+    // groups are counted in 31 bits: more tokens than that take several launches
+    const int64_t most = ((int64_t)1 << 30) / per_row;
+    EmbedLookup a = l.args;
+    a.dim = l.dim;
+    a.per_row = make_div((uint32_t)per_row);
+    for (int64_t t = 0; t < l.n_tokens; t += most) {
+        const int64_t n = l.n_tokens - t < most ? l.n_tokens - t : most;
+        a.tokens = static_cast<const char*>(l.args.tokens) + t * (a.wide ? 8 : 4);
+        a.out = static_cast<char*>(l.args.out) + t * a.out_ld * (l.out_dtype == ZERO_F32 ? 4 : 2);
+        a.groups = (uint32_t)(n * per_row);
+        const dim3 grid((a.groups + kThreads - 1) / kThreads);
+        if (l.table_dtype == kEmbedInt8) lookup_to<kEmbedInt8>(a, l.out_dtype, grid, s);
+        else if (l.table_dtype == ZERO_F32) lookup_to<ZERO_F32>(a, l.out_dtype, grid, s);
+        else if (l.table_dtype == ZERO_F16) lookup_to<ZERO_F16>(a, l.out_dtype, grid, s);
+        else lookup_to<ZERO_BF16>(a, l.out_dtype, grid, s);
+        if (const int e = last_error()) return e;
+    }
+    return 0;
+}
+
+int launch_embed_grad(const EmbedGradLaunch& l, void* stream) {
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    char* ws = static_cast<char*>(l.workspace);
+    EmbedSort a = l.sort;
+    const EmbedWorkspace w = embed_workspace(a.n_tokens, a.vocab, l.sum.dim);
+    uint32_t* keys[2] = {reinterpret_cast<uint32_t*>(ws + w.keys[0]), reinterpret_cast<uint32_t*>(ws + w.keys[1])};
+    int32_t* places[2] = {reinterpret_cast<int32_t*>(ws + w.places[0]), reinterpret_cast<int32_t*>(ws + w.places[1])};
+    a.flags = l.sum.accumulate ? nullptr : reinterpret_cast<uint32_t*>(ws + w.flags);
+    a.flag_words = (a.vocab + 3) / 4;
+    a.hist = reinterpret_cast<uint32_t*>(ws + w.hist);
+    int bits = 1;
+    while ((a.vocab >> bits) != 0) ++bits;                 // keys are 0 .. vocab
+    a.passes = (bits + 7) / 8;
+    a.digit_bits = (bits + a.passes - 1) / a.passes;
+    a.blocks = (int32_t)((a.n_tokens + kEmbedSortTile - 1) / kEmbedSortTile);
+    a.scanned = a.blocks > kEmbedScanBlocks;
+    int at = 0;
+    if (a.n_tokens <= kEmbedSmall) {
+        a.keys_out = keys[0];
+        a.places_out = places[0];
+        embed_sort_kernel<<<1, 1024, 0, s>>>(a);
+        if (const int e = last_error()) return e;
+    } else {
+        for (a.pass = 0; a.pass < a.passes; ++a.pass) {
+            a.keys_in = keys[at];
+            a.places_in = places[at];
+            at ^= 1;
+            a.keys_out = keys[at];
+            a.places_out = places[at];
+            embed_hist_kernel<<<a.blocks, kThreads, 0, s>>>(a);
+            if (const int e = last_error()) return e;
+            if (a.scanned) {
+                embed_scan_kernel<<<kBins, kThreads, 0, s>>>(a);
+                if (const int e = last_error()) return e;
+            }
+            embed_scatter_kernel<<<a.blocks, kThreads, 0, s>>>(a);
+            if (const int e = last_error()) return e;
+        }
+    }
+    EmbedSum b = l.sum;
+    b.keys = keys[at];
+    b.places = places[at];
+    b.flags = a.flags;
+    b.n_tokens = a.n_tokens;
+    b.vocab = a.vocab;
+    b.partials = reinterpret_cast<float*>(ws + w.partials);
+    b.tile = w.tile;
+    b.tiles = w.tiles;
+    b.pitch = w.pitch;
+    b.chunks = (b.dim + kChunk - 1) / kChunk;
+    b.sum_units = b.tiles * b.chunks;
+    b.zero_rows = b.accumulate ? 0 : b.vocab;
+    const dim3 grid((uint32_t)((b.sum_units + b.zero_rows + kWaves - 1) / kWaves));
+    if (l.dy_dtype == ZERO_F32) sum_to<ZERO_F32>(b, l.grad_dtype, grid, s);
+    else if (l.dy_dtype == ZERO_F16) sum_to<ZERO_F16>(b, l.grad_dtype, grid, s);
+    else sum_to<ZERO_BF16>(b, l.grad_dtype, grid, s);
+    if (const int e = last_error()) return e;
+    if (b.tiles > 1) {
+        const dim3 joins((uint32_t)(b.tiles - 1), (uint32_t)b.chunks);
+        if (l.grad_dtype == ZERO_F32) embed_join_kernel<ZERO_F32><<<joins, kThreads, 0, s>>>(b);
+        else if (l.grad_dtype == ZERO_F16) embed_join_kernel<ZERO_F16><<<joins, kThreads, 0, s>>>(b);
+        else embed_join_kernel<ZERO_BF16><<<joins, kThreads, 0, s>>>(b);
+        if (const int e = last_error()) return e;
+    }
+    return 0;
+}
+
+}  // namespace zf

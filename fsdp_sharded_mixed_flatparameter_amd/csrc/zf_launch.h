@@ -169,6 +169,100 @@ struct MultiAdamLaunch {
 int launch_multi_step(const MultiAdamLaunch& a, const MultiNormLaunch* norm, const MultiStep& step,
                       void* stream);
 
+// The embedding (zeroflat_embed.hip).
+constexpr int kEmbedInt8 = 3;            // a table's type beside zero_dtype_t: the INT8 payload
+constexpr int kEmbedSmall = 4096;        // tokens that one block sorts by itself
+constexpr int kEmbedSortTile = 1024;     // tokens of one block of the long sort
+constexpr int kEmbedScanBlocks = 128;    // blocks that sum the counts before theirs themselves
+constexpr int kEmbedBatch = 8;           // rows that a wave of the sums has in flight
+
+// n / d by a product (see zf_vec.h)
+struct Div {
+    uint32_t d, m, s;
+};
+
+struct EmbedLookup {
+    const void* tokens;
+    const void* table;      // INT8: the payload's codes
+    const float* scales;    // INT8 only, as the fields below it
+    int64_t elem_offset, slot_numel, slot_blocks;
+    void* out;
+    int64_t out_ld, first, vocab, dim;
+    Div per_row;            // groups of eight columns in a row
+    uint32_t groups;
+    int32_t wide;           // 1: 64-bit tokens
+    float scale;
+};
+struct EmbedLookupLaunch {
+    EmbedLookup args;
+    int64_t n_tokens, dim;
+    int32_t table_dtype, out_dtype;
+};
+int launch_embed_lookup(const EmbedLookupLaunch& a, void* stream);
+
+struct EmbedSort {
+    const void* tokens;
+    int64_t n_tokens, first, padding, vocab;
+    const uint32_t* keys_in;
+    const int32_t* places_in;
+    uint32_t* keys_out;
+    int32_t* places_out;
+    uint32_t* hist;
+    uint32_t* flags;        // a byte per row, 1 where a token names it; null: not asked for
+    int64_t flag_words;
+    int32_t wide, has_padding, passes, pass, digit_bits, blocks, scanned;
+};
+struct EmbedSum {
+    const uint32_t* keys;
+    const int32_t* places;
+    const uint32_t* flags;
+    const void* dy;
+    void* grad;
+    float* partials;        // two fp32 rows of `pitch` per tile: a run from before, a run that goes on
+    int64_t n_tokens, vocab, dim, dy_ld, pitch, tiles, chunks, sum_units, zero_rows;
+    int32_t tile;           // sorted positions of one tile
+    int32_t accumulate;
+    float scale;
+};
+struct EmbedGradLaunch {
+    EmbedSort sort;
+    EmbedSum sum;
+    void* workspace;
+    int32_t dy_dtype, grad_dtype;
+};
+int launch_embed_grad(const EmbedGradLaunch& a, void* stream);
+
+// The parts of its workspace, as byte offsets.
+struct EmbedWorkspace {
+    int64_t keys[2], places[2], hist, flags, partials, bytes;
+    int64_t tiles, pitch;
+    int32_t tile;
+};
+// The tile: long enough that its partial rows (fp32, two at most) are little
+// beside its rows, short enough that few tokens spread over the chip.
+inline EmbedWorkspace embed_workspace(int64_t n, int64_t vocab, int64_t dim) {
+    EmbedWorkspace w{};
+    const auto up = [](int64_t x) { return (x + 255) / 256 * 256; };
+    w.tile = n * ((dim + 511) / 512) >= 65536 ? 32 : 8;
+    w.tiles = (n + w.tile - 1) / w.tile;
+    w.pitch = (dim + 7) / 8 * 8;
+    int64_t at = 0;
+    for (int k = 0; k < 2; ++k) {
+        w.keys[k] = at;
+        at += up(n * 4);
+        w.places[k] = at;
+        at += up(n * 4);
+    }
+    w.hist = at;
+    at += up(((n + kEmbedSortTile - 1) / kEmbedSortTile + 1) * 256 * 4);
+    w.flags = at;
+    at += up(vocab);
+    w.partials = at;
+    at += up(w.tiles * 2 * w.pitch * 4);
+    w.bytes = at;
+    return w;
+}
+
 // ZeRO-Offload (zeroflat_offload.cpp).  The host update over host arrays:
 // *skipped = 1 (and nothing written) when the state says overflow.
 int offload_adam_host(const void* g, int32_t gdt, float* p, float* m, float* v, int64_t n,

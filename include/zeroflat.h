@@ -31,6 +31,9 @@
  *   9. zero_multi_unscale_norm / zero_multi_adamw_step  the statistics and the
  *                              step of 2 and 3 over a list of tensors, with
  *                              32-bit or 8-bit states.
+ *  10. zero_embed_lookup / zero_embed_grad  embedding rows from the gathered flat
+ *                              parameter (or its INT8 payload), and their
+ *                              gradient into the flat gradient.
  *
  * Sources (three web pages, cited by title and section):
  *   "DeepSpeed 与 FSDP" (docs.ifdog.com): ZeRO-1/2/3 memory arithmetic,
@@ -573,6 +576,55 @@ typedef struct {
     uint32_t seed, flags;
 } zero_multi_step_args_t;
 int zero_multi_adamw_step_args(const zero_multi_step_args_t* args, void* stream);
+
+/* ------------------------------------------------------------------------
+ * 10. Embedding rows and their gradient.
+ *
+ * What the first unit of a model does with the gathered flat parameter and
+ * what it gives back to the flat gradient.  A table of `vocab` rows of `dim`
+ * elements lies contiguously in the flat parameter; it holds the tokens first
+ * .. first + vocab - 1 (a rank that keeps some of the vocabulary's rows has
+ * first > 0), and any other token is one that this table has no row for.
+ * tokens: DEVICE int32 or int64 (token_bytes 4 or 8)[n_tokens].
+ *
+ * Lookup:  out[t*out_ld + c] = round_out_dtype( f32(table[(tokens[t]-first)*dim + c]) * scale )
+ *          and 0 for a token without a row.
+ *   zero_embed_lookup: table DEVICE fp32, fp16 or bf16 [vocab*dim].
+ *   zero_embed_lookup_int8: element j of the table is element elem_offset + j of
+ *   the payload of section 5 (n_slots slots of slot_numel codes, their block
+ *   scales; block == 256), f32(q) * scale_b in place of f32(table[.]): the rows
+ *   are read straight from the gathered slots and no table is restored.
+ * Each product is one fp32 operation; out_ld >= dim elements between rows, and
+ * out does not alias the inputs.
+ *
+ * Gradient:  S_v[c] = sum over t with tokens[t] == first + v and, where padding is
+ *                     given, tokens[t] != *padding, of f32(dy[t*dy_ld + c])
+ *   flags 0:               grad[v*dim + c] = round_grad_dtype( S_v[c] * scale ), every
+ *                          row written, those without a token with zeros;
+ *   flags ZERO_ACCUMULATE: grad[v*dim + c] = round_grad_dtype( f32(grad[v*dim + c]) +
+ *                          S_v[c] * scale ), rows without a token left as they are.
+ * The sums are fp32, in an order that the tokens alone fix: the positions are
+ * sorted by token, and no atomic adds values.  padding: HOST pointer or NULL.
+ * dy_ld >= 0 elements between rows (0: every token has the same row).
+ * workspace: DEVICE, 16-byte aligned, of the bytes that zero_embed_grad_workspace
+ *   gives (about 17 bytes per token, one per row and an fp32 row per 16 tokens), used from
+ *   the call's first kernel to its last: calls that overlap need one each.
+ * At most 2^28 tokens, 2^25 rows, 2^24 columns.
+ * ---------------------------------------------------------------------- */
+#define ZERO_ACCUMULATE 8u
+int zero_embed_lookup(const void* tokens, int32_t token_bytes, int64_t n_tokens, int64_t first,
+                      const void* table, int32_t table_dtype, int64_t vocab, int64_t dim, float scale,
+                      void* out, int32_t out_dtype, int64_t out_ld, void* stream);
+int zero_embed_lookup_int8(const void* tokens, int32_t token_bytes, int64_t n_tokens, int64_t first,
+                           const int8_t* q_buf, const float* q_scales, int32_t n_slots,
+                           int64_t slot_numel, int32_t block, int64_t elem_offset, int64_t vocab,
+                           int64_t dim, float scale, void* out, int32_t out_dtype, int64_t out_ld,
+                           void* stream);
+int zero_embed_grad_workspace(int64_t n_tokens, int64_t vocab, int64_t dim, int64_t* bytes);
+int zero_embed_grad(const void* tokens, int32_t token_bytes, int64_t n_tokens, int64_t first,
+                    const int64_t* padding, const void* dy, int32_t dy_dtype, int64_t dy_ld, float scale,
+                    void* grad, int32_t grad_dtype, int64_t vocab, int64_t dim, uint32_t flags,
+                    void* workspace, int64_t workspace_bytes, void* stream);
 #ifdef __cplusplus
 }
 #endif

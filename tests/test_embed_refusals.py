@@ -1,0 +1,149 @@
+"""What the embedding's entry points refuse before anything is launched (no GPU
+needed): the library on its arguments, and the binding on its tensors."""
+import ctypes as C
+
+import pytest
+import torch
+
+EINVAL, EALIGN, ERANGE = -1, -2, -3
+P = C.c_void_p(0x10000)         # never dereferenced: validation fails first, or nothing is to be done
+
+
+@pytest.fixture(scope="module")
+def zf():
+    import fsdp_sharded_mixed_flatparameter_amd as m
+    return m
+
+
+def at(x):
+    return C.c_void_p(x)
+
+
+def lookup(zf, tokens=P, token_bytes=8, n=4, first=0, table=P, tdt=2, vocab=10, dim=8, out=P, odt=2, ld=8):
+    return zf.lib().zero_embed_lookup(tokens, token_bytes, n, first, table, tdt, vocab, dim, 1.0, out, odt, ld, None)
+
+
+def lookup8(zf, n=4, q=P, s=P, n_slots=2, slot=40, block=256, offset=0, vocab=10, dim=8, ld=8):
+    return zf.lib().zero_embed_lookup_int8(P, 8, n, 0, q, s, n_slots, slot, block, offset, vocab, dim, 1.0, P, 2,
+                                           ld, None)
+
+
+def grad(zf, tokens=P, token_bytes=8, n=4, first=0, dy=P, ddt=2, ld=8, g=P, gdt=2, vocab=10, dim=8, flags=0, ws=P,
+         bytes_=1 << 40):
+    return zf.lib().zero_embed_grad(tokens, token_bytes, n, first, None, dy, ddt, ld, 1.0, g, gdt, vocab, dim, flags,
+                                    ws, bytes_, None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(token_bytes=2), EINVAL), (dict(n=-1), EINVAL), (dict(first=-1), EINVAL), (dict(vocab=-1), EINVAL),
+    (dict(dim=-1), EINVAL), (dict(n=(1 << 28) + 1), ERANGE), (dict(vocab=(1 << 25) + 1), ERANGE),
+    (dict(dim=(1 << 24) + 1), ERANGE), (dict(tokens=None), EINVAL), (dict(tokens=at(0x10004)), EALIGN),
+    (dict(tdt=7), EINVAL), (dict(odt=-1), EINVAL), (dict(table=None), EINVAL), (dict(table=at(0x10001)), EALIGN),
+    (dict(out=None), EINVAL), (dict(out=at(0x10002), odt=0), EALIGN), (dict(ld=7), EINVAL),
+    (dict(n=1 << 28, ld=1 << 40), ERANGE)])
+def test_lookup_refuses(zf, kw, code):
+    assert lookup(zf, **kw) == code
+    assert zf.lib().zero_last_error().decode().startswith("zero_embed_lookup: ")
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(block=128), EINVAL), (dict(n_slots=0), ERANGE), (dict(n_slots=65537), ERANGE), (dict(slot=-1), EINVAL),
+    (dict(offset=-1), EINVAL), (dict(offset=1), EINVAL), (dict(slot=39), EINVAL), (dict(slot=1 << 62), ERANGE),
+    (dict(offset=(1 << 63) - 1), ERANGE), (dict(q=None), EINVAL), (dict(s=None), EINVAL),
+    (dict(s=at(0x10002)), EALIGN), (dict(ld=7), EINVAL)])
+def test_lookup_in_the_payload_refuses(zf, kw, code):
+    assert lookup8(zf, **kw) == code
+    assert zf.lib().zero_last_error().decode().startswith("zero_embed_lookup_int8: ")
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(token_bytes=0), EINVAL), (dict(n=-1), EINVAL), (dict(tokens=None), EINVAL), (dict(ddt=3), EINVAL),
+    (dict(gdt=9), EINVAL), (dict(ld=-1), EINVAL), (dict(n=1 << 28, ld=1 << 40), ERANGE), (dict(flags=1), EINVAL),
+    (dict(dy=None), EINVAL), (dict(g=None), EINVAL), (dict(dy=at(0x10001)), EALIGN), (dict(g=at(0x10002), gdt=0), EALIGN),
+    (dict(ws=None), EINVAL), (dict(bytes_=100), EINVAL), (dict(ws=at(0x10008)), EALIGN)])
+def test_grad_refuses(zf, kw, code):
+    assert grad(zf, **kw) == code
+    assert zf.lib().zero_last_error().decode().startswith("zero_embed_grad: ")
+
+
+def test_calls_with_nothing_to_do(zf):
+    assert lookup(zf, n=0, tokens=None, table=None, out=None) == 0
+    assert lookup(zf, dim=0, table=None, out=None) == 0
+    assert lookup8(zf, n=0, q=None, s=None) == 0
+    assert grad(zf, n=0, tokens=None, dy=None, g=None, ws=None, bytes_=0, flags=8) == 0
+    assert grad(zf, vocab=0, dy=None, g=None, ws=None, bytes_=0) == 0
+    assert grad(zf, dim=0, dy=None, g=None, ws=None, bytes_=0) == 0
+
+
+def test_workspace_size(zf):
+    assert zf.zero_embed_grad_workspace(0, 0, 0) >= 0
+    # keys and places twice, a byte per row, two fp32 rows per tile
+    n, v, d = 100000, 5000, 1000
+    assert 16 * n + v + 2 * (n // 32) * d * 4 <= zf.zero_embed_grad_workspace(n, v, d) <= 18 * n + v + 2 * (n // 32 + 2) * d * 4
+    with pytest.raises(zf.ZeroError):
+        zf.zero_embed_grad_workspace(-1, 5, 5)
+    with pytest.raises(zf.ZeroError):
+        zf.zero_embed_grad_workspace(1, 1 << 26, 5)
+
+
+def test_host_tensors_are_refused(zf):
+    tok, w, y = torch.zeros(4, dtype=torch.int64), torch.zeros(10, 8), torch.zeros(4, 8)
+    with pytest.raises(ValueError, match="device"):
+        zf.zero_embed_lookup(tok, w, y)
+    with pytest.raises(ValueError, match="device"):
+        zf.zero_embed_grad(tok, y, w)
+    with pytest.raises(ValueError, match="device"):
+        zf.zero_embed_lookup_int8(tok, torch.zeros(80, dtype=torch.int8), torch.zeros(1), 1, 80, 0, 10, y)
+
+
+def test_other_types_are_refused(zf):
+    tok, w, y = torch.zeros(4), torch.zeros(10, 8), torch.zeros(4, 8)
+    with pytest.raises(ValueError, match="tokens must be int64 or int32"):
+        zf.zero_embed_lookup(tok, w, y)
+
+
+class Device:
+    """Stands for a device tensor, of which the checks ask shape, type and place only."""
+
+    def __init__(self, t, index=0, base=1 << 20):
+        self.t, self.base = t, base
+        self.device = torch.device("cuda", index)
+
+    is_cuda = True
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+    def data_ptr(self):
+        return self.base + self.t.storage_offset() * self.t.element_size()
+
+
+def test_another_device_is_refused(zf, monkeypatch):
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    with pytest.raises(ValueError, match="current device is cuda:0"):
+        zf.unit._here(Device(torch.zeros(4), index=1), "x")
+    assert zf.unit._here(Device(torch.zeros(4)), "x")
+
+
+def test_rows_and_overlaps(zf, monkeypatch):
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    u, f = zf.unit, ("float32",)
+    t = torch.zeros(6, 20)
+    assert u._rows(Device(t), "x", 6, 20, f) == 20
+    assert u._rows(Device(t[:, 3:9]), "x", 6, 6, f) == 20
+    assert u._rows(Device(t[0].expand(6, 20)), "x", 6, 20, f) == 0
+    assert u._rows(Device(t.view(2, 3, 20)), "x", 6, 20, f) == 20
+    assert u._rows(Device(t[:1, 3:9]), "x", 1, 6, f, written=True) == 6
+    assert u._rows(Device(t[:0]), "x", 0, 20, f) == 20
+    for bad, rows, cols, written in ((t, 6, 19, False), (t, 5, 20, False), (t[:, ::2], 6, 10, False),
+                                     (t.t(), 20, 6, False), (t[0].expand(6, 20), 6, 20, True),
+                                     (t.view(2, 3, 20)[:, :, :5], 6, 5, False)):
+        with pytest.raises(ValueError, match="x must"):
+            u._rows(Device(bad), "x", rows, cols, f, written)
+    u._apart(Device(t[:, :8]), Device(t[:, 8:]), "a", "b")
+    u._apart(Device(t[:, 8:]), Device(t[:, :8]), "a", "b")
+    u._apart(Device(t[:3]), Device(t[3:]), "a", "b")
+    u._apart(Device(t[:0]), Device(t), "a", "b")
+    for a, b in ((t, t), (t[:, :8], t[:, 7:]), (t[:, 7:], t[:, :8]), (t[1:, :8], t[:-1, 4:12]), (t[:4], t[3:])):
+        with pytest.raises(ValueError, match="a and b overlap"):
+            u._apart(Device(a), Device(b), "a", "b")
