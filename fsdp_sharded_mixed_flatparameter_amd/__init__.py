@@ -31,7 +31,8 @@ EXPORTS = ("zero_last_error", "zero_flat_layout", "zero_step_state_init",
            "zero_grad_reduce_shard_noalloc", "zero_multi_plan_init", "zero_multi_bind",
            "zero_multi_unscale_norm", "zero_multi_adamw_step", "zero_multi_adamw_step_args",
            "zero_embed_lookup", "zero_embed_lookup_int8", "zero_embed_grad_workspace",
-           "zero_embed_grad")
+           "zero_embed_grad", "zero_act_save8", "zero_act_restore8", "zero_act_forward8",
+           "zero_act_backward8", "zero_weight_grad8_workspace", "zero_weight_grad8")
 
 
 class zero_span_t(C.Structure):
@@ -136,6 +137,18 @@ def _load():
     L.zero_embed_grad_workspace.argtypes = [i64, i64, i64, vp]
     L.zero_embed_grad.restype = C.c_int
     L.zero_embed_grad.argtypes = [vp, i32, i64, i64, vp, vp, i32, i64, f32, vp, i32, i64, i64, u32, vp, i64, vp]
+    L.zero_act_save8.restype = C.c_int
+    L.zero_act_save8.argtypes = [vp, i32, i64, i64, i64, vp, vp, vp]
+    L.zero_act_restore8.restype = C.c_int
+    L.zero_act_restore8.argtypes = [vp, vp, i64, i64, vp, i32, i64, vp]
+    L.zero_act_forward8.restype = C.c_int
+    L.zero_act_forward8.argtypes = [i32, vp, i64, vp, i64, i32, i64, i64, vp, i64, vp, vp, vp, vp, vp]
+    L.zero_act_backward8.restype = C.c_int
+    L.zero_act_backward8.argtypes = [i32, vp, i64, i32, i64, i64, vp, vp, vp, vp, vp, i64, vp, i64, vp, vp, vp]
+    L.zero_weight_grad8_workspace.restype = C.c_int
+    L.zero_weight_grad8_workspace.argtypes = [i64, i64, i64, vp]
+    L.zero_weight_grad8.restype = C.c_int
+    L.zero_weight_grad8.argtypes = [vp, i32, i64, i64, i64, vp, vp, i64, vp, i32, u32, vp, i64, vp]
     return L
 
 
@@ -579,5 +592,7 @@ def zero_multi_adamw_step(plan, master, exp_avg, exp_avg_sq, hp, state, exp_avg_
 from . import multi, shard, unit  # noqa: E402
 from .multi import MultiPlan, TensorListOptimizer  # noqa: E402,F401
 from .shard import MultiShardOptimizer, OffloadShardOptimizer, ShardOptimizer  # noqa: E402,F401
-from .unit import (ZERO_ACCUMULATE, zero_embed_grad, zero_embed_grad_workspace,  # noqa: E402,F401
-                   zero_embed_lookup, zero_embed_lookup_int8)
+from .unit import (ZERO_ACCUMULATE, ZERO_BLOCK8, ZERO_GELU, ZERO_GELU_TANH, ZERO_SILU, Saved8,  # noqa: E402,F401
+                   zero_act_backward8, zero_act_forward8, zero_act_restore8, zero_act_save8,
+                   zero_embed_grad, zero_embed_grad_workspace, zero_embed_lookup,
+                   zero_embed_lookup_int8, zero_weight_grad8, zero_weight_grad8_workspace)

@@ -17,6 +17,8 @@ LIB = os.path.join(HERE, "libzeroflat.so")
 SOURCES = [os.path.join(HERE, "csrc", "zeroflat_kernels.hip"),
            os.path.join(HERE, "csrc", "zeroflat_multi.hip"),
            os.path.join(HERE, "csrc", "zeroflat_embed.hip"),
+           os.path.join(HERE, "csrc", "zeroflat_act.hip"),
+           os.path.join(HERE, "csrc", "zeroflat_wgrad.hip"),
            os.path.join(HERE, "csrc", "zeroflat_api.cpp")]
 # host-only C++ (the ZeRO-Offload host step): built by the host compiler, so
 # that it can carry one machine-code clone per x86 ISA level

@@ -942,4 +942,199 @@ int zero_embed_grad(const void* tokens, int32_t token_bytes, int64_t n_tokens, i
     return ok();
 }
 
+// ---------------------------------------------------------------------------
+// 11. Activations kept in 8 bits.
+namespace {
+int check_matrix(const char* fn, const char* name, const void* p, int32_t dtype, int64_t rows, int64_t cols,
+                 int64_t ld, bool written) {
+    if (!p) return fail(ZERO_EINVAL, "%s: NULL %s", fn, name);
+    if (!aligned(p, esize(dtype))) return fail(ZERO_EALIGN, "%s: %s not aligned to its element size", fn, name);
+    int64_t end;
+    if (ld < 0 || (written && rows > 1 && ld < cols))
+        return fail(ZERO_EINVAL, "%s: bad row distance of %s", fn, name);
+    if (!mul_ok(rows, ld, &end) || end > INT64_MAX / 8) return fail(ZERO_ERANGE, "%s: %s is too large", fn, name);
+    return ZERO_OK;
+}
+int check_saved(const char* fn, const char* name, const int8_t* codes, const uint8_t* exponents) {
+    if (!codes || !exponents) return fail(ZERO_EINVAL, "%s: NULL checkpoint (%s)", fn, name);
+    if (!aligned(codes, 16)) return fail(ZERO_EALIGN, "%s: codes of %s not 16-byte aligned", fn, name);
+    return ZERO_OK;
+}
+// 0: go on; 1: nothing to do; negative: an error
+int check_act(const char* fn, int32_t dtype, int64_t rows, int64_t cols) {
+    if (!valid_dtype(dtype)) return fail(ZERO_EINVAL, "%s: bad dtype %d", fn, dtype);
+    if (rows < 0 || cols < 0) return fail(ZERO_EINVAL, "%s: negative size", fn);
+    if (cols > kMaxCols || rows > (int64_t)1 << 40) return fail(ZERO_ERANGE, "%s: more than 2^40 rows or 2^24 columns", fn);
+    return rows == 0 || cols == 0 ? 1 : 0;
+}
+zf::ActLaunch act_launch(int32_t kind, int32_t dtype, int64_t rows, int64_t cols) {
+    zf::ActLaunch a;
+    memset(&a, 0, sizeof a);
+    a.rows = rows;
+    a.cols = cols;
+    a.dtype = dtype;
+    a.kind = kind;
+    a.least = dtype == ZERO_F16 ? 109 : 7;
+    return a;
+}
+int run_act(const char* fn, const zf::ActLaunch& a, int backward, void* stream) {
+    const int e = zf::launch_act(a, backward, stream);
+    if (e) return hip_fail(e, fn);
+    return ok();
+}
+bool valid_kind(int32_t k) { return k == ZERO_GELU || k == ZERO_GELU_TANH || k == ZERO_SILU; }
+}  // namespace
+
+int zero_act_save8(const void* x, int32_t dtype, int64_t rows, int64_t cols, int64_t x_ld, int8_t* codes,
+                   uint8_t* exponents, void* stream) {
+    const char* fn = "zero_act_save8";
+    if (int e = check_act(fn, dtype, rows, cols)) return e < 0 ? e : ok();
+    if (int e = check_matrix(fn, "x", x, dtype, rows, cols, x_ld, false)) return e;
+    if (int e = check_saved(fn, "x", codes, exponents)) return e;
+    zf::ActLaunch a = act_launch(-1, dtype, rows, cols);
+    a.x = x;
+    a.x_ld = x_ld;
+    a.codes = codes;
+    a.exponents = exponents;
+    return run_act(fn, a, 0, stream);
+}
+
+int zero_act_restore8(const int8_t* codes, const uint8_t* exponents, int64_t rows, int64_t cols, void* out,
+                      int32_t dtype, int64_t out_ld, void* stream) {
+    const char* fn = "zero_act_restore8";
+    if (int e = check_act(fn, dtype, rows, cols)) return e < 0 ? e : ok();
+    if (int e = check_matrix(fn, "out", out, dtype, rows, cols, out_ld, true)) return e;
+    if (int e = check_saved(fn, "x", codes, exponents)) return e;
+    zf::ActLaunch a = act_launch(-1, dtype, rows, cols);
+    a.y = out;
+    a.y_ld = out_ld;
+    a.codes = const_cast<int8_t*>(codes);
+    a.exponents = const_cast<uint8_t*>(exponents);
+    return run_act(fn, a, 1, stream);
+}
+
+int zero_act_forward8(int32_t kind, const void* x, int64_t x_ld, const void* up, int64_t up_ld, int32_t dtype,
+                      int64_t rows, int64_t cols, void* y, int64_t y_ld, int8_t* codes, uint8_t* exponents,
+                      int8_t* up_codes, uint8_t* up_exponents, void* stream) {
+    const char* fn = "zero_act_forward8";
+    if (!valid_kind(kind)) return fail(ZERO_EINVAL, "%s: bad kind %d", fn, kind);
+    if (int e = check_act(fn, dtype, rows, cols)) return e < 0 ? e : ok();
+    if (int e = check_matrix(fn, "x", x, dtype, rows, cols, x_ld, false)) return e;
+    if (int e = check_matrix(fn, "y", y, dtype, rows, cols, y_ld, true)) return e;
+    if (int e = check_saved(fn, "x", codes, exponents)) return e;
+    zf::ActLaunch a = act_launch(kind, dtype, rows, cols);
+    a.x = x;
+    a.x_ld = x_ld;
+    a.y = y;
+    a.y_ld = y_ld;
+    a.codes = codes;
+    a.exponents = exponents;
+    if (up) {
+        if (int e = check_matrix(fn, "up", up, dtype, rows, cols, up_ld, false)) return e;
+        if (int e = check_saved(fn, "up", up_codes, up_exponents)) return e;
+        a.up = up;
+        a.up_ld = up_ld;
+        a.up_codes = up_codes;
+        a.up_exponents = up_exponents;
+    } else if (up_codes || up_exponents) {
+        return fail(ZERO_EINVAL, "%s: a checkpoint of up without up", fn);
+    }
+    return run_act(fn, a, 0, stream);
+}
+
+int zero_act_backward8(int32_t kind, const void* dy, int64_t dy_ld, int32_t dtype, int64_t rows, int64_t cols,
+                       const int8_t* codes, const uint8_t* exponents, const int8_t* up_codes,
+                       const uint8_t* up_exponents, void* dx, int64_t dx_ld, void* dup, int64_t dup_ld,
+                       int8_t* again_codes, uint8_t* again_exponents, void* stream) {
+    const char* fn = "zero_act_backward8";
+    if (!valid_kind(kind)) return fail(ZERO_EINVAL, "%s: bad kind %d", fn, kind);
+    if (int e = check_act(fn, dtype, rows, cols)) return e < 0 ? e : ok();
+    if (int e = check_matrix(fn, "dy", dy, dtype, rows, cols, dy_ld, false)) return e;
+    if (int e = check_matrix(fn, "dx", dx, dtype, rows, cols, dx_ld, true)) return e;
+    if (int e = check_saved(fn, "x", codes, exponents)) return e;
+    zf::ActLaunch a = act_launch(kind, dtype, rows, cols);
+    a.x = dy;
+    a.x_ld = dy_ld;
+    a.y = dx;
+    a.y_ld = dx_ld;
+    a.codes = const_cast<int8_t*>(codes);
+    a.exponents = const_cast<uint8_t*>(exponents);
+    if (up_codes || up_exponents) {
+        if (int e = check_saved(fn, "up", up_codes, up_exponents)) return e;
+        if (int e = check_matrix(fn, "dup", dup, dtype, rows, cols, dup_ld, true)) return e;
+        a.up_codes = const_cast<int8_t*>(up_codes);
+        a.up_exponents = const_cast<uint8_t*>(up_exponents);
+        a.dup = dup;
+        a.dup_ld = dup_ld;
+    } else if (dup) {
+        return fail(ZERO_EINVAL, "%s: dup without a checkpoint of up", fn);
+    }
+    if (again_codes || again_exponents) {
+        if (int e = check_saved(fn, "act(x)", again_codes, again_exponents)) return e;
+        a.again_codes = again_codes;
+        a.again_exponents = again_exponents;
+    }
+    return run_act(fn, a, 1, stream);
+}
+
+namespace {
+int weight_plan(const char* fn, int64_t rows, int64_t outs, int64_t cols, zf::WeightGrad* a, int64_t* bytes) {
+    if (rows < 0 || outs < 0 || cols < 0) return fail(ZERO_EINVAL, "%s: negative size", fn);
+    if (rows > (int64_t)1 << 36 || outs > kMaxCols || cols > kMaxCols || outs * cols > (int64_t)1 << 38)
+        return fail(ZERO_ERANGE, "%s: more than 2^36 rows, 2^24 columns or 2^38 weights", fn);
+    memset(a, 0, sizeof *a);
+    a->rows = rows;
+    a->outs = outs;
+    a->cols = cols;
+    a->pitch = (cols + 31) / 32 * 32;
+    zf::plan_weight_grad(*a);
+    *bytes = a->splits > 1 ? a->splits * outs * cols * 4 : 0;
+    return ZERO_OK;
+}
+}  // namespace
+
+int zero_weight_grad8_workspace(int64_t rows, int64_t outs, int64_t cols, int64_t* bytes) {
+    const char* fn = "zero_weight_grad8_workspace";
+    if (!bytes) return fail(ZERO_EINVAL, "%s: NULL bytes", fn);
+    zf::WeightGrad a;
+    if (int e = weight_plan(fn, rows, outs, cols, &a, bytes)) return e;
+    return ok();
+}
+
+int zero_weight_grad8(const void* dy, int32_t dy_dtype, int64_t dy_ld, int64_t rows, int64_t outs,
+                      const int8_t* codes, const uint8_t* exponents, int64_t cols, void* grad,
+                      int32_t grad_dtype, uint32_t flags, void* workspace, int64_t workspace_bytes,
+                      void* stream) {
+    const char* fn = "zero_weight_grad8";
+    if (dy_dtype != ZERO_F16 && dy_dtype != ZERO_BF16)
+        return fail(ZERO_EINVAL, "%s: dy_dtype must be fp16 or bf16", fn);
+    if (!valid_dtype(grad_dtype)) return fail(ZERO_EINVAL, "%s: bad grad_dtype %d", fn, grad_dtype);
+    if (flags & ~ZERO_ACCUMULATE) return fail(ZERO_EINVAL, "%s: unknown flags", fn);
+    zf::WeightGrad a;
+    int64_t need;
+    if (int e = weight_plan(fn, rows, outs, cols, &a, &need)) return e;
+    const bool accumulate = flags & ZERO_ACCUMULATE;
+    if (outs == 0 || cols == 0 || (rows == 0 && accumulate)) return ok();
+    if (!grad) return fail(ZERO_EINVAL, "%s: NULL grad", fn);
+    if (!aligned(grad, esize(grad_dtype))) return fail(ZERO_EALIGN, "%s: grad not aligned to its element size", fn);
+    if (rows > 0) {
+        if (int e = check_matrix(fn, "dy", dy, dy_dtype, rows, outs, dy_ld, false)) return e;
+        if (int e = check_saved(fn, "x", codes, exponents)) return e;
+    }
+    if (need > 0 && (!workspace || workspace_bytes < need))
+        return fail(ZERO_EINVAL, "%s: the workspace needs %lld bytes", fn, (long long)need);
+    if (need > 0 && !aligned(workspace, 16)) return fail(ZERO_EALIGN, "%s: workspace not 16-byte aligned", fn);
+    a.dy = dy;
+    a.dy_ld = dy_ld;
+    a.codes = codes;
+    a.exponents = exponents;
+    a.grad = grad;
+    a.grad_dtype = grad_dtype;
+    a.accumulate = accumulate;
+    a.partials = need > 0 ? static_cast<float*>(workspace) : nullptr;
+    const int e = zf::launch_weight_grad(a, dy_dtype, stream);
+    if (e) return hip_fail(e, fn);
+    return ok();
+}
+
 }  // extern "C"

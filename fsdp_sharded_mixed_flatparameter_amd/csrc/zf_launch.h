@@ -263,6 +263,57 @@ inline EmbedWorkspace embed_workspace(int64_t n, int64_t vocab, int64_t dim) {
     return w;
 }
 
+// Activations kept in 8 bits (zeroflat_act.hip).  Forward: x, and up where it is
+// gated, into their checkpoints, y = act(x) [* up].  Backward: x is dy, y its
+// gradient of x.  kind < 0: no function, the checkpoint alone, or restored to y.
+struct ActLaunch {
+    const void* x;
+    const void* up;
+    void* y;
+    void* dup;
+    int8_t* codes;
+    uint8_t* exponents;
+    int8_t* up_codes;            // null: not gated
+    uint8_t* up_exponents;
+    int8_t* again_codes;         // backward: the checkpoint of act(x) [* up], or null
+    uint8_t* again_exponents;
+    int64_t rows, cols, x_ld, up_ld, y_ld, dup_ld;
+    Div per_row;                 // groups of eight columns in a checkpoint's row
+    uint32_t groups;
+    int32_t dtype, kind;
+    int32_t least;               // the least exponent that a checkpoint takes
+};
+int launch_act(const ActLaunch& a, int backward, void* stream);
+
+// A weight gradient (zeroflat_wgrad.hip).
+struct WeightGrad {
+    const void* dy;
+    const int8_t* codes;
+    const uint8_t* exponents;
+    void* grad;
+    float* partials;             // splits x outs x cols, or null: one split
+    int64_t rows, outs, cols, pitch, dy_ld;
+    int64_t share;               // rows of a split
+    int64_t tiles, tiles_i;
+    int32_t tile, splits, grad_dtype, accumulate;
+};
+int launch_weight_grad(const WeightGrad& a, int dtype, void* stream);
+// The tile and the split, which the sizes alone fix.
+inline void plan_weight_grad(WeightGrad& a) {
+    const auto tiles = [&](int64_t t) { return ((a.outs + t - 1) / t) * ((a.cols + t - 1) / t); };
+    a.tile = tiles(256) >= 128 ? 256 : 128;
+    a.tiles = tiles(a.tile);
+    a.tiles_i = (a.cols + a.tile - 1) / a.tile;
+    const int64_t steps = (a.rows + 63) / 64;
+    int64_t splits = 1;
+    if (a.tiles < 256) splits = 512 / (a.tiles > 0 ? a.tiles : 1);
+    if (splits > steps / 2) splits = steps / 2;
+    if (splits < 1) splits = 1;
+    a.share = (steps + splits - 1) / splits * 64;
+    a.splits = (int32_t)(a.share > 0 ? (a.rows + a.share - 1) / a.share : 1);
+    if (a.splits < 1) a.splits = 1;
+}
+
 // ZeRO-Offload (zeroflat_offload.cpp).  The host update over host arrays:
 // *skipped = 1 (and nothing written) when the state says overflow.
 int offload_adam_host(const void* g, int32_t gdt, float* p, float* m, float* v, int64_t n,

@@ -34,6 +34,9 @@
  *  10. zero_embed_lookup / zero_embed_grad  embedding rows from the gathered flat
  *                              parameter (or its INT8 payload), and their
  *                              gradient into the flat gradient.
+ *  11. zero_act_* / zero_weight_grad8  activations kept in 8 bits, the functions
+ *                              that keep and read them, and the weight gradient
+ *                              taken from them.
  *
  * Sources (three web pages, cited by title and section):
  *   "DeepSpeed 与 FSDP" (docs.ifdog.com): ZeRO-1/2/3 memory arithmetic,
@@ -625,6 +628,69 @@ int zero_embed_grad(const void* tokens, int32_t token_bytes, int64_t n_tokens, i
                     const int64_t* padding, const void* dy, int32_t dy_dtype, int64_t dy_ld, float scale,
                     void* grad, int32_t grad_dtype, int64_t vocab, int64_t dim, uint32_t flags,
                     void* workspace, int64_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * 11. Activations kept in 8 bits, and what reads them.
+ *
+ * What a unit keeps of its forward pass for its backward pass, in a byte per
+ * element.  The checkpoint of a matrix x (rows, cols) is
+ *   codes      DEVICE int8[rows*pitch], pitch = 32 * ceil(cols/32), 16-byte aligned,
+ *   exponents  DEVICE uint8[rows*pitch/32], one per block of 32 columns:
+ *     E = max( floor(log2 max|x|) + 127, E_min ),  E_min = 109 for fp16, else 7
+ *     q = clamp( rint( x * 2^(133-E) ), -127, 127 ), ties to even; 0 beyond cols
+ *   and E = 255, q = 0 for a block with an infinity or a NaN.  It stands for
+ *     x^ = q * 2^(E-133), NaN where E == 255:
+ * an overflow of the forward pass reaches the gradients and their overflow test.
+ * The exponent is a power of two (the rule of the OCP Microscaling formats for
+ * shared exponents), so that x^ is exact in fp32 and bf16, and in fp16 where that
+ * reaches it (always, for a checkpoint of fp16 values below 65,024 in magnitude).
+ *
+ * zero_act_save8:    the checkpoint of x (DEVICE dtype, x_ld elements between rows).
+ * zero_act_restore8: out = round_dtype( x^ ).
+ * zero_act_forward8: y = round_dtype( act(x) ), or act(x) * up where up is not NULL, and
+ *   the checkpoints of x and up, in one pass.
+ * zero_act_backward8: from the checkpoints, with dy the gradient of y,
+ *     dx  = round_dtype( dy * act'(x^) ),  gated: round_dtype( dy * up^ * act'(x^) )
+ *     dup = round_dtype( dy * act(x^) )    (gated only)
+ *   and where again_codes is not NULL the checkpoint of act(x^) [* up^], which the next
+ *   layer's weight gradient reads: the output itself is not kept.
+ *   kind: ZERO_GELU x P(X < x) for a normal X, ZERO_GELU_TANH its tanh form
+ *   x/2 (1 + tanh(sqrt(2/pi) (x + 0.044715 x^3))), ZERO_SILU x / (1 + e^-x); fp32.
+ * dtype (fp32, fp16 or bf16) is that of every matrix of a call.  Rows of inputs are
+ * any number of elements apart (0 repeats one), of outputs cols or more.  dx may be
+ * dy itself, y may be x or up itself, and dup dy; no other overlap of what a call
+ * writes.  cols <= 2^24.
+ *
+ * zero_weight_grad8: the gradient of a linear layer's weight (outs, cols), y = x W^T,
+ * from the checkpoint of its input:
+ *     S[o][i] = sum over t < rows of dy[t*dy_ld + o] * round_dy_dtype( x^[t][i] )
+ *   flags 0: grad = round_grad_dtype( S ); ZERO_ACCUMULATE: round_grad_dtype( f32(grad) + S ).
+ *   dy: DEVICE fp16 or bf16; grad: DEVICE fp32, fp16 or bf16 [outs*cols], contiguous, at
+ *   any element offset (a view of the flat gradient).  The products are exact and the
+ *   sums fp32, on the matrix cores, in an order that the sizes fix.  workspace: DEVICE,
+ *   16-byte aligned, of the bytes that zero_weight_grad8_workspace gives (0 where the
+ *   sum is not split), one per call in flight.
+ * ---------------------------------------------------------------------- */
+typedef enum { ZERO_GELU = 0, ZERO_GELU_TANH = 1, ZERO_SILU = 2 } zero_act_t;
+
+int zero_act_save8(const void* x, int32_t dtype, int64_t rows, int64_t cols, int64_t x_ld,
+                   int8_t* codes, uint8_t* exponents, void* stream);
+int zero_act_restore8(const int8_t* codes, const uint8_t* exponents, int64_t rows, int64_t cols,
+                      void* out, int32_t dtype, int64_t out_ld, void* stream);
+int zero_act_forward8(int32_t kind, const void* x, int64_t x_ld, const void* up, int64_t up_ld,
+                      int32_t dtype, int64_t rows, int64_t cols, void* y, int64_t y_ld,
+                      int8_t* codes, uint8_t* exponents, int8_t* up_codes, uint8_t* up_exponents,
+                      void* stream);
+int zero_act_backward8(int32_t kind, const void* dy, int64_t dy_ld, int32_t dtype, int64_t rows,
+                       int64_t cols, const int8_t* codes, const uint8_t* exponents,
+                       const int8_t* up_codes, const uint8_t* up_exponents, void* dx, int64_t dx_ld,
+                       void* dup, int64_t dup_ld, int8_t* again_codes, uint8_t* again_exponents,
+                       void* stream);
+int zero_weight_grad8_workspace(int64_t rows, int64_t outs, int64_t cols, int64_t* bytes);
+int zero_weight_grad8(const void* dy, int32_t dy_dtype, int64_t dy_ld, int64_t rows, int64_t outs,
+                      const int8_t* codes, const uint8_t* exponents, int64_t cols, void* grad,
+                      int32_t grad_dtype, uint32_t flags, void* workspace, int64_t workspace_bytes,
+                      void* stream);
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,510 @@
+"""Activations kept in 8 bits and what reads them, against the definitions in 64
+bits, on the GPU: codes and exponents bit for bit (ties, borders of a code,
+subnormal and largest numbers, infinities and NaN), the activation functions and
+their gradients with the bounds that fp32 operations allow, also against
+differences, weight gradients of whole numbers exactly and of others within the
+sums' bounds, at odd sizes, offsets and row distances, on streams, in graphs."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+DT = {"fp32": torch.float32, "fp16": torch.float16, "bf16": torch.bfloat16}
+HALF = {"fp32": 2.0 ** -24, "fp16": 2.0 ** -11, "bf16": 2.0 ** -8}
+LEAST = {"fp32": 2.0 ** -126, "fp16": 2.0 ** -25, "bf16": 2.0 ** -126}
+EMIN = {"fp32": 7, "fp16": 109, "bf16": 7}
+U = 2.0 ** -24
+KINDS = ("gelu", "gelu_tanh", "silu")
+
+
+@pytest.fixture(scope="module")
+def zf():
+    import fsdp_sharded_mixed_flatparameter_amd as m
+    assert torch.cuda.is_available()
+    return m
+
+
+def gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def kind_of(zf, kind):
+    return {"gelu": zf.ZERO_GELU, "gelu_tanh": zf.ZERO_GELU_TANH, "silu": zf.ZERO_SILU}[kind]
+
+
+def matrix(rows, cols, dtype, ld, shift, values=None):
+    """A (rows, cols) matrix of row distance ld, `shift` elements into a buffer of
+    sevens, and the buffer."""
+    buf = torch.full((rows * ld + shift + 64,), 7.0, dtype=dtype, device="cuda")
+    t = buf[shift:shift + rows * ld].view(rows, ld)[:, :cols] if rows else buf[:0].view(0, cols)
+    if values is not None:
+        t.copy_(values)
+    return t, buf
+
+
+def rest_kept(t, buf, shift, ld):
+    rows, cols = t.shape
+    mask = torch.ones_like(buf, dtype=torch.bool)
+    if rows:
+        mask[shift:shift + rows * ld].view(rows, ld)[:, :cols] = False
+    assert bool((buf[mask] == 7.0).all()), "memory beside the output was written"
+
+
+def checkpoint(x, emin):
+    """(codes, exponents) by the definition, in 64 bits on the host."""
+    rows, cols = x.shape
+    pitch = -(-cols // 32) * 32
+    p = np.zeros((rows, pitch))
+    p[:, :cols] = x.double().cpu().numpy()
+    p = p.reshape(rows, pitch // 32, 32)
+    with np.errstate(all="ignore"):
+        top = np.abs(p).max(2)
+        bad = ~np.isfinite(top)
+        e = np.where((top > 0) & ~bad, np.frexp(np.where(bad, 1.0, top))[1] - 1 + 127, 0)
+        e = np.maximum(e, emin)
+        q = np.clip(np.rint(np.ldexp(np.where(np.isfinite(p), p, 0.0), (133 - e)[:, :, None])), -127, 127)
+    q[bad] = 0
+    return q.astype(np.int8).reshape(rows, pitch), np.where(bad, 255, e).astype(np.uint8)
+
+
+def units(exponents):
+    """What one unit of a code stands for, from a table: the device's power of two
+    is not exact in 64 bits."""
+    table = torch.tensor([2.0 ** (e - 133) for e in range(255)] + [math.nan], dtype=torch.float64, device="cuda")
+    return table[exponents.long()]
+
+
+def values(saved):
+    """What a checkpoint stands for, in 64 bits."""
+    s = units(saved.exponents)
+    x = saved.codes.view(*saved.exponents.shape, 32).double() * s[:, :, None]
+    return x.view(saved.codes.shape)[:, :saved.cols]
+
+
+def activations(rows, cols, g):
+    x = torch.randn(rows, cols, generator=g, device="cuda") * torch.randn(cols, generator=g, device="cuda").exp()
+    if rows > 2 and cols > 2:
+        x[1] *= 30
+        x[2, ::3] = 0
+    return x
+
+
+def assert_near(got, want, tol):
+    got = got.double()
+    bad = ~((got - want).abs() <= tol)
+    bad &= ~(torch.isnan(got) & torch.isnan(want))
+    bad &= ~(torch.isinf(want) & (got == want))
+    assert not bool(bad.any()), (int(bad.sum()), got[bad][:4], want[bad][:4])
+
+
+SHAPES = [  # rows, cols, row distance more, shift
+    (1, 1, 0, 0), (1, 32, 0, 0), (3, 7, 2, 1), (5, 8, 0, 3), (2, 31, 1, 0), (4, 33, 0, 1), (65, 61, 6, 5),
+    (7, 64, 0, 0), (33, 100, 28, 0), (9, 1001, 0, 1), (130, 256, 256, 0), (3, 4096, 0, 7), (0, 40, 0, 0), (6, 0, 3, 0)]
+
+
+@pytest.mark.parametrize("dt", list(DT))
+@pytest.mark.parametrize("rows,cols,more,shift", SHAPES)
+def test_save_and_restore(zf, rows, cols, more, shift, dt):
+    g = gen(rows * 100 + cols)
+    ld = cols + more
+    x, _ = matrix(rows, cols, DT[dt], ld, shift, activations(rows, cols, g))
+    s = zf.Saved8(rows, cols)
+    s.codes.fill_(77)
+    s.exponents.fill_(99)
+    zf.zero_act_save8(x, s)
+    q, e = checkpoint(x, EMIN[dt])
+    assert np.array_equal(s.exponents.cpu().numpy(), e)
+    assert np.array_equal(s.codes.cpu().numpy(), q)
+    for odt in DT:
+        y, buf = matrix(rows, cols, DT[odt], ld, shift)
+        zf.zero_act_restore8(s, y)
+        want = values(s)
+        assert torch.equal(y.double(), want.to(DT[odt]).double())
+        # a code's unit is at most 2^-6 of the block's largest value: half of it, or all where it was cut at 127
+        if dt == odt and rows and cols:
+            top = torch.nn.functional.pad(x.double().abs(), (0, -cols % 32)).view(rows, -1, 32).amax(2)
+            unit = top.repeat_interleave(32, 1)[:, :cols] * 2.0 ** -6
+            assert bool(((want - x.double()).abs() <= torch.where(x.double().abs() >= unit * 63.7, unit, unit / 2)
+                         + 2.0 ** -24 * (dt == "fp16") + 2.0 ** -126).all())
+        rest_kept(y, buf, shift, ld)
+
+
+def edge_rows(dt):
+    """Blocks of 32 where the rounding could go wrong, one per row."""
+    fi = torch.finfo(DT[dt])
+    one = torch.ones(32, dtype=torch.float64)
+    k = torch.arange(32, dtype=torch.float64)
+    rows = [0 * one, one, -one, one * fi.max, one * -fi.max, one * fi.tiny, one * fi.tiny / 4, k + 0.5, -(k + 0.5),
+            (k + 96) / 1.0, torch.where(k == 3, 127.0, k + 0.5), torch.where(k == 0, 127.5, k - 15.5),
+            torch.where(k == 0, 127.75, 126.5), torch.where(k == 9, -128.0, k), torch.where(k == 9, 64.0, 0.25 * k),
+            torch.where(k == 31, math.inf, k), torch.where(k == 0, -math.inf, k), torch.where(k == 7, math.nan, k),
+            torch.where(k < 2, math.nan, math.inf), torch.where(k == 4, -0.0, 0.0), one * fi.smallest_normal / 64,
+            torch.where(k == 1, fi.max, fi.tiny), 2.0 ** (k - 16), -(2.0 ** (-k / 2))]
+    return torch.stack(rows).to(DT[dt])
+
+
+@pytest.mark.parametrize("dt", list(DT))
+def test_codes_at_their_edges(zf, dt):
+    x = edge_rows(dt).cuda()
+    s = zf.Saved8(*x.shape)
+    zf.zero_act_save8(x, s)
+    q, e = checkpoint(x, EMIN[dt])
+    assert np.array_equal(s.exponents.cpu().numpy(), e)
+    assert np.array_equal(s.codes.cpu().numpy(), q)
+    y = torch.empty_like(x)
+    zf.zero_act_restore8(s, y)
+    assert torch.equal(torch.isnan(y), torch.isnan(values(s)))
+    assert torch.equal(torch.nan_to_num(y.double()), torch.nan_to_num(values(s).to(DT[dt]).double()))
+
+
+def reference(kind, x):
+    """act, act', and bounds of their errors in fp32 operations, in 64 bits.  The
+    functions' exponentials take an argument rounded twice, so their relative
+    error grows with it; the approximate exponential and reciprocal are off by
+    one unit in the last place (2^-23)."""
+    if kind == "gelu":
+        c = x.clamp(-40, 40)
+        # by erfc: torch's ndtr is 1 + erf, which has no tail
+        cdf, tail = 0.5 * torch.special.erfc(-x * math.sqrt(0.5)), 0.5 * torch.special.erfc(x.abs() * math.sqrt(0.5))
+        density = torch.exp(-0.5 * c * c) / math.sqrt(2 * math.pi)
+        off = tail * (20 + 1.5 * c * c) * U + (x >= 0) * U
+        slope = cdf + c * density
+        return (x * cdf, slope, x.abs() * off + (x * cdf).abs() * U,
+                off + c.abs() * density * (1.5 * c * c + 8) * U + 2 * U * slope.abs())
+    if kind == "silu":
+        s, r = torch.sigmoid(x), torch.sigmoid(-x)
+        c = x.clamp(-100, 100)
+        off = s * (r * (c.abs() + 1) * 2 + 4) * U
+        slope = s + x * s * r
+        return (x * s, slope, x.abs() * off + (x * s).abs() * U,
+                off * (1 + c.abs() * r) + s * c.clamp(-100, 20).abs() * (off + 2 * U) + 4 * U * (s + (x * s * r).abs()))
+    c = x.clamp(-20, 20)
+    v = 2 * math.sqrt(2 / math.pi) * c * (1 + 0.044715 * c * c)
+    dv = 2 * math.sqrt(2 / math.pi) * (1 + 3 * 0.044715 * c * c)
+    s, r = torch.sigmoid(v), torch.sigmoid(-v)
+    off = s * (r * v.abs().clamp(max=100) * 6 + 6) * U
+    slope = s + c * s * r * dv
+    lead = c.abs() * dv * s * (v < 18)
+    return (x * s, slope, x.abs() * off + (x * s).abs() * U,
+            off + c.abs() * dv * r * off + lead * (off + 2 * U) + 12 * U * (s + c.abs() * s * r * dv))
+
+
+def function_inputs(rows, cols, g, dt):
+    x = torch.randn(rows, cols, generator=g, device="cuda") * 3
+    if rows > 3:
+        x[1] *= 20
+        x[2] *= 1e-3
+        x[3] *= 500 if dt == "fp16" else 1e12
+    return x
+
+
+@pytest.mark.parametrize("gated", (False, True))
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("dt", list(DT))
+@pytest.mark.parametrize("rows,cols,more,shift", [(1, 1, 0, 0), (6, 33, 2, 1), (40, 61, 61, 3), (9, 1000, 0, 0),
+                                                  (128, 256, 0, 0)])
+def test_forward_and_backward(zf, rows, cols, more, shift, dt, kind, gated):
+    g = gen(rows + cols)
+    ld = cols + more
+    x, _ = matrix(rows, cols, DT[dt], ld, shift, function_inputs(rows, cols, g, dt))
+    u = d = su = du = None
+    if gated:
+        u, _ = matrix(rows, cols, DT[dt], ld + 3, shift, torch.randn(rows, cols, generator=g, device="cuda"))
+        su = zf.Saved8(rows, cols)
+    s = zf.Saved8(rows, cols)
+    y, ybuf = matrix(rows, cols, DT[dt], ld, shift)
+    zf.zero_act_forward8(kind_of(zf, kind), x, y, s, up=u, saved_up=su)
+    rest_kept(y, ybuf, shift, ld)
+    for saved, m in ((s, x), (su, u)):
+        if saved is not None:
+            q, e = checkpoint(m, EMIN[dt])
+            assert np.array_equal(saved.codes.cpu().numpy(), q) and np.array_equal(saved.exponents.cpu().numpy(), e)
+    want, _, tol, _ = reference(kind, x.double())
+    factor = u.double() if gated else torch.ones_like(want)
+    want, tol = want * factor, tol * factor.abs() + (want * factor).abs() * U
+    half = 0.0 if dt == "fp32" else HALF[dt]
+    assert_near(y, want, tol + (want.abs() + tol) * half
+                + LEAST[dt] * (1 + factor.abs()) * (1 + x.double().abs()))
+    # backward, from the checkpoints
+    d, _ = matrix(rows, cols, DT[dt], ld, shift, torch.randn(rows, cols, generator=g, device="cuda"))
+    dx, dbuf = matrix(rows, cols, DT[dt], ld + 1, shift)
+    if gated:
+        du, ubuf = matrix(rows, cols, DT[dt], ld, shift)
+    again = zf.Saved8(rows, cols)
+    zf.zero_act_backward8(kind_of(zf, kind), d, s, dx, saved_up=su, dup=du, again=again)
+    rest_kept(dx, dbuf, shift, ld + 1)
+    xv = values(s)
+    uv = values(su) if gated else torch.ones_like(xv)
+    a, slope, a_tol, s_tol = reference(kind, xv)
+    scale = d.double() * uv
+    want, tol = scale * slope, scale.abs() * s_tol + (scale * slope).abs() * 2 * U
+    small = LEAST[dt] + 2.0 ** -120 * (1 + scale.abs() + d.double().abs()) * (1 + xv.abs())
+    assert_near(dx, want, tol + (want.abs() + tol) * half + small)
+    if gated:
+        rest_kept(du, ubuf, shift, ld)
+        want, tol = d.double() * a, d.double().abs() * a_tol + (d.double() * a).abs() * U
+        assert_near(du, want, tol + (want.abs() + tol) * half + small)
+    # the output's checkpoint made anew: within one code of the one of the exact output, by its own units
+    yv = a * uv
+    unit = units(again.exponents)
+    unit = unit.repeat_interleave(32, 1)[:, :cols]
+    off = (values(again) - yv).abs() - (a_tol * uv.abs() + yv.abs() * U + small)
+    assert bool((off <= torch.where(yv.abs() >= 126.5 * unit, unit, unit / 2)).all())
+    assert bool((again.codes[:, cols:] == 0).all())
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_functions_over_the_whole_line(zf, kind):
+    """fp32 over all magnitudes: forward, and the gradient at the checkpoints' values."""
+    x = torch.cat([torch.linspace(-30, 30, 40001), torch.logspace(-37, 37, 3000), -torch.logspace(-37, 37, 3000)])
+    x = torch.nn.functional.pad(x, (0, -x.numel() % 32)).cuda()
+    x = x.view(-1, 1).expand(-1, 32)              # every value is its block's largest
+    x = x * torch.linspace(0.5, 1, 32, device="cuda")
+    y, s = torch.empty_like(x), zf.Saved8(*x.shape)
+    zf.zero_act_forward8(kind_of(zf, kind), x, y, s)
+    want, _, tol, _ = reference(kind, x.double())
+    assert_near(y, want, tol + 2.0 ** -125 * (1 + x.double().abs()))
+    d, dx = torch.ones_like(x), torch.empty_like(x)
+    zf.zero_act_backward8(kind_of(zf, kind), d, s, dx)
+    _, slope, _, s_tol = reference(kind, values(s))
+    assert_near(dx, slope, s_tol + 2.0 ** -120)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_gradient_against_differences(zf, kind):
+    """(act(x + h) - act(x - h)) / 2h at the checkpoints' values."""
+    g = gen(7)
+    x = torch.randn(50, 64, generator=g, device="cuda") * 2
+    s = zf.Saved8(50, 64)
+    zf.zero_act_save8(x, s)
+    x = torch.empty_like(x)
+    zf.zero_act_restore8(s, x)
+    h = 2.0 ** -6
+    up, down, t = torch.empty_like(x), torch.empty_like(x), zf.Saved8(50, 64)
+    zf.zero_act_forward8(kind_of(zf, kind), x + h, up, t)
+    zf.zero_act_forward8(kind_of(zf, kind), x - h, down, t)
+    d, dx = torch.ones_like(x), torch.empty_like(x)
+    zf.zero_act_backward8(kind_of(zf, kind), d, s, dx)
+    # third derivatives are below 2 everywhere: h^2 / 6 of it, and the difference of two fp32 numbers below 16
+    assert float((dx.double() - (up - down).double() / (2 * h)).abs().max()) <= 2 * h * h / 6 + 16 * 8 * U / h
+
+
+def test_infinities_reach_the_gradients(zf):
+    x = torch.ones(3, 96, device="cuda")
+    x[0, 5], x[1, 40], x[2, 95] = math.inf, -math.inf, math.nan
+    s, y = zf.Saved8(3, 96), torch.empty_like(x)
+    zf.zero_act_forward8(zf.ZERO_SILU, x, y, s)
+    assert s.exponents.tolist() == [[255, 127, 127], [127, 255, 127], [127, 127, 255]]
+    assert float(y[0, 5]) == math.inf and bool(torch.isnan(y[1, 40])) and bool(torch.isnan(y[2, 95]))
+    for kind in (zf.ZERO_SILU, zf.ZERO_GELU, zf.ZERO_GELU_TANH):
+        dx, again = torch.empty_like(x), zf.Saved8(3, 96)
+        zf.zero_act_backward8(kind, torch.ones_like(x), s, dx, again=again)
+        assert torch.equal(torch.isnan(dx), (s.exponents == 255).repeat_interleave(32, 1))
+        assert torch.equal(again.exponents == 255, s.exponents == 255)
+    dw = torch.empty(4, 96, device="cuda")
+    zf.zero_weight_grad8(torch.ones(3, 4, device="cuda").bfloat16(), s, dw)
+    assert bool(torch.isnan(dw).all())            # every block of columns has its NaN
+    s.exponents[s.exponents == 255] = 133
+    zf.zero_weight_grad8(torch.ones(3, 4, device="cuda").half(), s, dw)
+    assert bool(torch.isfinite(dw).all())
+    # the overflow test of the step sees them
+    st = zf.StepState(1.0, False)
+    zf.zero_unscale_norm(dx, st)
+    assert st.read().overflow == 1
+
+
+def test_in_place(zf):
+    g = gen(3)
+    x = torch.randn(40, 70, generator=g, device="cuda")
+    u = torch.randn(40, 70, generator=g, device="cuda")
+    a, b = zf.Saved8(40, 70), zf.Saved8(40, 70)
+    y = torch.empty_like(x)
+    zf.zero_act_forward8(zf.ZERO_SILU, x, y, a, up=u, saved_up=b)
+    for over in (x.clone(), u.clone()):
+        xx, uu = (over, u) if torch.equal(over, x) else (x, over)
+        c, d = zf.Saved8(40, 70), zf.Saved8(40, 70)
+        zf.zero_act_forward8(zf.ZERO_SILU, xx, over, c, up=uu, saved_up=d)
+        assert torch.equal(over, y) and torch.equal(c.codes, a.codes) and torch.equal(d.codes, b.codes)
+    dy = torch.randn(40, 70, generator=g, device="cuda")
+    dx, dup = torch.empty_like(x), torch.empty_like(x)
+    zf.zero_act_backward8(zf.ZERO_SILU, dy, a, dx, saved_up=b, dup=dup)
+    for first in (True, False):
+        t, other = dy.clone(), torch.empty_like(x)
+        zf.zero_act_backward8(zf.ZERO_SILU, t, a, t if first else other, saved_up=b, dup=other if first else t)
+        assert torch.equal(t if first else other, dx) and torch.equal(other if first else t, dup)
+    # one gradient row for all
+    row = torch.randn(70, generator=g, device="cuda")
+    zf.zero_act_backward8(zf.ZERO_GELU, row.expand(40, 70), a, dx)
+    zf.zero_act_backward8(zf.ZERO_GELU, row.expand(40, 70).contiguous(), a, dup)
+    assert torch.equal(dx, dup)
+
+
+# ------------------------------------------------------------------ weight gradients
+WHOLE = [  # rows, outs, cols, dy, grad, accumulate, shift, row distance more
+    (1, 1, 1, "bf16", "fp32", False, 0, 0), (2, 16, 32, "fp16", "fp32", False, 0, 0), (63, 17, 33, "bf16", "fp32", True, 1, 3),
+    (64, 128, 128, "bf16", "fp32", False, 0, 0), (65, 129, 127, "fp16", "fp32", True, 3, 0), (127, 8, 260, "bf16", "fp32", False, 1, 1),
+    (128, 300, 40, "bf16", "fp32", True, 0, 12), (200, 257, 1000, "fp16", "fp32", False, 5, 0), (1000, 61, 61, "bf16", "fp32", False, 1, 0),
+    (5000, 130, 200, "bf16", "fp32", True, 0, 0), (70, 4096, 2085, "bf16", "fp32", False, 1, 0), (513, 2048, 4096, "fp16", "fp32", True, 0, 0),
+    (129, 4100, 2049, "bf16", "fp32", True, 0, 5), (0, 20, 40, "bf16", "fp32", False, 0, 0), (0, 20, 40, "bf16", "fp32", True, 0, 0),
+    (30, 0, 40, "bf16", "fp32", False, 0, 0), (30, 20, 0, "bf16", "fp32", False, 0, 0)]
+
+
+def whole_saved(zf, rows, cols, g):
+    """Whole numbers of up to 127 with exponents that differ by block."""
+    s = zf.Saved8(rows, cols)
+    s.codes.zero_()
+    s.codes[:, :cols] = torch.randint(-127, 128, (rows, cols), generator=g, device="cuda", dtype=torch.int8) \
+        if rows and cols else 0
+    s.exponents.copy_(torch.randint(132, 135, s.exponents.shape, generator=g, device="cuda").to(torch.uint8))
+    return s
+
+
+@pytest.mark.parametrize("rows,outs,cols,dt,gt,accumulate,shift,more", WHOLE)
+def test_weight_grad_of_whole_numbers_is_exact(zf, rows, outs, cols, dt, gt, accumulate, shift, more):
+    g = gen(rows + outs + cols)
+    s = whole_saved(zf, rows, cols, g)
+    dy, _ = matrix(rows, outs, DT[dt], outs + more, shift,
+                   torch.randint(-3, 4, (rows, outs), generator=g, device="cuda").float())
+    buf = torch.full((outs * cols + 128 + shift,), 7.0, device="cuda")
+    grad = buf[64 + shift:64 + shift + outs * cols].view(outs, cols)
+    if accumulate:
+        grad.copy_(torch.randint(-50, 51, (outs, cols), generator=g, device="cuda"))
+    # sums are multiples of 1/2 below 5000 * 3 * 254: exact in fp32 in any order
+    want = torch.matmul(dy.double().t().contiguous(), values(s)) + (grad.double() if accumulate else 0.0)
+    zf.zero_weight_grad8(dy, s, grad, accumulate=accumulate)
+    assert torch.equal(grad.double(), want)
+    assert bool((buf[:64 + shift] == 7).all()) and bool((buf[64 + shift + outs * cols:] == 7).all())
+
+
+@pytest.mark.parametrize("rows,outs,cols,shift", [(77, 40, 61, 1), (1500, 200, 130, 0), (300, 4096, 2080, 0), (20000, 33, 65, 0)])
+@pytest.mark.parametrize("dt", ("bf16", "fp16"))
+@pytest.mark.parametrize("gt", list(DT))
+@pytest.mark.parametrize("accumulate", (False, True))
+def test_weight_grad(zf, rows, outs, cols, shift, dt, gt, accumulate):
+    g = gen(rows + outs)
+    s = zf.Saved8(rows, cols)
+    zf.zero_act_save8(activations(rows, cols, g).clamp(-3e4, 3e4).to(DT[dt]), s)
+    dy = (torch.randn(rows, outs, generator=g, device="cuda") * 0.01).to(DT[dt])
+    grad = torch.zeros(outs * cols + shift, dtype=DT[gt], device="cuda")[shift:].view(outs, cols)
+    old = torch.zeros((), dtype=torch.float64, device="cuda")
+    if accumulate:
+        grad.copy_(torch.randn(outs, cols, generator=g, device="cuda"))
+        old = grad.double()
+    zf.zero_weight_grad8(dy, s, grad, accumulate=accumulate)
+    x = values(s).to(DT[dt]).double()
+    total = torch.matmul(dy.double().t().contiguous(), x)
+    size = torch.matmul(dy.double().abs().t().contiguous(), x.abs())
+    want = total + old
+    # exact products; each of the additions off by at most a step (2^-23) of a partial sum
+    tol = size * rows * 2 * U + want.abs() * U * bool(accumulate)
+    half = 0.0 if gt == "fp32" else HALF[gt]
+    assert_near(grad, want, tol + (want.abs() + tol) * half + LEAST[gt])
+
+
+def test_weight_grad_is_the_same_every_time_and_on_its_own_workspace(zf):
+    g = gen(2)
+    s = zf.Saved8(4000, 300)
+    zf.zero_act_save8(torch.randn(4000, 300, generator=g, device="cuda"), s)
+    dy = torch.randn(4000, 200, generator=g, device="cuda").bfloat16()
+    a, b = torch.empty(200, 300, device="cuda"), torch.empty(200, 300, device="cuda")
+    zf.zero_weight_grad8(dy, s, a)
+    need = zf.zero_weight_grad8_workspace(4000, 200, 300)
+    assert need > 0
+    buf = torch.full((need + 256,), 0xAB, dtype=torch.uint8, device="cuda")
+    zf.zero_weight_grad8(dy, s, b, workspace=buf[:need])
+    assert torch.equal(a, b) and bool((buf[need:] == 0xAB).all())
+
+
+def test_weight_grad_against_differences(zf):
+    """<dy, x (W + D)^T - x W^T> = <grad, D>, on whole numbers: exactly."""
+    g = gen(12)
+    s = whole_saved(zf, 90, 40, g)
+    x = torch.empty(90, 40, device="cuda")
+    zf.zero_act_restore8(s, x)
+    d = torch.randint(-3, 4, (24, 40), generator=g, device="cuda").float()
+    dy = torch.randint(-3, 4, (90, 24), generator=g, device="cuda").float()
+    grad = torch.empty(24, 40, device="cuda")
+    zf.zero_weight_grad8(dy.bfloat16(), s, grad)
+    moved = x.double() @ d.double().t().contiguous()
+    assert float((dy.double() * moved).sum()) == float((grad.double() * d.double()).sum())
+
+
+def test_offsets_past_2_to_the_31(zf):
+    """A matrix of more than 2^31 elements: its last rows are where they belong."""
+    rows, cols = 140000, 16384
+    x = torch.zeros(rows, cols, dtype=torch.bfloat16, device="cuda")
+    x[-1] = 3.0
+    x[131072] = -2.0
+    x[131071, -1] = 5.0
+    s, y = zf.Saved8(rows, cols), torch.empty_like(x)
+    zf.zero_act_save8(x, s)
+    zf.zero_act_restore8(s, y)
+    assert torch.equal(x, y)
+    del y
+    dy = torch.zeros(rows, 16, dtype=torch.bfloat16, device="cuda")
+    dy[-1], dy[131072], dy[131071] = 1.0, 4.0, 16.0
+    grad = torch.empty(16, cols, device="cuda")
+    zf.zero_weight_grad8(dy, s, grad)
+    want = torch.full((cols,), 3.0 - 8.0, device="cuda")
+    want[-1] += 80.0
+    assert torch.equal(grad, want.expand(16, cols))
+
+
+def unit_calls(zf, x, packed, dy, s, y, grads):
+    """A unit's gated layer, forward and backward, into views of its buffers."""
+    c = packed.shape[1] // 2
+    zf.zero_act_save8(x, s[0])
+    zf.zero_act_forward8(zf.ZERO_SILU, packed[:, :c], y, s[1], up=packed[:, c:], saved_up=s[2])
+    both = torch.empty_like(packed)
+    zf.zero_act_backward8(zf.ZERO_SILU, dy, s[1], both[:, :c], saved_up=s[2], dup=both[:, c:], again=s[3])
+    zf.zero_weight_grad8(both, s[0], grads[0])
+    zf.zero_weight_grad8(dy, s[3], grads[1], accumulate=True)
+    return both
+
+
+def test_captured_calls_replay_as_eager_ones(zf):
+    g = gen(14)
+    n, k, c = 700, 96, 160
+    x, packed = torch.zeros(n, k, device="cuda").bfloat16(), torch.zeros(n, 2 * c, device="cuda").bfloat16()
+    dy = torch.zeros(n, c, device="cuda").bfloat16()
+
+    def buffers():
+        return ([zf.Saved8(n, k)] + [zf.Saved8(n, c) for _ in range(3)], torch.empty(n, c, device="cuda").bfloat16(),
+                [torch.zeros(2 * c, k, device="cuda"), torch.zeros(c, c, device="cuda").bfloat16()])
+
+    s, y, grads = buffers()
+    unit_calls(zf, x, packed, dy, s, y, grads)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        both = unit_calls(zf, x, packed, dy, s, y, grads)
+    s2, y2, grads2 = buffers()
+    grads[1].zero_()
+    for r in range(3):
+        for t in (x, packed, dy):
+            t.copy_(torch.randn(t.shape, generator=g, device="cuda"))
+        graph.replay()
+        torch.cuda.synchronize()
+        both2 = unit_calls(zf, x, packed, dy, s2, y2, grads2)
+        torch.cuda.synchronize()
+        assert torch.equal(both, both2) and torch.equal(y, y2) and torch.equal(s[3].codes, s2[3].codes)
+        assert all(torch.equal(a, b) for a, b in zip(grads, grads2)), r
+
+
+def test_on_another_stream(zf):
+    g = gen(15)
+    s = zf.Saved8(3000, 300)
+    zf.zero_act_save8(torch.randn(3000, 300, generator=g, device="cuda"), s)
+    dy = torch.randn(3000, 100, generator=g, device="cuda").bfloat16()
+    a, b = torch.empty(100, 300, device="cuda"), torch.empty(100, 300, device="cuda")
+    zf.zero_weight_grad8(dy, s, a)
+    side = torch.cuda.Stream()
+    for st in (side, side.cuda_stream):
+        b.fill_(7.0)
+        side.wait_stream(torch.cuda.current_stream())
+        zf.zero_weight_grad8(dy, s, b, stream=st)
+        torch.cuda.current_stream().wait_stream(side)
+        assert torch.equal(a, b)
