@@ -12,117 +12,129 @@ dimension is contiguous: a row may be any distance from the next, so a slice of
 columns needs no copy.
 """
 import ctypes as C
+import functools
 
 import torch
 
-from . import (_FLOATS, _check, _current_raw_stream, _dtype_code, _dtype_name, _lib, _ptr, _stream)
+from . import _DTYPE_CODES, _check, _current_raw_stream, _dtype_name, _lib, _stream
 
 ZERO_ACCUMULATE = 8
 ZERO_GELU, ZERO_GELU_TANH, ZERO_SILU = 0, 1, 2
 ZERO_BLOCK8 = 32                 # columns that share an exponent
 
+# the checks below run before every launch, and a small call is as long as its
+# host's part: tensors are asked once each, and details only for an error
+_FLOATS = {getattr(torch, n): c for n, c in _DTYPE_CODES.items()}
+_HALVES = {t: c for t, c in _FLOATS.items() if t != torch.float32}
+_FP32, _INT8, _UINT8 = {torch.float32: 0}, {torch.int8: 1}, {torch.uint8: 1}
+_TOKENS = {torch.int64: 8, torch.int32: 4}
+_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
 
-def _here(t, name):
-    """`t`, a tensor of the current device."""
-    if not t.is_cuda:
+
+def _refuse(t, name, codes):
+    """Says what is wrong with the type or the place of a tensor."""
+    if t.dtype not in codes:
+        raise ValueError("%s must be %s, not %s" % (name, " or ".join(_dtype_name(d) for d in codes), t.dtype))
+    if t.get_device() < 0:
         raise ValueError("%s must be a device (CUDA) tensor" % name)
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError("%s is on %s, the current device is cuda:%d"
-                         % (name, t.device, torch.cuda.current_device()))
-    return t
+    raise ValueError("%s is on cuda:%d, the current device is cuda:%d" % (name, t.get_device(), _device()))
 
 
-def _typed(t, name, dtypes):
-    if _dtype_name(t.dtype) not in dtypes:
-        raise ValueError("%s must be %s, not %s" % (name, " or ".join(dtypes), t.dtype))
-    return _here(t, name)
+def _here(t, name, codes):
+    """The current device, which `t` has to be on."""
+    d = t.get_device()
+    if d < 0 or t.dtype not in codes or d != _device():
+        _refuse(t, name, codes)
+    return d
 
 
-def _flat(t, name, dtypes):
-    """A contiguous argument."""
-    _typed(t, name, dtypes)
+def _flat(t, name, codes, here):
+    """(first byte, byte behind the last, code of its type) of a contiguous argument."""
+    code = codes.get(t.dtype)
+    if code is None or t.get_device() != here:
+        _refuse(t, name, codes)
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
-    return t
+    p = t.data_ptr()
+    return p, p + t.nbytes, code
 
 
-def _rows(t, name, rows, cols, dtypes, written=False):
-    """The row stride of a matrix argument: (rows, cols), or a contiguous tensor
-    of that many elements whose last dimension is cols."""
-    _typed(t, name, dtypes)
-    if t.dim() == 0 or t.shape[-1] != cols or t.numel() != rows * cols:
-        raise ValueError("%s must hold %d rows of %d, not %s" % (name, rows, cols, tuple(t.shape)))
-    if t.is_contiguous() or t.numel() == 0:
-        return cols
-    if t.dim() != 2 or (cols > 1 and t.stride(1) != 1) or (written and rows > 1 and t.stride(0) < cols):
+def _rows(t, name, rows, cols, codes, here, written=False):
+    """(first byte, byte behind the last, code of its type, row distance) of a matrix
+    argument: (rows, cols), or a contiguous tensor of that many elements whose last
+    dimension is cols."""
+    code = codes.get(t.dtype)
+    if code is None or t.get_device() != here:
+        _refuse(t, name, codes)
+    shape = t.shape
+    if not shape or shape[-1] != cols or t.numel() != rows * cols:
+        raise ValueError("%s must hold %d rows of %d, not %s" % (name, rows, cols, tuple(shape)))
+    p = t.data_ptr()
+    if t.is_contiguous():
+        return p, p + t.nbytes, code, cols
+    ld, step = t.stride() if len(shape) == 2 else (0, 0)
+    if rows == 1 and step == 1:
+        return p, p + t.nbytes, code, cols
+    if len(shape) != 2 or (cols > 1 and step != 1) or (written and rows > 1 and ld < cols):
         raise ValueError("%s must be contiguous, or a matrix whose rows are" % name)
-    return t.stride(0) if rows > 1 else cols
-
-
-def _span(t):
-    """[first, last) byte of a tensor's memory."""
-    if t.numel() == 0:
-        return 0, 0
-    size = t.element_size()
-    return t.data_ptr(), t.data_ptr() + (1 + sum((n - 1) * s for n, s in zip(t.shape, t.stride()))) * size
+    ld = ld if rows > 1 else cols
+    return p, p + ((rows - 1) * ld + cols) * t.element_size(), code, ld
 
 
 def _apart(a, b, name_a, name_b):
-    """Refuses two tensors of which one is written where the other is used."""
-    (a0, a1), (b0, b1) = _span(a), _span(b)
-    if a1 <= b0 or b1 <= a0:
+    """Refuses two arguments, as _flat and _rows give them, of which one is written
+    where the other is used."""
+    if a[0] >= b[1] or b[0] >= a[1] or a[0] == a[1] or b[0] == b[1]:
         return
-    if a.dim() == 2 and b.dim() == 2 and a.element_size() == b.element_size() and a.stride(0) == b.stride(0) \
-            and a.stride(1) == 1 and b.stride(1) == 1:
+    if len(a) == len(b) == 4 and a[2] == b[2] and a[3] == b[3] > 0:
         # columns of one buffer: the distance of the rows' beginnings, within a row
-        ld = a.stride(0)
-        off = (b0 - a0) // a.element_size() % ld
-        if a.shape[1] <= off and off + b.shape[1] <= ld and (b0 - a0) % a.element_size() == 0:
+        size, ld = 2 if a[2] else 4, a[3]
+        cols_a, cols_b = ((x[1] - x[0]) // size % ld or ld for x in (a, b))
+        off = (b[0] - a[0]) // size % ld
+        if cols_a <= off and off + cols_b <= ld and (b[0] - a[0]) % size == 0:
             return
     raise ValueError("%s and %s overlap" % (name_a, name_b))
 
 
-def _scratch(workspace, need, device, stream):
+def _on(stream):
+    """The call's stream as an integer handle."""
+    return _current_raw_stream() if stream is None else _stream(stream).value or 0
+
+
+def _scratch(workspace, need, device, here, stream, handle):
     """The call's workspace: the caller's, or one of the call's own, which its
     stream keeps until the kernels are done with it."""
     if workspace is not None:
-        _flat(workspace, "workspace", ("uint8",))
-        if workspace.numel() < need:
+        if _flat(workspace, "workspace", _UINT8, here) and workspace.numel() < need:
             raise ValueError("the workspace needs %d bytes" % need)
         return workspace
     workspace = torch.empty(need, dtype=torch.uint8, device=device)
-    if stream is not None:
-        s = _stream(stream).value or 0
-        if s != _current_raw_stream():
-            workspace.record_stream(stream if isinstance(stream, torch.cuda.Stream)
-                                    else torch.cuda.ExternalStream(s))
+    if stream is not None and handle != _current_raw_stream():
+        workspace.record_stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(handle))
     return workspace
 
 
 # ------------------------------------------------------------------ embedding
-def _tokens(tokens):
-    _flat(tokens, "tokens", ("int64", "int32"))
-    return _ptr(tokens), tokens.element_size(), tokens.numel()
-
-
-def _table(t, name):
-    _flat(t, name, _FLOATS)
+def _table(t, name, here):
+    x = _flat(t, name, _FLOATS, here)
     if t.dim() != 2:
         raise ValueError("%s must be a matrix (rows by token)" % name)
-    return t.shape
+    return x, t.shape
 
 
 def zero_embed_lookup(tokens, table, out, scale=1.0, first=0, stream=None):
     """out[t] = table[tokens[t] - first] * scale, zeros for a token outside the
     table.  tokens: int32 or int64 of any shape; table: (vocab, dim), a view of
     the flat parameter; out: a row per token, fp32, fp16 or bf16."""
-    ptr, size, n = _tokens(tokens)
-    vocab, dim = _table(table, "table")
-    ld = _rows(out, "out", n, dim, _FLOATS, written=True)
-    _apart(out, table, "out", "table")
-    _apart(out, tokens, "out", "tokens")
-    _check(_lib.zero_embed_lookup(ptr, size, n, first, _ptr(table), _dtype_code(table), vocab, dim, scale,
-                                  _ptr(out), _dtype_code(out), ld, _stream(stream)))
+    here = _here(tokens, "tokens", _TOKENS)
+    t, n = _flat(tokens, "tokens", _TOKENS, here), tokens.numel()
+    w, (vocab, dim) = _table(table, "table", here)
+    y = _rows(out, "out", n, dim, _FLOATS, here, True)
+    _apart(y, w, "out", "table")
+    _apart(y, t, "out", "tokens")
+    rc = _lib.zero_embed_lookup(t[0], t[2], n, first, w[0], w[2], vocab, dim, scale, y[0], y[2], y[3], _on(stream))
+    if rc:
+        _check(rc)
 
 
 def zero_embed_lookup_int8(tokens, q_buf, q_scales, n_slots, slot_numel, elem_offset, vocab, out, scale=1.0,
@@ -130,22 +142,25 @@ def zero_embed_lookup_int8(tokens, q_buf, q_scales, n_slots, slot_numel, elem_of
     """zero_embed_lookup on a table that lies elem_offset elements into the flat
     parameter whose n_slots INT8 slots have been gathered (the payload that
     zero_dequant_allgather takes)."""
-    ptr, size, n = _tokens(tokens)
-    _flat(q_buf, "q_buf", ("int8",))
-    _flat(q_scales, "q_scales", ("float32",))
+    here = _here(tokens, "tokens", _TOKENS)
+    t, n = _flat(tokens, "tokens", _TOKENS, here), tokens.numel()
+    q, s = _flat(q_buf, "q_buf", _INT8, here), _flat(q_scales, "q_scales", _FP32, here)
     if out.dim() == 0:
         raise ValueError("out must have a row per token")
     dim = out.shape[-1]
-    ld = _rows(out, "out", n, dim, _FLOATS, written=True)
+    y = _rows(out, "out", n, dim, _FLOATS, here, True)
     if q_buf.numel() < n_slots * slot_numel or q_scales.numel() < n_slots * -(-slot_numel // block):
         raise ValueError("buffers are shorter than n_slots slots")
-    for t, name in ((tokens, "tokens"), (q_buf, "q_buf"), (q_scales, "q_scales")):
-        _apart(out, t, "out", name)
-    _check(_lib.zero_embed_lookup_int8(ptr, size, n, first, _ptr(q_buf), _ptr(q_scales), n_slots, slot_numel,
-                                       block, elem_offset, vocab, dim, scale, _ptr(out), _dtype_code(out), ld,
-                                       _stream(stream)))
+    _apart(y, t, "out", "tokens")
+    _apart(y, q, "out", "q_buf")
+    _apart(y, s, "out", "q_scales")
+    rc = _lib.zero_embed_lookup_int8(t[0], t[2], n, first, q[0], s[0], n_slots, slot_numel, block, elem_offset, vocab,
+                                     dim, scale, y[0], y[2], y[3], _on(stream))
+    if rc:
+        _check(rc)
 
 
+@functools.lru_cache(maxsize=256)
 def zero_embed_grad_workspace(n_tokens, vocab, dim):
     """The bytes of workspace that zero_embed_grad needs."""
     b = C.c_int64(0)
@@ -162,16 +177,19 @@ def zero_embed_grad(tokens, dy, grad, scale=1.0, first=0, padding=None, accumula
     in which the GPU does the work.  Without a workspace the call takes one of
     its own from torch's allocator; a captured graph that brings its own must
     not share it with what may run at the same time."""
-    ptr, size, n = _tokens(tokens)
-    vocab, dim = _table(grad, "grad")
-    ld = _rows(dy, "dy", n, dim, _FLOATS)
-    _apart(grad, dy, "grad", "dy")
-    _apart(grad, tokens, "grad", "tokens")
-    workspace = _scratch(workspace, zero_embed_grad_workspace(n, vocab, dim), grad.device, stream)
+    here = _here(tokens, "tokens", _TOKENS)
+    t, n = _flat(tokens, "tokens", _TOKENS, here), tokens.numel()
+    g, (vocab, dim) = _table(grad, "grad", here)
+    d = _rows(dy, "dy", n, dim, _FLOATS, here)
+    _apart(g, d, "grad", "dy")
+    _apart(g, t, "grad", "tokens")
+    handle = _on(stream)
+    ws = _scratch(workspace, zero_embed_grad_workspace(n, vocab, dim), grad.device, here, stream, handle)
     pad = None if padding is None else C.byref(C.c_int64(padding))
-    _check(_lib.zero_embed_grad(ptr, size, n, first, pad, _ptr(dy), _dtype_code(dy), ld, scale, _ptr(grad),
-                                _dtype_code(grad), vocab, dim, ZERO_ACCUMULATE if accumulate else 0,
-                                _ptr(workspace), workspace.numel(), _stream(stream)))
+    rc = _lib.zero_embed_grad(t[0], t[2], n, first, pad, d[0], d[2], d[3], scale, g[0], g[2], vocab, dim,
+                              ZERO_ACCUMULATE if accumulate else 0, ws.data_ptr(), ws.numel(), handle)
+    if rc:
+        _check(rc)
 
 
 # ------------------------------------------------------------------ activations in 8 bits
@@ -185,66 +203,84 @@ class Saved8:
         rows, cols = int(rows), int(cols)
         if rows < 0 or cols < 0:
             raise ValueError("negative size")
-        pitch = -(-cols // ZERO_BLOCK8) * ZERO_BLOCK8
         self.rows, self.cols = rows, cols
-        self.codes = torch.empty(rows, pitch, dtype=torch.int8, device=device)
-        self.exponents = torch.empty(rows, pitch // ZERO_BLOCK8, dtype=torch.uint8, device=device)
-
-    def _tensors(self, name):
-        pitch = -(-self.cols // ZERO_BLOCK8) * ZERO_BLOCK8
-        for t, part, dt, shape in ((self.codes, "codes", "int8", (self.rows, pitch)),
-                                   (self.exponents, "exponents", "uint8", (self.rows, pitch // ZERO_BLOCK8))):
-            _flat(t, "%s.%s" % (name, part), (dt,))
-            if t.shape != shape:
-                raise ValueError("%s.%s must be %s" % (name, part, shape))
-        return self.codes, self.exponents
+        self.codes = torch.empty(rows, -(-cols // ZERO_BLOCK8) * ZERO_BLOCK8, dtype=torch.int8, device=device)
+        self.exponents = torch.empty(rows, -(-cols // ZERO_BLOCK8), dtype=torch.uint8, device=device)
 
 
-def _saved(s, name):
-    """(codes, exponents) pointers of a checkpoint argument, or of none."""
+_NONE = (None, None)
+
+
+def _saved(s, name, here, rows=None, cols=None):
+    """(codes, exponents) of a checkpoint argument, as _flat gives them."""
     if s is None:
-        return None, None
-    c, e = s._tensors(name)
-    return _ptr(c), _ptr(e)
-
-
-def _fits(s, name, rows, cols):
-    if s is not None and (s.rows, s.cols) != (rows, cols):
+        return _NONE
+    if rows is not None and (s.rows != rows or s.cols != cols):
         raise ValueError("%s is of a (%d, %d) matrix, not (%d, %d)" % (name, s.rows, s.cols, rows, cols))
+    c, e = _flat(s.codes, name + ".codes", _INT8, here), _flat(s.exponents, name + ".exponents", _UINT8, here)
+    blocks = -(-s.cols // ZERO_BLOCK8)
+    if s.codes.shape != (s.rows, blocks * ZERO_BLOCK8) or s.exponents.shape != (s.rows, blocks):
+        raise ValueError("%s.codes must be (%d, %d), its exponents (%d, %d)"
+                         % (name, s.rows, blocks * ZERO_BLOCK8, s.rows, blocks))
+    return c, e
 
 
-def _same_place(a, b):
-    return a.data_ptr() == b.data_ptr() and a.dtype == b.dtype and a.shape == b.shape and a.stride() == b.stride()
+def _at(x):
+    return None if x is None else x[0]
 
 
 def _apart_all(written, read, same=()):
     """Refuses overlaps of what is written with one another and with what is read,
-    but for the pairs in `same`, which may be one and the same tensor."""
-    for k, (a, name_a) in enumerate(written):
-        for b, name_b in written[k + 1:] + read:
-            if a is None or b is None or ((name_a, name_b) in same and _same_place(a, b)):
-                continue
-            _apart(a, b, name_a, name_b)
+    but for the pairs in `same`, which may be one and the same matrix.  Arguments
+    are (name, what _flat or _rows gave, or None)."""
+    written = [x for x in written if x[1] is not None]
+    read = [x for x in read if x[1] is not None]
+    # nothing meets where every written range ends before the next range begins
+    ranges = sorted([x[1][:2] + (True,) for x in written if x[1][0] < x[1][1]]
+                    + [x[1][:2] + (False,) for x in read if x[1][0] < x[1][1]])
+    end, end_read, clash = 0, 0, False
+    for first, last, w in ranges:
+        if first < end or (w and first < end_read):
+            clash = True
+            break
+        if w:
+            end = max(end, last)
+        else:
+            end_read = max(end_read, last)
+    if not clash:
+        return
+    for k, (name_a, a) in enumerate(written):
+        for name_b, b in written[k + 1:] + read:
+            if not ((name_a, name_b) in same and a == b):
+                _apart(a, b, name_a, name_b)
 
 
-def _parts(s, name):
-    return [] if s is None else [(s.codes, name + ".codes"), (s.exponents, name + ".exponents")]
+def _parts(name, s):
+    return [(name + ".codes", s[0]), (name + ".exponents", s[1])]
 
 
 def zero_act_save8(x, saved, stream=None):
     """The checkpoint of x, a (saved.rows, saved.cols) matrix."""
-    c, e = _saved(saved, "saved")
-    ld = _rows(x, "x", saved.rows, saved.cols, _FLOATS)
-    _apart_all(_parts(saved, "saved"), [(x, "x")])
-    _check(_lib.zero_act_save8(_ptr(x), _dtype_code(x), saved.rows, saved.cols, ld, c, e, _stream(stream)))
+    here = _here(saved.codes, "saved.codes", _INT8)
+    c, e = _saved(saved, "saved", here)
+    m = _rows(x, "x", saved.rows, saved.cols, _FLOATS, here)
+    _apart(c, m, "saved.codes", "x")
+    _apart(e, m, "saved.exponents", "x")
+    rc = _lib.zero_act_save8(m[0], m[2], saved.rows, saved.cols, m[3], c[0], e[0], _on(stream))
+    if rc:
+        _check(rc)
 
 
 def zero_act_restore8(saved, out, stream=None):
     """out = the values that the checkpoint stands for, in out's type."""
-    c, e = _saved(saved, "saved")
-    ld = _rows(out, "out", saved.rows, saved.cols, _FLOATS, written=True)
-    _apart_all([(out, "out")], _parts(saved, "saved"))
-    _check(_lib.zero_act_restore8(c, e, saved.rows, saved.cols, _ptr(out), _dtype_code(out), ld, _stream(stream)))
+    here = _here(saved.codes, "saved.codes", _INT8)
+    c, e = _saved(saved, "saved", here)
+    m = _rows(out, "out", saved.rows, saved.cols, _FLOATS, here, True)
+    _apart(m, c, "out", "saved.codes")
+    _apart(m, e, "out", "saved.exponents")
+    rc = _lib.zero_act_restore8(c[0], e[0], saved.rows, saved.cols, m[0], m[2], m[3], _on(stream))
+    if rc:
+        _check(rc)
 
 
 def zero_act_forward8(kind, x, out, saved, up=None, saved_up=None, stream=None):
@@ -253,18 +289,18 @@ def zero_act_forward8(kind, x, out, saved, up=None, saved_up=None, stream=None):
     columns of one buffer; out may be x or up itself."""
     if (up is None) != (saved_up is None):
         raise ValueError("up and saved_up go together")
-    c, e = _saved(saved, "saved")
-    uc, ue = _saved(saved_up, "saved_up")
-    rows, cols = saved.rows, saved.cols
-    _fits(saved_up, "saved_up", rows, cols)
-    dt = (_dtype_name(x.dtype),)
-    x_ld = _rows(x, "x", rows, cols, _FLOATS)
-    y_ld = _rows(out, "out", rows, cols, dt, written=True)
-    u_ld = 0 if up is None else _rows(up, "up", rows, cols, dt)
-    _apart_all([(out, "out")] + _parts(saved, "saved") + _parts(saved_up, "saved_up"), [(x, "x"), (up, "up")],
+    here, rows, cols = _here(saved.codes, "saved.codes", _INT8), saved.rows, saved.cols
+    s, su = _saved(saved, "saved", here), _saved(saved_up, "saved_up", here, rows, cols)
+    m = _rows(x, "x", rows, cols, _FLOATS, here)
+    dt = {x.dtype: m[2]}
+    y = _rows(out, "out", rows, cols, dt, here, True)
+    u = None if up is None else _rows(up, "up", rows, cols, dt, here)
+    _apart_all([("out", y)] + _parts("saved", s) + _parts("saved_up", su), [("x", m), ("up", u)],
                (("out", "x"), ("out", "up")))
-    _check(_lib.zero_act_forward8(kind, _ptr(x), x_ld, _ptr(up), u_ld, _dtype_code(x), rows, cols, _ptr(out), y_ld,
-                                  c, e, uc, ue, _stream(stream)))
+    rc = _lib.zero_act_forward8(kind, m[0], m[3], _at(u), 0 if u is None else u[3], m[2], rows, cols, y[0], y[3],
+                                s[0][0], s[1][0], _at(su[0]), _at(su[1]), _on(stream))
+    if rc:
+        _check(rc)
 
 
 def zero_act_backward8(kind, dy, saved, dx, saved_up=None, dup=None, again=None, stream=None):
@@ -274,25 +310,25 @@ def zero_act_backward8(kind, dy, saved, dx, saved_up=None, dup=None, again=None,
     may be dy itself."""
     if (dup is None) != (saved_up is None):
         raise ValueError("dup and saved_up go together")
-    c, e = _saved(saved, "saved")
-    uc, ue = _saved(saved_up, "saved_up")
-    ac, ae = _saved(again, "again")
-    rows, cols = saved.rows, saved.cols
-    _fits(saved_up, "saved_up", rows, cols)
-    _fits(again, "again", rows, cols)
-    dt = (_dtype_name(dy.dtype),)
-    d_ld = _rows(dy, "dy", rows, cols, _FLOATS)
-    x_ld = _rows(dx, "dx", rows, cols, dt, written=True)
-    u_ld = 0 if dup is None else _rows(dup, "dup", rows, cols, dt, written=True)
-    _apart_all([(dx, "dx"), (dup, "dup")] + _parts(again, "again"),
-               [(dy, "dy")] + _parts(saved, "saved") + _parts(saved_up, "saved_up"),
-               (("dx", "dy"), ("dup", "dy")))
-    _check(_lib.zero_act_backward8(kind, _ptr(dy), d_ld, _dtype_code(dy), rows, cols, c, e, uc, ue, _ptr(dx), x_ld,
-                                   _ptr(dup), u_ld, ac, ae, _stream(stream)))
+    here, rows, cols = _here(saved.codes, "saved.codes", _INT8), saved.rows, saved.cols
+    s, su = _saved(saved, "saved", here), _saved(saved_up, "saved_up", here, rows, cols)
+    sa = _saved(again, "again", here, rows, cols)
+    d = _rows(dy, "dy", rows, cols, _FLOATS, here)
+    dt = {dy.dtype: d[2]}
+    x = _rows(dx, "dx", rows, cols, dt, here, True)
+    u = None if dup is None else _rows(dup, "dup", rows, cols, dt, here, True)
+    _apart_all([("dx", x), ("dup", u)] + _parts("again", sa),
+               [("dy", d)] + _parts("saved", s) + _parts("saved_up", su), (("dx", "dy"), ("dup", "dy")))
+    rc = _lib.zero_act_backward8(kind, d[0], d[3], d[2], rows, cols, s[0][0], s[1][0], _at(su[0]), _at(su[1]), x[0], x[3],
+                                 _at(u), 0 if u is None else u[3], _at(sa[0]), _at(sa[1]), _on(stream))
+    if rc:
+        _check(rc)
 
 
+@functools.lru_cache(maxsize=256)
 def zero_weight_grad8_workspace(rows, outs, cols):
-    """The bytes of workspace that zero_weight_grad8 needs (0 for most sizes)."""
+    """The bytes of workspace that zero_weight_grad8 needs (0 where it does not split
+    its sums)."""
     b = C.c_int64(0)
     _check(_lib.zero_weight_grad8_workspace(rows, outs, cols, C.byref(b)))
     return b.value
@@ -303,16 +339,22 @@ def zero_weight_grad8(dy, saved, grad, accumulate=False, workspace=None, stream=
     checkpoint of its input; with `accumulate` added to what grad holds.  dy: (rows,
     outs), fp16 or bf16; grad: a view of the flat gradient, fp32, fp16 or bf16.
     The workspace is as zero_embed_grad's."""
-    c, e = _saved(saved, "saved")
-    _flat(grad, "grad", _FLOATS)
+    here = _here(saved.codes, "saved.codes", _INT8)
+    c, e = _saved(saved, "saved", here)
+    g = _flat(grad, "grad", _FLOATS, here)
     if grad.dim() != 2 or grad.shape[1] != saved.cols:
         raise ValueError("grad must be a matrix of %d columns" % saved.cols)
     rows, cols, outs = saved.rows, saved.cols, grad.shape[0]
-    ld = _rows(dy, "dy", rows, outs, ("float16", "bfloat16"))
-    _apart_all([(grad, "grad")], [(dy, "dy")] + _parts(saved, "saved"))
-    need = zero_weight_grad8_workspace(rows, outs, cols)
+    d = _rows(dy, "dy", rows, outs, _HALVES, here)
+    _apart(g, d, "grad", "dy")
+    _apart(g, c, "grad", "saved.codes")
+    _apart(g, e, "grad", "saved.exponents")
+    handle = _on(stream)
+    need, ws, size = zero_weight_grad8_workspace(rows, outs, cols), None, 0
     if need or workspace is not None:
-        workspace = _scratch(workspace, need, grad.device, stream)
-    _check(_lib.zero_weight_grad8(_ptr(dy), _dtype_code(dy), ld, rows, outs, c, e, cols, _ptr(grad),
-                                  _dtype_code(grad), ZERO_ACCUMULATE if accumulate else 0, _ptr(workspace),
-                                  0 if workspace is None else workspace.numel(), _stream(stream)))
+        ws = _scratch(workspace, need, grad.device, here, stream, handle)
+        ws, size = ws.data_ptr(), ws.numel()
+    rc = _lib.zero_weight_grad8(d[0], d[2], d[3], rows, outs, c[0], e[0], cols, g[0], g[2],
+                                ZERO_ACCUMULATE if accumulate else 0, ws, size, handle)
+    if rc:
+        _check(rc)

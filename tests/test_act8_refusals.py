@@ -104,14 +104,15 @@ def test_workspace_sizes(zf):
             zf.zero_weight_grad8_workspace(*bad)
 
 
-def test_tensors_are_refused(zf):
+def test_tensors_are_refused(zf, monkeypatch):
+    monkeypatch.setattr(zf.unit, "_device", lambda: 0)
     s = zf.Saved8(4, 40, device="cpu")
     assert s.codes.shape == (4, 64) and s.exponents.shape == (4, 2)
     x = torch.zeros(4, 40)
-    with pytest.raises(ValueError, match="device"):
-        zf.zero_act_save8(x, s)
     with pytest.raises(ValueError, match="go together"):
         zf.zero_act_forward8(zf.ZERO_SILU, x, x, s, up=x)
+    with pytest.raises(ValueError, match="saved.codes must be a device"):
+        zf.zero_act_save8(x, s)
     with pytest.raises(ValueError, match="go together"):
         zf.zero_act_backward8(zf.ZERO_SILU, x, s, x, dup=x)
     with pytest.raises(ValueError, match="negative"):
@@ -124,7 +125,8 @@ class Device:
     def __init__(self, t, base):
         self.t, self.base, self.device = t, base, torch.device("cuda", 0)
 
-    is_cuda = True
+    def get_device(self):
+        return 0
 
     def __getattr__(self, name):
         return getattr(self.t, name)
@@ -136,7 +138,7 @@ class Device:
 @pytest.fixture
 def place(zf, monkeypatch):
     """Tensors that pass for device tensors, and a library that must not be called."""
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(zf.unit, "_device", lambda: 0)
     monkeypatch.setattr(zf.unit, "_lib", None)
     base = [1 << 20]
 

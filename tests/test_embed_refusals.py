@@ -109,7 +109,8 @@ class Device:
         self.t, self.base = t, base
         self.device = torch.device("cuda", index)
 
-    is_cuda = True
+    def get_device(self):
+        return self.device.index
 
     def __getattr__(self, name):
         return getattr(self.t, name)
@@ -119,31 +120,44 @@ class Device:
 
 
 def test_another_device_is_refused(zf, monkeypatch):
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
-    with pytest.raises(ValueError, match="current device is cuda:0"):
-        zf.unit._here(Device(torch.zeros(4), index=1), "x")
-    assert zf.unit._here(Device(torch.zeros(4)), "x")
+    monkeypatch.setattr(zf.unit, "_device", lambda: 0)
+    u, f = zf.unit, zf.unit._FLOATS
+    with pytest.raises(ValueError, match="x is on cuda:1, the current device is cuda:0"):
+        u._flat(Device(torch.zeros(4), index=1), "x", f, 0)
+    with pytest.raises(ValueError, match="x is on cuda:1"):
+        u._rows(Device(torch.zeros(4, 2), index=1), "x", 4, 2, f, 0)
+    assert u._flat(Device(torch.zeros(4)), "x", f, 0) == (1 << 20, (1 << 20) + 16, 0)
 
 
-def test_rows_and_overlaps(zf, monkeypatch):
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
-    u, f = zf.unit, ("float32",)
+def test_rows_and_overlaps(zf):
+    u, f = zf.unit, zf.unit._FLOATS
     t = torch.zeros(6, 20)
-    assert u._rows(Device(t), "x", 6, 20, f) == 20
-    assert u._rows(Device(t[:, 3:9]), "x", 6, 6, f) == 20
-    assert u._rows(Device(t[0].expand(6, 20)), "x", 6, 20, f) == 0
-    assert u._rows(Device(t.view(2, 3, 20)), "x", 6, 20, f) == 20
-    assert u._rows(Device(t[:1, 3:9]), "x", 1, 6, f, written=True) == 6
-    assert u._rows(Device(t[:0]), "x", 0, 20, f) == 20
-    for bad, rows, cols, written in ((t, 6, 19, False), (t, 5, 20, False), (t[:, ::2], 6, 10, False),
-                                     (t.t(), 20, 6, False), (t[0].expand(6, 20), 6, 20, True),
-                                     (t.view(2, 3, 20)[:, :, :5], 6, 5, False)):
+
+    def rows(t, n, cols, written=False):
+        return u._rows(Device(t), "x", n, cols, f, 0, written)
+
+    base = 1 << 20
+    assert rows(t, 6, 20) == (base, base + 480, 0, 20)
+    assert rows(t[:, 3:9], 6, 6) == (base + 12, base + 12 + 4 * 106, 0, 20)
+    assert rows(t[0].expand(6, 20), 6, 20) == (base, base + 80, 0, 0)
+    assert rows(t.view(2, 3, 20), 6, 20)[3] == 20
+    assert rows(t[:1, 3:9], 1, 6, True) == (base + 12, base + 36, 0, 6)
+    assert rows(t[:0], 0, 20)[3] == 20
+    for bad, n, cols, written in ((t, 6, 19, False), (t, 5, 20, False), (t[:, ::2], 6, 10, False),
+                                  (t.t(), 20, 6, False), (t[0].expand(6, 20), 6, 20, True),
+                                  (t.view(2, 3, 20)[:, :, :5], 6, 5, False), (t[0, 0], 1, 1, False)):
         with pytest.raises(ValueError, match="x must"):
-            u._rows(Device(bad), "x", rows, cols, f, written)
-    u._apart(Device(t[:, :8]), Device(t[:, 8:]), "a", "b")
-    u._apart(Device(t[:, 8:]), Device(t[:, :8]), "a", "b")
-    u._apart(Device(t[:3]), Device(t[3:]), "a", "b")
-    u._apart(Device(t[:0]), Device(t), "a", "b")
-    for a, b in ((t, t), (t[:, :8], t[:, 7:]), (t[:, 7:], t[:, :8]), (t[1:, :8], t[:-1, 4:12]), (t[:4], t[3:])):
+            rows(bad, n, cols, written)
+
+    def apart(a, b):
+        u._apart(rows(a, *a.shape), rows(b, *b.shape), "a", "b")
+
+    apart(t[:, :8], t[:, 8:])
+    apart(t[:, 8:], t[:, :8])
+    apart(t[:, 8:9], t[:, 9:])
+    apart(t[:3], t[3:])
+    apart(t[:0], t)
+    for a, b in ((t, t), (t[:, :8], t[:, 7:]), (t[:, 7:], t[:, :8]), (t[1:, :8], t[:-1, 4:12]), (t[:4], t[3:]),
+                 (t[:, 2:5], t[2])):
         with pytest.raises(ValueError, match="a and b overlap"):
-            u._apart(Device(a), Device(b), "a", "b")
+            apart(a, b if b.dim() == 2 else b[None])
