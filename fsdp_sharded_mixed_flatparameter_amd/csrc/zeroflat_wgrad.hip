@@ -16,6 +16,7 @@ namespace {
 
 constexpr int kDepth = 64;                 // rows t of one step
 
+typedef signed char v4c __attribute__((ext_vector_type(4)));
 typedef short v4s __attribute__((ext_vector_type(4)));
 typedef short v8s __attribute__((ext_vector_type(8)));
 typedef __bf16 v8b __attribute__((ext_vector_type(8)));
@@ -44,11 +45,12 @@ __device__ __forceinline__ void restore16(v4u codes, uint32_t exponent, v4u& lo,
     const float s = exponent == 255u ? __uint_as_float(0x7fc00000u) : __uint_as_float((exponent - 6u) << 23);
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
+        const uint32_t word = codes[w];
+        const v4c c = __builtin_bit_cast(v4c, word);
         uint32_t out[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const float a = (float)(int8_t)(codes[w] >> (16 * h)) * s;
-            const float b = (float)(int8_t)(codes[w] >> (16 * h + 8)) * s;
+            const float a = (float)c[2 * h] * s, b = (float)c[2 * h + 1] * s;
             if constexpr (DT == ZERO_BF16)     // exact: the low halves are zero
                 out[h] = __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
             else
@@ -137,49 +139,75 @@ __global__ __launch_bounds__(WO * WI * 64) void weight_grad_kernel(WeightGrad a)
     const int64_t o0 = to * TO, i0 = ti * TI;
     const int64_t t0 = split * a.share, t1 = min(a.rows, t0 + a.share);
     const int steps = (int)((t1 - t0 + kDepth - 1) / kDepth);
+    // Steps whose loads need no test.  Columns beyond the matrix are read from
+    // inside it (their results are not written), but for a last group of fewer
+    // than eight outputs, which runs into the next row: there has to be one.
+    const bool over = a.outs % 8 != 0;
+    const int whole = a.outs < 8 || (over && a.dy_ld < a.outs) ? 0
+        : (int)((min(t1, a.rows - (over ? 1 : 0)) - t0) / kDepth);
+
+    // This thread's part of a step: groups of eight outputs and of sixteen codes.
+    constexpr int ywide = TO / 8, xwide = TI / 16;             // in a row
+    constexpr int yrows = S::threads / ywide, xrows = S::threads / xwide;   // rows apart
+    static_assert(yrows * ywide == S::threads && xrows * xwide == S::threads, "whole rows per load");
+    const int ycol = tid % ywide * 8, yk = tid / ywide;
+    const int xcol = tid % xwide * 16, xk = tid / xwide;
+    const int64_t o = min(o0 + ycol, (a.outs - 1) / 8 * 8), i = min(i0 + xcol, a.pitch - 16);
+    const uint16_t* yp = static_cast<const uint16_t*>(a.dy) + (t0 + yk) * a.dy_ld + o;
+    const int8_t* xp = a.codes + (t0 + xk) * a.pitch + i;
+    const uint8_t* ep = a.exponents + (t0 + xk) * (a.pitch / 32) + i / 32;
+    const int64_t ystep = yrows * a.dy_ld, xstep = xrows * a.pitch;
 
     v4u yreg[S::y_loads], xreg[S::x_loads];
     uint32_t ereg[S::x_loads];
-    auto fetch = [&](int step) {
+    auto fetch = [&]() {                       // of a whole step
+#pragma unroll
+        for (int j = 0; j < S::y_loads; ++j, yp += ystep) yreg[j] = *reinterpret_cast<const v4u_any*>(yp);
+#pragma unroll
+        for (int j = 0; j < S::x_loads; ++j, xp += xstep, ep += xstep / 32) {
+            xreg[j] = *reinterpret_cast<const v4u*>(xp);
+            ereg[j] = *ep;
+        }
+    };
+    auto fetch_some = [&](int step) {          // of any step, zeros beyond the rows
         const int64_t t = t0 + (int64_t)step * kDepth;
 #pragma unroll
         for (int j = 0; j < S::y_loads; ++j) {
-            const int e = j * S::threads + tid, k = e / (TO / 8), c = e % (TO / 8) * 8;
-            const int64_t o = o0 + c;
-            const uint16_t* p = static_cast<const uint16_t*>(a.dy) + (t + k) * a.dy_ld + o;
-            if (t + k < t1 && o + 8 <= a.outs) {
-                yreg[j] = *reinterpret_cast<const v4u_any*>(p);
-            } else {
-                yreg[j] = v4u{0, 0, 0, 0};
-                if (t + k < t1)
+            const int64_t row = t + yk + j * yrows;
+            yreg[j] = v4u{0, 0, 0, 0};
+            if (row < t1) {
+                const uint16_t* p = static_cast<const uint16_t*>(a.dy) + row * a.dy_ld + o;
+                if (o + 8 <= a.outs) {
+                    yreg[j] = *reinterpret_cast<const v4u_any*>(p);
+                } else {
 #pragma unroll
-                    for (int q = 0; q < 8; ++q)
+                    for (int q = 0; q < 7; ++q)
                         if (o + q < a.outs) yreg[j][q / 2] |= (uint32_t)p[q] << (16 * (q & 1));
+                }
             }
         }
 #pragma unroll
         for (int j = 0; j < S::x_loads; ++j) {
-            const int e = j * S::threads + tid, k = e / (TI / 16), c = e % (TI / 16) * 16;
-            const int64_t i = i0 + c;
+            const int64_t row = t + xk + j * xrows;
             xreg[j] = v4u{0, 0, 0, 0};
             ereg[j] = 7;
-            if (t + k < t1 && i < a.pitch) {
-                xreg[j] = *reinterpret_cast<const v4u*>(a.codes + (t + k) * a.pitch + i);
-                ereg[j] = a.exponents[(t + k) * (a.pitch / 32) + i / 32];
+            if (row < t1) {
+                xreg[j] = *reinterpret_cast<const v4u*>(a.codes + row * a.pitch + i);
+                ereg[j] = a.exponents[row * (a.pitch / 32) + i / 32];
             }
         }
     };
     auto stage = [&](int buf) {
 #pragma unroll
         for (int j = 0; j < S::y_loads; ++j) {
-            const int e = j * S::threads + tid, k = e / (TO / 8), c = e % (TO / 8);
-            const int at = k * TO + (((c >> 1) ^ swizzle<TO>(k)) << 4) + (c & 1) * 8;
+            const int k = yk + j * yrows;
+            const int at = k * TO + (((ycol >> 4) ^ swizzle<TO>(k)) << 4) + (ycol & 8);
             *reinterpret_cast<v4u*>(&ysh[buf][at]) = yreg[j];
         }
 #pragma unroll
         for (int j = 0; j < S::x_loads; ++j) {
-            const int e = j * S::threads + tid, k = e / (TI / 16), c = e % (TI / 16);
-            const int at = k * TI + ((c ^ swizzle<TI>(k)) << 4);
+            const int k = xk + j * xrows;
+            const int at = k * TI + (((xcol >> 4) ^ swizzle<TI>(k)) << 4);
             v4u lo, hi;
             restore16<DT>(xreg[j], ereg[j], lo, hi);
             *reinterpret_cast<v4u*>(&xsh[buf][at]) = lo;
@@ -192,15 +220,15 @@ __global__ __launch_bounds__(WO * WI * 64) void weight_grad_kernel(WeightGrad a)
     for (int o = 0; o < S::fo; ++o)
 #pragma unroll
         for (int i = 0; i < S::fi; ++i) acc[o][i] = v4f{0, 0, 0, 0};
-    const int wo = wave / WI * (TO / WO / 16), wi = wave % WI * (TI / WI / 16);
+    const int wo = wave / WI * S::fo, wi = wave % WI * S::fi;
     const int krow = 8 * (lane / 16) + lane % 16 / 4;            // this lane's row of a transposing load
     const int kcol = lane % 4 * 4;
-    auto compute = [&](int buf) {
+    auto multiply = [&](int buf) {
 #pragma unroll
-        for (int kk = 0; kk < kDepth; kk += 32) {
+        for (int half = 0; half < kDepth; half += 32) {
             v8s x[S::fi], y[S::fo];
             auto frag = [&](const uint16_t* sh, int T, int chunk) {
-                const uint16_t* p = sh + (kk + krow) * T + (chunk << 4) + kcol;
+                const uint16_t* p = sh + (half + krow) * T + (chunk << 4) + kcol;
                 const v4s u = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(p));
                 const v4s v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(p + 4 * T));
                 return __builtin_shufflevector(u, v, 0, 1, 2, 3, 4, 5, 6, 7);
@@ -216,15 +244,29 @@ __global__ __launch_bounds__(WO * WI * 64) void weight_grad_kernel(WeightGrad a)
         }
     };
 
+    // While step s is multiplied, the next step's registers go to the other buffer
+    // and the loads of the step after that are on their way.
     if (steps > 0) {
-        fetch(0);
+        if (whole > 0) fetch();
+        else fetch_some(0);
         stage(0);
-    }
-    for (int s = 0; s < steps; ++s) {
+        if (whole > 1) fetch();
+        else if (steps > 1) fetch_some(1);
         __syncthreads();
-        if (s + 1 < steps) fetch(s + 1);
-        compute(s & 1);
+    }
+    int s = 0;
+    for (; s + 2 < whole; ++s) {
+        stage((s + 1) & 1);
+        fetch();
+        __builtin_amdgcn_sched_barrier(0);
+        multiply(s & 1);
+        __syncthreads();
+    }
+    for (; s < steps; ++s) {
         if (s + 1 < steps) stage((s + 1) & 1);
+        if (s + 2 < steps) fetch_some(s + 2);
+        multiply(s & 1);
+        __syncthreads();
     }
 
     // a lane has four consecutive inputs i of one output o
