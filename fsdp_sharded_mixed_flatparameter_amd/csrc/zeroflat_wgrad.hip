@@ -223,25 +223,24 @@ __global__ __launch_bounds__(WO * WI * 64) void weight_grad_kernel(WeightGrad a)
     const int wo = wave / WI * S::fo, wi = wave % WI * S::fi;
     const int krow = 8 * (lane / 16) + lane % 16 / 4;            // this lane's row of a transposing load
     const int kcol = lane % 4 * 4;
-    auto multiply = [&](int buf) {
+    v8s x[S::fi], y[S::fo];
+    auto operands = [&](int buf, int half) {
+        auto frag = [&](const uint16_t* sh, int T, int chunk) {
+            const uint16_t* p = sh + (half + krow) * T + (chunk << 4) + kcol;
+            const v4s u = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(p));
+            const v4s v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(p + 4 * T));
+            return __builtin_shufflevector(u, v, 0, 1, 2, 3, 4, 5, 6, 7);
+        };
 #pragma unroll
-        for (int half = 0; half < kDepth; half += 32) {
-            v8s x[S::fi], y[S::fo];
-            auto frag = [&](const uint16_t* sh, int T, int chunk) {
-                const uint16_t* p = sh + (half + krow) * T + (chunk << 4) + kcol;
-                const v4s u = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(p));
-                const v4s v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(p + 4 * T));
-                return __builtin_shufflevector(u, v, 0, 1, 2, 3, 4, 5, 6, 7);
-            };
+        for (int i = 0; i < S::fi; ++i) x[i] = frag(xsh[buf], TI, (wi + i) ^ swizzle<TI>(krow));
 #pragma unroll
-            for (int i = 0; i < S::fi; ++i) x[i] = frag(xsh[buf], TI, (wi + i) ^ swizzle<TI>(krow));
+        for (int o = 0; o < S::fo; ++o) y[o] = frag(ysh[buf], TO, (wo + o) ^ swizzle<TO>(krow));
+    };
+    auto multiply = [&]() {
 #pragma unroll
-            for (int o = 0; o < S::fo; ++o) y[o] = frag(ysh[buf], TO, (wo + o) ^ swizzle<TO>(krow));
+        for (int o = 0; o < S::fo; ++o)
 #pragma unroll
-            for (int o = 0; o < S::fo; ++o)
-#pragma unroll
-                for (int i = 0; i < S::fi; ++i) acc[o][i] = mfma<DT>(x[i], y[o], acc[o][i]);
-        }
+            for (int i = 0; i < S::fi; ++i) acc[o][i] = mfma<DT>(x[i], y[o], acc[o][i]);
     };
 
     // While step s is multiplied, the next step's registers go to the other buffer
@@ -256,16 +255,22 @@ __global__ __launch_bounds__(WO * WI * 64) void weight_grad_kernel(WeightGrad a)
     }
     int s = 0;
     for (; s + 2 < whole; ++s) {
+        operands(s & 1, 0);
         stage((s + 1) & 1);
         fetch();
         __builtin_amdgcn_sched_barrier(0);
-        multiply(s & 1);
+        multiply();
+        operands(s & 1, 32);
+        multiply();
         __syncthreads();
     }
     for (; s < steps; ++s) {
         if (s + 1 < steps) stage((s + 1) & 1);
         if (s + 2 < steps) fetch_some(s + 2);
-        multiply(s & 1);
+        operands(s & 1, 0);
+        multiply();
+        operands(s & 1, 32);
+        multiply();
         __syncthreads();
     }
 
