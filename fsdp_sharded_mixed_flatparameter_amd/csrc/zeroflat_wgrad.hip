@@ -14,7 +14,7 @@
 namespace zf {
 namespace {
 
-constexpr int kDepth = 64;                 // rows t of one step
+constexpr int kDepth = 32;                 // rows t of one step
 
 typedef signed char v4c __attribute__((ext_vector_type(4)));
 typedef short v4s __attribute__((ext_vector_type(4)));
@@ -31,35 +31,28 @@ __device__ __forceinline__ v4f mfma(v8s a, v8s b, v4f c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, a), __builtin_bit_cast(v8h, b), c, 0, 0, 0);
 }
 
-// A row of a tile in LDS is T 16-bit elements in chunks of 16, each at its place
-// xor a number of the row: the transposing load's sixteen lanes read one chunk
-// of four rows, which then lie in different banks.
-template <int T>
-__device__ __forceinline__ int swizzle(int k) {
-    return ((k & 3) | ((k >> 3) & 1) << 2) & (T / 16 - 1);
-}
+// A row of a tile in LDS is T 16-bit elements and 16 more: the transposing load's
+// sixteen lanes read 32 bytes of four rows, which then lie in different banks, and
+// every address of a lane is one number and a constant.
+constexpr int kPad = 16;
 
-// Sixteen codes with one exponent to 16-bit values.
+__device__ __forceinline__ float scale_of(uint32_t exponent) {
+    return exponent == 255u ? __uint_as_float(0x7fc00000u) : __uint_as_float((exponent - 6u) << 23);
+}
+// Four codes to 16-bit values.
 template <int DT>
-__device__ __forceinline__ void restore16(v4u codes, uint32_t exponent, v4u& lo, v4u& hi) {
-    const float s = exponent == 255u ? __uint_as_float(0x7fc00000u) : __uint_as_float((exponent - 6u) << 23);
+__device__ __forceinline__ v2u restore4(uint32_t codes, float s) {
+    const v4c c = __builtin_bit_cast(v4c, codes);
+    v2u out;
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
-        const uint32_t word = codes[w];
-        const v4c c = __builtin_bit_cast(v4c, word);
-        uint32_t out[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const float a = (float)c[2 * h] * s, b = (float)c[2 * h + 1] * s;
-            if constexpr (DT == ZERO_BF16)     // exact: the low halves are zero
-                out[h] = __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
-            else
-                out[h] = (uint32_t)from_f32<ZERO_F16>(a) | (uint32_t)from_f32<ZERO_F16>(b) << 16;
-        }
-        v4u& to = w < 2 ? lo : hi;
-        to[2 * (w & 1)] = out[0];
-        to[2 * (w & 1) + 1] = out[1];
+    for (int h = 0; h < 2; ++h) {
+        const float a = (float)c[2 * h] * s, b = (float)c[2 * h + 1] * s;
+        if constexpr (DT == ZERO_BF16)     // exact: the low halves are zero
+            out[h] = __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
+        else
+            out[h] = (uint32_t)from_f32<ZERO_F16>(a) | (uint32_t)from_f32<ZERO_F16>(b) << 16;
     }
+    return out;
 }
 
 // Four consecutive elements at any element offset, the first n of which exist.
@@ -130,8 +123,9 @@ struct Tile {
 template <int DT, int TO, int TI, int WO, int WI>
 __global__ __launch_bounds__(WO * WI * 64) void weight_grad_kernel(WeightGrad a) {
     using S = Tile<DT, TO, TI, WO, WI>;
-    __shared__ __attribute__((aligned(16))) uint16_t ysh[2][kDepth * TO];
-    __shared__ __attribute__((aligned(16))) uint16_t xsh[2][kDepth * TI];
+    constexpr int ly = TO + kPad, lx = TI + kPad;
+    __shared__ __attribute__((aligned(16))) uint16_t ysh[2 * kDepth * ly];
+    __shared__ __attribute__((aligned(16))) uint16_t xsh[2 * kDepth * lx];
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
     const int64_t b = blockIdx.x;
     const int64_t split = b / a.tiles, tile = b - split * a.tiles;
@@ -141,9 +135,10 @@ __global__ __launch_bounds__(WO * WI * 64) void weight_grad_kernel(WeightGrad a)
     const int steps = (int)((t1 - t0 + kDepth - 1) / kDepth);
     // Steps whose loads need no test.  Columns beyond the matrix are read from
     // inside it (their results are not written), but for a last group of fewer
-    // than eight outputs, which runs into the next row: there has to be one.
+    // than eight outputs, which runs into the next row: there has to be one.  A
+    // thread's rows are within 32 bits of a step's first.
     const bool over = a.outs % 8 != 0;
-    const int whole = a.outs < 8 || (over && a.dy_ld < a.outs) ? 0
+    const int whole = a.outs < 8 || (over && a.dy_ld < a.outs) || a.dy_ld > (int64_t)1 << 25 ? 0
         : (int)((min(t1, a.rows - (over ? 1 : 0)) - t0) / kDepth);
 
     // This thread's part of a step: groups of eight outputs and of sixteen codes.
@@ -153,66 +148,79 @@ __global__ __launch_bounds__(WO * WI * 64) void weight_grad_kernel(WeightGrad a)
     const int ycol = tid % ywide * 8, yk = tid / ywide;
     const int xcol = tid % xwide * 16, xk = tid / xwide;
     const int64_t o = min(o0 + ycol, (a.outs - 1) / 8 * 8), i = min(i0 + xcol, a.pitch - 16);
-    const uint16_t* yp = static_cast<const uint16_t*>(a.dy) + (t0 + yk) * a.dy_ld + o;
-    const int8_t* xp = a.codes + (t0 + xk) * a.pitch + i;
-    const uint8_t* ep = a.exponents + (t0 + xk) * (a.pitch / 32) + i / 32;
-    const int64_t ystep = yrows * a.dy_ld, xstep = xrows * a.pitch;
+    // a step's first row, the same for the whole block, and this thread's place in bytes
+    const char* yp = static_cast<const char*>(a.dy) + t0 * a.dy_ld * 2;
+    const char* xp = reinterpret_cast<const char*>(a.codes) + t0 * a.pitch;
+    const char* ep = reinterpret_cast<const char*>(a.exponents) + t0 * (a.pitch / 32);
+    const uint32_t yat = (uint32_t)(yk * a.dy_ld + o) * 2, xat = (uint32_t)(xk * a.pitch + i);
+    const uint32_t eat = (uint32_t)(xk * (a.pitch / 32) + i / 32);
+    const int64_t ystep = yrows * a.dy_ld * 2, xstep = xrows * a.pitch;
 
-    v4u yreg[S::y_loads], xreg[S::x_loads];
-    uint32_t ereg[S::x_loads];
-    auto fetch = [&]() {                       // of a whole step
-#pragma unroll
-        for (int j = 0; j < S::y_loads; ++j, yp += ystep) yreg[j] = *reinterpret_cast<const v4u_any*>(yp);
-#pragma unroll
-        for (int j = 0; j < S::x_loads; ++j, xp += xstep, ep += xstep / 32) {
-            xreg[j] = *reinterpret_cast<const v4u*>(xp);
-            ereg[j] = *ep;
-        }
+    // two steps' loads on their way
+    v4u yreg[2][S::y_loads], xreg[2][S::x_loads];
+    uint32_t ereg[2][S::x_loads];
+    auto fetch_y = [&](int set, int j) { yreg[set][j] = *reinterpret_cast<const v4u_any*>(yp + j * ystep + yat); };
+    auto fetch_x = [&](int set, int j) {
+        xreg[set][j] = *reinterpret_cast<const v4u*>(xp + j * xstep + xat);
+        ereg[set][j] = *reinterpret_cast<const uint8_t*>(ep + j * (xstep / 32) + eat);
     };
-    auto fetch_some = [&](int step) {          // of any step, zeros beyond the rows
-        const int64_t t = t0 + (int64_t)step * kDepth;
+    auto advance = [&]() {
+        yp += kDepth * a.dy_ld * 2;
+        xp += kDepth * a.pitch;
+        ep += kDepth * (a.pitch / 32);
+    };
+    auto fetch = [&](int set, int n) {         // step n, zeros beyond the rows
+        if (n >= steps) return;
+        // its addresses are made anew from the thread's number: kept over the main
+        // loop they would take the registers that its loads need
+        int id = tid;
+        asm volatile("" : "+v"(id));
+        const int yk = id / ywide, xk = id / xwide;
+        const int64_t o = min(o0 + id % ywide * 8, (a.outs - 1) / 8 * 8), i = min(i0 + id % xwide * 16, a.pitch - 16);
+        const int64_t t = t0 + (int64_t)n * kDepth;
 #pragma unroll
         for (int j = 0; j < S::y_loads; ++j) {
             const int64_t row = t + yk + j * yrows;
-            yreg[j] = v4u{0, 0, 0, 0};
+            yreg[set][j] = v4u{0, 0, 0, 0};
             if (row < t1) {
                 const uint16_t* p = static_cast<const uint16_t*>(a.dy) + row * a.dy_ld + o;
                 if (o + 8 <= a.outs) {
-                    yreg[j] = *reinterpret_cast<const v4u_any*>(p);
+                    yreg[set][j] = *reinterpret_cast<const v4u_any*>(p);
                 } else {
 #pragma unroll
                     for (int q = 0; q < 7; ++q)
-                        if (o + q < a.outs) yreg[j][q / 2] |= (uint32_t)p[q] << (16 * (q & 1));
+                        if (o + q < a.outs) yreg[set][j][q / 2] |= (uint32_t)p[q] << (16 * (q & 1));
                 }
             }
         }
 #pragma unroll
         for (int j = 0; j < S::x_loads; ++j) {
             const int64_t row = t + xk + j * xrows;
-            xreg[j] = v4u{0, 0, 0, 0};
-            ereg[j] = 7;
+            xreg[set][j] = v4u{0, 0, 0, 0};
+            ereg[set][j] = 7;
             if (row < t1) {
-                xreg[j] = *reinterpret_cast<const v4u*>(a.codes + row * a.pitch + i);
-                ereg[j] = a.exponents[row * (a.pitch / 32) + i / 32];
+                xreg[set][j] = *reinterpret_cast<const v4u*>(a.codes + row * a.pitch + i);
+                ereg[set][j] = a.exponents[row * (a.pitch / 32) + i / 32];
             }
         }
     };
-    auto stage = [&](int buf) {
+    // set k goes to buffer k
+    auto stage_y = [&](int set, int j) {
+        *reinterpret_cast<v4u*>(&ysh[(set * kDepth + yk + j * yrows) * ly + ycol]) = yreg[set][j];
+    };
+    v4u half;
+    auto stage_x = [&](int set, int w) {       // word w % 4 of load w / 4
+        const v2u r = restore4<DT>(xreg[set][w / 4][w % 4], scale_of(ereg[set][w / 4]));
+        half[2 * (w & 1)] = r[0];
+        half[2 * (w & 1) + 1] = r[1];
+        if (w & 1)
+            *reinterpret_cast<v4u*>(&xsh[(set * kDepth + xk + w / 4 * xrows) * lx + xcol + (w & 2) * 4]) = half;
+    };
+    auto stage = [&](int set) {
 #pragma unroll
-        for (int j = 0; j < S::y_loads; ++j) {
-            const int k = yk + j * yrows;
-            const int at = k * TO + (((ycol >> 4) ^ swizzle<TO>(k)) << 4) + (ycol & 8);
-            *reinterpret_cast<v4u*>(&ysh[buf][at]) = yreg[j];
-        }
+        for (int j = 0; j < S::y_loads; ++j) stage_y(set, j);
 #pragma unroll
-        for (int j = 0; j < S::x_loads; ++j) {
-            const int k = xk + j * xrows;
-            const int at = k * TI + (((xcol >> 4) ^ swizzle<TI>(k)) << 4);
-            v4u lo, hi;
-            restore16<DT>(xreg[j], ereg[j], lo, hi);
-            *reinterpret_cast<v4u*>(&xsh[buf][at]) = lo;
-            *reinterpret_cast<v4u*>(&xsh[buf][at + 8]) = hi;
-        }
+        for (int w = 0; w < 4 * S::x_loads; ++w) stage_x(set, w);
     };
 
     v4f acc[S::fo][S::fi];
@@ -223,55 +231,83 @@ __global__ __launch_bounds__(WO * WI * 64) void weight_grad_kernel(WeightGrad a)
     const int wo = wave / WI * S::fo, wi = wave % WI * S::fi;
     const int krow = 8 * (lane / 16) + lane % 16 / 4;            // this lane's row of a transposing load
     const int kcol = lane % 4 * 4;
-    v8s x[S::fi], y[S::fo];
-    auto operands = [&](int buf, int half) {
-        auto frag = [&](const uint16_t* sh, int T, int chunk) {
-            const uint16_t* p = sh + (half + krow) * T + (chunk << 4) + kcol;
-            const v4s u = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(p));
-            const v4s v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(p + 4 * T));
-            return __builtin_shufflevector(u, v, 0, 1, 2, 3, 4, 5, 6, 7);
-        };
-#pragma unroll
-        for (int i = 0; i < S::fi; ++i) x[i] = frag(xsh[buf], TI, (wi + i) ^ swizzle<TI>(krow));
-#pragma unroll
-        for (int o = 0; o < S::fo; ++o) y[o] = frag(ysh[buf], TO, (wo + o) ^ swizzle<TO>(krow));
+    v8s x[S::fi], y[S::fo];                     // a step's operands
+    auto frag = [&](const uint16_t* p, int row) {
+        const v4s u = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(p));
+        const v4s v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(p + 4 * row));
+        return __builtin_shufflevector(u, v, 0, 1, 2, 3, 4, 5, 6, 7);
     };
-    auto multiply = [&]() {
+    const uint16_t* xread = xsh + krow * lx + kcol + wi * 16;
+    const uint16_t* yread = ysh + krow * ly + kcol + wo * 16;
+    auto xfrag = [&](int buf, int i) { return frag(xread + buf * kDepth * lx + i * 16, lx); };
+    auto yfrag = [&](int buf, int o) { return frag(yread + buf * kDepth * ly + o * 16, ly); };
+    // Multiplies the step whose operands are held ; row by row they
+    // give way to those of the next one, in the other buffer, and `work` gets its
+    // turns beside them.
+    auto multiply = [&](int buf, bool more, auto work) {
 #pragma unroll
-        for (int o = 0; o < S::fo; ++o)
+        for (int o = 0; o < S::fo; ++o) {
 #pragma unroll
-            for (int i = 0; i < S::fi; ++i) acc[o][i] = mfma<DT>(x[i], y[o], acc[o][i]);
+            for (int i = 0; i < S::fi; ++i) {
+                acc[o][i] = mfma<DT>(x[i], y[o], acc[o][i]);
+                if (more && o == S::fo - 1) x[i] = xfrag(1 - buf, i);
+            }
+            if (more) y[o] = yfrag(1 - buf, o);
+            work(o);
+            __builtin_amdgcn_sched_barrier(0);
+        }
     };
 
-    // While step s is multiplied, the next step's registers go to the other buffer
-    // and the loads of the step after that are on their way.
+    // Step s multiplies what was read from buffer s % 2 during step s - 1, reads step
+    // s + 1 from the other buffer, writes step s + 2 over its own and issues the loads
+    // of step s + 4.
     if (steps > 0) {
-        if (whole > 0) fetch();
-        else fetch_some(0);
+        fetch(0, 0);
+        fetch(1, 1);
         stage(0);
-        if (whole > 1) fetch();
-        else if (steps > 1) fetch_some(1);
+        if (steps > 1) stage(1);
+        fetch(0, 2);
+        fetch(1, 3);
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < S::fi; ++i) x[i] = xfrag(0, i);
+#pragma unroll
+        for (int o = 0; o < S::fo; ++o) y[o] = yfrag(0, o);
         __syncthreads();
     }
     int s = 0;
-    for (; s + 2 < whole; ++s) {
-        operands(s & 1, 0);
-        stage((s + 1) & 1);
-        fetch();
-        __builtin_amdgcn_sched_barrier(0);
-        multiply();
-        operands(s & 1, 32);
-        multiply();
-        __syncthreads();
+    yp += 4 * kDepth * a.dy_ld * 2;
+    xp += 4 * kDepth * a.pitch;
+    ep += 4 * kDepth * (a.pitch / 32);
+    for (; s + 5 < whole; s += 2) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            multiply(k, true, [&](int o) {
+#pragma unroll
+                for (int j = o * S::y_loads / S::fo; j < (o + 1) * S::y_loads / S::fo; ++j) {
+                    stage_y(k, j);
+                    fetch_y(k, j);
+                }
+#pragma unroll
+                for (int w = o * 4 * S::x_loads / S::fo; w < (o + 1) * 4 * S::x_loads / S::fo; ++w) {
+                    stage_x(k, w);
+                    if (w % 4 == 3) fetch_x(k, w / 4);
+                }
+            });
+            advance();
+            __syncthreads();
+        }
     }
-    for (; s < steps; ++s) {
-        if (s + 1 < steps) stage((s + 1) & 1);
-        if (s + 2 < steps) fetch_some(s + 2);
-        operands(s & 1, 0);
-        multiply();
-        operands(s & 1, 32);
-        multiply();
-        __syncthreads();
+    for (; s < steps; s += 2) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            if (s + k < steps) {
+                if (s + k + 2 < steps) stage(k);
+                fetch(k, s + k + 4);
+                multiply(k, s + k + 1 < steps, [](int) {});
+                __syncthreads();
+            }
+        }
     }
 
     // a lane has four consecutive inputs i of one output o
