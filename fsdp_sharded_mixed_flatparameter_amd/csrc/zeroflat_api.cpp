@@ -1088,7 +1088,7 @@ int weight_plan(const char* fn, int64_t rows, int64_t outs, int64_t cols, zf::We
     a->cols = cols;
     a->pitch = (cols + 31) / 32 * 32;
     zf::plan_weight_grad(*a);
-    *bytes = a->splits > 1 ? a->splits * outs * cols * 4 : 0;
+    *bytes = (a->tiles - a->whole_tiles) * a->splits * a->tile * a->tile * 4;
     return ZERO_OK;
 }
 }  // namespace

@@ -110,8 +110,31 @@ __device__ __forceinline__ void finish4(const WeightGrad& a, int64_t at, int n, 
     else finish4_as<ZERO_BF16>(a, at, n, x);
 }
 
+// What block b does.  The first blocks take whole tiles, the ones behind them
+// shares of the rows of the tiles that are left.  Blocks go to the eight dies in
+// turn: each die gets a run of tiles, in bands of four, so that the tiles it has
+// at a time share their strips of dy and x in its cache.
+struct Unit {
+    uint32_t to, ti, split, part;
+    bool shared;
+};
+__device__ __forceinline__ Unit unit_of(const WeightGrad& a, uint32_t b) {
+    Unit u;
+    const uint32_t cut = (uint32_t)a.whole_tiles, rest = (uint32_t)a.tiles - cut;
+    u.shared = b >= cut;
+    u.part = b - cut;
+    u.split = u.shared ? u.part / rest : 0;
+    const uint32_t nth = u.shared ? u.part - u.split * rest : b, in_run = u.shared ? rest : cut;
+    const uint32_t die = nth % 8, tile = (u.shared ? cut : 0) + die * (in_run / 8) + min(die, in_run % 8) + nth / 8;
+    const uint32_t wide = (uint32_t)a.tiles_i, band = tile / (4 * wide), in_band = tile - band * 4 * wide;
+    const uint32_t high = min(4u, (uint32_t)a.tiles_o - band * 4);
+    u.to = band * 4 + in_band % high;
+    u.ti = in_band / high;
+    return u;
+}
+
 // A block's tile is TO outputs o by TI inputs i, its waves WO by WI of them.
-template <int DT, int TO, int TI, int WO, int WI>
+template <int TO, int TI, int WO, int WI>
 struct Tile {
     static constexpr int threads = WO * WI * 64;
     static constexpr int fo = TO / WO / 16, fi = TI / WI / 16;      // 16 x 16 fragments of a wave
@@ -122,16 +145,15 @@ struct Tile {
 
 template <int DT, int TO, int TI, int WO, int WI>
 __global__ __launch_bounds__(WO * WI * 64) void weight_grad_kernel(WeightGrad a) {
-    using S = Tile<DT, TO, TI, WO, WI>;
+    using S = Tile<TO, TI, WO, WI>;
     constexpr int ly = TO + kPad, lx = TI + kPad;
     __shared__ __attribute__((aligned(16))) uint16_t ysh[2 * kDepth * ly];
     __shared__ __attribute__((aligned(16))) uint16_t xsh[2 * kDepth * lx];
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
-    const int64_t b = blockIdx.x;
-    const int64_t split = b / a.tiles, tile = b - split * a.tiles;
-    const int64_t to = tile / a.tiles_i, ti = tile - to * a.tiles_i;
-    const int64_t o0 = to * TO, i0 = ti * TI;
-    const int64_t t0 = split * a.share, t1 = min(a.rows, t0 + a.share);
+    const Unit u = unit_of(a, blockIdx.x);
+    const int64_t o0 = (int64_t)u.to * TO, i0 = (int64_t)u.ti * TI;
+    const bool shared = u.shared;
+    const int64_t t0 = shared ? u.split * a.share : 0, t1 = shared ? min(a.rows, t0 + a.share) : a.rows;
     const int steps = (int)((t1 - t0 + kDepth - 1) / kDepth);
     // Steps whose loads need no test.  Columns beyond the matrix are read from
     // inside it (their results are not written), but for a last group of fewer
@@ -320,47 +342,110 @@ __global__ __launch_bounds__(WO * WI * 64) void weight_grad_kernel(WeightGrad a)
             const int64_t col = i0 + (wi + i) * 16 + lane / 16 * 4;
             const int n = (int)min((int64_t)4, a.cols - col);
             if (n <= 0) continue;
-            if (a.partials) write4<ZERO_F32>(a.partials, (split * a.outs + row) * a.cols + col, n, acc[o][i]);
-            else finish4(a, row * a.cols + col, n, acc[o][i]);
+            if (shared) {
+                // by unit, wave, fragment and lane: whole lines
+                float* p = a.partials + (int64_t)u.part * (TO * TI);
+                *reinterpret_cast<v4f*>(p + (((wave * S::fo + o) * S::fi + i) * 64 + lane) * 4) = acc[o][i];
+            } else {
+                finish4(a, row * a.cols + col, n, acc[o][i]);
+            }
         }
     }
 }
 
-// The splits' sums added in order: four elements per thread.
+// The shares' sums of a tile added in order: four elements per thread.
+template <int TO, int TI, int WO, int WI>
 __global__ __launch_bounds__(256) void weight_join_kernel(WeightGrad a) {
-    const int64_t size = a.outs * a.cols;
-    const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
-    if (at >= size) return;
-    const int n = (int)min((int64_t)4, size - at);
-    v4f sum = read4<ZERO_F32>(a.partials, at, n);
+    using S = Tile<TO, TI, WO, WI>;
+    constexpr uint32_t blocks = TO * TI / 1024;
+    const uint32_t rest = (uint32_t)(a.tiles - a.whole_tiles), nth = blockIdx.x / blocks;
+    const Unit u = unit_of(a, (uint32_t)a.whole_tiles + nth);
+    const int q = (int)(blockIdx.x % blocks) * 256 + threadIdx.x, lane = q & 63, frag = q >> 6;
+    const int i = frag % S::fi, o = frag / S::fi % S::fo, wave = frag / (S::fi * S::fo);
+    const int64_t row = (int64_t)u.to * TO + (wave / WI * S::fo + o) * 16 + lane % 16;
+    const int64_t col = (int64_t)u.ti * TI + (wave % WI * S::fi + i) * 16 + lane / 16 * 4;
+    const int n = (int)min((int64_t)4, a.cols - col);
+    if (row >= a.outs || n <= 0) return;
+    const float* p = a.partials + (int64_t)nth * (TO * TI) + q * 4;
+    v4f sum = *reinterpret_cast<const v4f*>(p);
 #pragma unroll 4
     for (int s = 1; s < a.splits; ++s) {
-        const v4f x = read4<ZERO_F32>(a.partials, s * size + at, n);
+        const v4f x = *reinterpret_cast<const v4f*>(p + (int64_t)s * rest * (TO * TI));
 #pragma unroll
         for (int k = 0; k < 4; ++k) sum[k] += x[k];
     }
-    finish4(a, at, n, sum);
+    finish4(a, row * a.cols + col, n, sum);
 }
 
+template <int DT, int TO, int TI, int WO, int WI>
+int launch_tile(const WeightGrad& a, hipStream_t s) {
+    const int64_t rest = a.tiles - a.whole_tiles;
+    weight_grad_kernel<DT, TO, TI, WO, WI><<<(uint32_t)(a.whole_tiles + rest * a.splits), WO * WI * 64, 0, s>>>(a);
+    if (const int e = (int)hipGetLastError()) return e;
+    if (rest) weight_join_kernel<TO, TI, WO, WI><<<(uint32_t)(rest * (TO * TI / 1024)), 256, 0, s>>>(a);
+    return (int)hipGetLastError();
+}
 template <int DT>
 int launch_dt(const WeightGrad& a, hipStream_t s) {
-    const dim3 grid((uint32_t)(a.tiles * a.splits));
-    if (a.tile == 256) weight_grad_kernel<DT, 256, 256, 2, 4><<<grid, 512, 0, s>>>(a);
-    else weight_grad_kernel<DT, 128, 128, 2, 2><<<grid, 256, 0, s>>>(a);
-    return (int)hipGetLastError();
+    if (a.tile == 256) return launch_tile<DT, 256, 256, 2, 4>(a, s);
+    if (a.tile == 128) return launch_tile<DT, 128, 128, 2, 2>(a, s);
+    return launch_tile<DT, 64, 64, 1, 2>(a, s);
 }
 
 }  // namespace
 
-int launch_weight_grad(const WeightGrad& l, int dtype, void* stream) {
-    const hipStream_t s = static_cast<hipStream_t>(stream);
-    if (const int e = dtype == ZERO_BF16 ? launch_dt<ZERO_BF16>(l, s) : launch_dt<ZERO_F16>(l, s)) return e;
-    if (l.partials) {
-        const int64_t quads = (l.outs * l.cols + 3) / 4;
-        weight_join_kernel<<<(uint32_t)((quads + 255) / 256), 256, 0, s>>>(l);
-        return (int)hipGetLastError();
+// The tile and the split: the least of the times that the measured parts add up to.
+// A tile's blocks fill `slots` places of the chip; whole rounds of tiles are summed
+// by a block each, and the tiles left over, which would leave places empty, may be
+// shared by blocks, whose sums (fp32) cost their writing and reading.  In ns: a step
+// of 32 rows with the chip empty and with every place taken, a block's beginning and
+// end, a share's traffic, the second launch.  Large tiles move fewer bytes per
+// product, small ones spread small gradients over the chip.  Measured, the best split
+// of each, us: 512 x 1024 over 512 rows 10.6, 13.7, 17.5 with tiles of 64, 128, 256;
+// 1024 x 1024 over 8192 rows 43.6, 37.3 with 64, 128; 4096 x 4096 over 2048 rows 96, 67
+// with 128, 256; 4099 x 4001 over 16384 rows 732, 488 (unsplit 906, 825).
+void plan_weight_grad(WeightGrad& a) {
+    struct Kind {
+        int64_t tile, slots, step, step_full, ends, part;
+    };
+    static const Kind kinds[] = {{256, 256, 740, 880, 6000, 86},
+                                 {128, 512, 400, 700, 4500, 22},
+                                 {64, 1024, 400, 500, 4000, 6}};
+    static const int64_t splits[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64, 96};
+    const int64_t steps = (a.rows + 31) / 32;
+    int64_t best = INT64_MAX;
+    for (const Kind& k : kinds) {
+        const int64_t to = (a.outs + k.tile - 1) / k.tile, ti = (a.cols + k.tile - 1) / k.tile, tiles = to * ti;
+        const auto round = [&](int64_t n, int64_t units) {     // n steps of `units` blocks at once
+            return n * (k.step + (k.step_full - k.step) * units / k.slots) + k.ends;
+        };
+        for (const int64_t s : splits) {
+            if (s > 1 && s * 2 > steps) break;
+            const int64_t whole = s == 1 ? tiles : tiles / k.slots * k.slots, rest = tiles - whole;
+            if (s > 1 && rest == 0) break;
+            const int64_t units = rest * s, share = (steps + s - 1) / s;
+            int64_t time = whole / k.slots * round(steps, k.slots);
+            if (whole % k.slots) time += round(steps, whole % k.slots);
+            if (units) {
+                time += units / k.slots * round(share, k.slots) + units * k.part + 3000;
+                if (units % k.slots) time += round(share, units % k.slots);
+            }
+            if (time >= best) continue;
+            best = time;
+            a.tile = (int32_t)k.tile;
+            a.tiles_o = to;
+            a.tiles_i = ti;
+            a.tiles = tiles;
+            a.whole_tiles = whole;
+            a.share = share * 32;
+            a.splits = s == 1 ? 1 : (int32_t)((a.rows + a.share - 1) / a.share);
+        }
     }
-    return 0;
+}
+
+int launch_weight_grad(const WeightGrad& a, int dtype, void* stream) {
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    return dtype == ZERO_BF16 ? launch_dt<ZERO_BF16>(a, s) : launch_dt<ZERO_F16>(a, s);
 }
 
 }  // namespace zf

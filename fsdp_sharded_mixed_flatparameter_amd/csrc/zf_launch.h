@@ -291,28 +291,16 @@ struct WeightGrad {
     const int8_t* codes;
     const uint8_t* exponents;
     void* grad;
-    float* partials;             // splits x outs x cols, or null: one split
+    float* partials;             // the shares' sums, a whole tile each
     int64_t rows, outs, cols, pitch, dy_ld;
-    int64_t share;               // rows of a split
-    int64_t tiles, tiles_i;
+    int64_t share;               // rows of a share
+    int64_t tiles, tiles_o, tiles_i;
+    int64_t whole_tiles;         // tiles that one block sums; the others are shared by `splits` blocks
     int32_t tile, splits, grad_dtype, accumulate;
 };
 int launch_weight_grad(const WeightGrad& a, int dtype, void* stream);
 // The tile and the split, which the sizes alone fix.
-inline void plan_weight_grad(WeightGrad& a) {
-    const auto tiles = [&](int64_t t) { return ((a.outs + t - 1) / t) * ((a.cols + t - 1) / t); };
-    a.tile = tiles(256) >= 128 ? 256 : 128;
-    a.tiles = tiles(a.tile);
-    a.tiles_i = (a.cols + a.tile - 1) / a.tile;
-    const int64_t steps = (a.rows + 63) / 64;
-    int64_t splits = 1;
-    if (a.tiles < 256) splits = 512 / (a.tiles > 0 ? a.tiles : 1);
-    if (splits > steps / 2) splits = steps / 2;
-    if (splits < 1) splits = 1;
-    a.share = (steps + splits - 1) / splits * 64;
-    a.splits = (int32_t)(a.share > 0 ? (a.rows + a.share - 1) / a.share : 1);
-    if (a.splits < 1) a.splits = 1;
-}
+void plan_weight_grad(WeightGrad& a);
 
 // ZeRO-Offload (zeroflat_offload.cpp).  The host update over host arrays:
 // *skipped = 1 (and nothing written) when the state says overflow.

@@ -349,7 +349,11 @@ WHOLE = [  # rows, outs, cols, dy, grad, accumulate, shift, row distance more
     (128, 300, 40, "bf16", "fp32", True, 0, 12), (200, 257, 1000, "fp16", "fp32", False, 5, 0), (1000, 61, 61, "bf16", "fp32", False, 1, 0),
     (5000, 130, 200, "bf16", "fp32", True, 0, 0), (70, 4096, 2085, "bf16", "fp32", False, 1, 0), (513, 2048, 4096, "fp16", "fp32", True, 0, 0),
     (129, 4100, 2049, "bf16", "fp32", True, 0, 5), (0, 20, 40, "bf16", "fp32", False, 0, 0), (0, 20, 40, "bf16", "fp32", True, 0, 0),
-    (30, 0, 40, "bf16", "fp32", False, 0, 0), (30, 20, 0, "bf16", "fp32", False, 0, 0)]
+    (30, 0, 40, "bf16", "fp32", False, 0, 0), (30, 20, 0, "bf16", "fp32", False, 0, 0),
+    # tiles of 256 in two rounds, the second shared, all of them shared; tiles of 128 whole and shared
+    (400, 4099, 4001, "bf16", "fp32", False, 0, 0), (1500, 4099, 4001, "fp16", "fp32", True, 1, 0),
+    (4000, 2048, 2304, "bf16", "fp32", True, 0, 0), (2000, 2050, 2000, "bf16", "fp32", True, 0, 2),
+    (2500, 1000, 1100, "bf16", "fp32", True, 3, 0)]
 
 
 def whole_saved(zf, rows, cols, g):
@@ -402,6 +406,24 @@ def test_weight_grad(zf, rows, outs, cols, shift, dt, gt, accumulate):
     tol = size * rows * 2 * U + want.abs() * U * bool(accumulate)
     half = 0.0 if gt == "fp32" else HALF[gt]
     assert_near(grad, want, tol + (want.abs() + tol) * half + LEAST[gt])
+
+
+@pytest.mark.parametrize("dt,exponent,power", [("bf16", 254, -121), ("bf16", 7, 100), ("fp16", 109, 10),
+                                               ("fp16", 142, -14), ("fp16", 120, 0)])
+@pytest.mark.parametrize("rows,outs,cols", [(40, 20, 70), (300, 200, 130)])
+def test_weight_grad_at_the_ends_of_the_range(zf, rows, outs, cols, dt, exponent, power):
+    """Values of q * 2^(exponent - 133) with the largest and smallest exponents that dy's
+    type holds, and dy small whole numbers times 2^power: exact all the same."""
+    g = gen(exponent)
+    s = whole_saved(zf, rows, cols, g)
+    s.exponents.fill_(exponent)
+    if exponent == 142:
+        s.codes.clamp_(-126, 126)                 # 127 * 2^9 is the largest that fp16 holds without a rounding
+    dy = torch.randint(-3, 4, (rows, outs), generator=g, device="cuda").double()
+    grad = torch.empty(outs, cols, device="cuda")
+    zf.zero_weight_grad8((dy * 2.0 ** power).to(DT[dt]), s, grad)
+    want = torch.matmul(dy.t().contiguous(), s.codes[:, :cols].double()) * 2.0 ** (exponent - 133 + power)
+    assert torch.equal(grad.double(), want)
 
 
 def test_weight_grad_is_the_same_every_time_and_on_its_own_workspace(zf):
