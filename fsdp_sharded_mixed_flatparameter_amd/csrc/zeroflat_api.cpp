@@ -916,9 +916,9 @@ int zero_embed_grad(const void* tokens, int32_t token_bytes, int64_t n_tokens, i
     if (!aligned(dy, esize(dy_dtype)) || !aligned(grad, esize(grad_dtype)))
         return fail(ZERO_EALIGN, "%s: dy or grad not aligned to its element size", fn);
     const zf::EmbedWorkspace w = zf::embed_workspace(n_tokens, vocab, dim);
-    if (!workspace || workspace_bytes < w.bytes)
+    if (w.bytes > 0 && (!workspace || workspace_bytes < w.bytes))
         return fail(ZERO_EINVAL, "%s: the workspace needs %lld bytes", fn, (long long)w.bytes);
-    if (!aligned(workspace, 16)) return fail(ZERO_EALIGN, "%s: workspace not 16-byte aligned", fn);
+    if (w.bytes > 0 && !aligned(workspace, 16)) return fail(ZERO_EALIGN, "%s: workspace not 16-byte aligned", fn);
     zf::EmbedGradLaunch l;
     memset(&l, 0, sizeof l);
     l.sort.tokens = tokens;

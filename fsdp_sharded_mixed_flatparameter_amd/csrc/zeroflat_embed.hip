@@ -1,8 +1,9 @@
 // zeroflat_embed.hip -- gfx950 (MI355X, CDNA4, wave64) kernels of the embedding:
 //   embed_lookup_kernel   rows of the table by token, scaled; the table a view
 //                         of the flat parameter, or the gathered INT8 payload
-//   embed_sort_kernel, embed_hist_kernel, embed_scan_kernel,
-//   embed_scatter_kernel  the tokens' positions sorted by token, stable
+//   embed_few_kernel      the gradient of up to kEmbedFew tokens, in one launch
+//   embed_hist_kernel, embed_scan_kernel, embed_scatter_kernel
+//                         the positions of more, sorted by token, stable
 //   embed_sum_kernel      the gradient's rows summed over runs of equal tokens
 //   embed_join_kernel     the runs that cross tiles
 //
@@ -12,7 +13,14 @@
 // are cut into tiles of one length whatever the tokens are, so that every wave
 // has the same work; a run inside a tile is summed in registers and written
 // once, and one that crosses tiles leaves an fp32 partial row per tile, which
-// the join adds in order.  Every sum's order is fixed by the tokens alone.
+// the join adds in order.  Few tokens need no sort: the wave of a token's first
+// position finds the others by comparing.  Every sum's order is fixed by the
+// tokens alone.
+//
+// Bound by memory: dy once, the written rows once.  The sort's launches move next
+// to nothing and take 25 us; where every row is written, they write zeros
+// meanwhile, to rows that a token names too (those are written again), and the
+// sums' launch to the others that are left.
 #include "zf_vec.h"
 
 namespace zf {
@@ -123,97 +131,31 @@ __device__ __forceinline__ uint32_t key_at(const EmbedSort& a, int64_t i) {
     return token == a.padding && a.has_padding ? (uint32_t)a.vocab : row_of(token, a.first, (uint32_t)a.vocab);
 }
 
-// The whole sort in one block's LDS: up to kEmbedSmall tokens, four per thread,
-// in as many stable passes as the vocabulary's digits need.  Item r * 64 + lane
-// of wave w's 256 keeps the order of the input.
-__global__ __launch_bounds__(1024) void embed_sort_kernel(EmbedSort a) {
-    constexpr int kW = 16, kR = kEmbedSmall / 1024;
-    __shared__ uint32_t keys[kEmbedSmall];
-    __shared__ uint16_t places[kEmbedSmall];
-    __shared__ uint32_t count[kW][kBins];
-    __shared__ uint32_t sums[kW];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int n = (int)a.n_tokens;
-    if (a.flags)
-        for (int i = threadIdx.x; i < a.flag_words; i += 1024) a.flags[i] = 0;
-    uint32_t key[kR], place[kR], rank[kR];
-#pragma unroll
-    for (int r = 0; r < kR; ++r) {
-        place[r] = wave * 64 * kR + r * 64 + lane;
-        key[r] = (int)place[r] < n ? key_at(a, place[r]) : (uint32_t)a.vocab;
-    }
-    __syncthreads();
-    if (a.flags) {
-#pragma unroll
-        for (int r = 0; r < kR; ++r)
-            if (key[r] < (uint32_t)a.vocab) reinterpret_cast<uint8_t*>(a.flags)[key[r]] = 1;
-    }
-    for (int p = 0; p < a.passes; ++p) {
-        for (int i = threadIdx.x; i < kW * kBins; i += 1024) (&count[0][0])[i] = 0;
-        __syncthreads();
-        const uint32_t mask = (1u << a.digit_bits) - 1, shift = p * a.digit_bits;
-#pragma unroll
-        for (int r = 0; r < kR; ++r) {
-            const bool live = (int)(wave * 64 * kR + r * 64 + lane) < n;
-            const uint32_t d = (key[r] >> shift) & mask;
-            const uint64_t m = same_digit(d, a.digit_bits, live);
-            const int below = __popcll(m & ((1ull << lane) - 1));
-            const uint32_t had = live ? count[wave][d] : 0;
-            rank[r] = had + below;
-            __syncthreads();
-            if (live && below == 0) count[wave][d] = had + __popcll(m);
-            __syncthreads();
-        }
-        // digits' totals, then each wave's first place of each digit
-        uint32_t mine = 0, all;
-        if (threadIdx.x < kBins)
-            for (int w = 0; w < kW; ++w) mine += count[w][threadIdx.x];
-        uint32_t at = block_scan<kW>(mine, sums, &all);
-        if (threadIdx.x < kBins)
-            for (int w = 0; w < kW; ++w) {
-                const uint32_t c = count[w][threadIdx.x];
-                count[w][threadIdx.x] = at;
-                at += c;
-            }
-        __syncthreads();
-#pragma unroll
-        for (int r = 0; r < kR; ++r) {
-            if ((int)(wave * 64 * kR + r * 64 + lane) < n) {
-                const uint32_t to = count[wave][(key[r] >> shift) & mask] + rank[r];
-                keys[to] = key[r];
-                places[to] = (uint16_t)place[r];
-            }
-        }
-        __syncthreads();
-#pragma unroll
-        for (int r = 0; r < kR; ++r) {
-            const int i = wave * 64 * kR + r * 64 + lane;
-            if (i < n) {
-                key[r] = keys[i];
-                place[r] = places[i];
-            }
-        }
-        __syncthreads();
-    }
-#pragma unroll
-    for (int r = 0; r < kR; ++r) {
-        const int i = wave * 64 * kR + r * 64 + lane;
-        if (i < n) {
-            a.keys_out[i] = key[r];
-            a.places_out[i] = (int32_t)place[r];
-        }
+// Zeros over [first, last) bytes of a gradient, both multiples of two: 16 KiB a
+// block, 16 bytes a lane and store at any address.
+constexpr int64_t kZeroBlock = 16384;
+__device__ __forceinline__ void zero_bytes(char* grad, int64_t first, int64_t last, int64_t block) {
+    const int64_t from = first + block * kZeroBlock, to = min(last, from + kZeroBlock);
+    for (int64_t at = from + threadIdx.x * 16; at < to; at += kThreads * 16) {
+        if (at + 16 <= to) *reinterpret_cast<v4u_any*>(grad + at) = v4u{0, 0, 0, 0};
+        else
+            for (int64_t b = at; b < to; b += 2) *reinterpret_cast<uint16_t*>(grad + b) = 0;
     }
 }
 
-// One pass over a long list, first half: how many of each digit a block of
+// One pass, first half: how many of each digit a block of
 // kEmbedSortTile items holds.  The first pass reads the tokens and clears the
 // rows' marks.
 __global__ __launch_bounds__(kThreads) void embed_hist_kernel(EmbedSort a) {
     __shared__ uint32_t count[kBins];
+    if (blockIdx.x >= (uint32_t)a.blocks) {
+        zero_bytes(a.grad, a.zero_first, a.zero_last, blockIdx.x - a.blocks);
+        return;
+    }
     count[threadIdx.x] = 0;
     if (a.pass == 0 && a.flags)
         for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < a.flag_words;
-             i += (int64_t)gridDim.x * kThreads)
+             i += (int64_t)a.blocks * kThreads)
             a.flags[i] = 0;
     __syncthreads();
     const uint32_t mask = (1u << a.digit_bits) - 1, shift = a.pass * a.digit_bits;
@@ -251,6 +193,10 @@ __global__ __launch_bounds__(kThreads) void embed_scan_kernel(EmbedSort a) {
 __global__ __launch_bounds__(kThreads) void embed_scatter_kernel(EmbedSort a) {
     __shared__ uint32_t count[kWaves][kBins];
     __shared__ uint32_t sums[kWaves];
+    if (blockIdx.x >= (uint32_t)a.blocks) {
+        zero_bytes(a.grad, a.zero_first, a.zero_last, blockIdx.x - a.blocks);
+        return;
+    }
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     uint32_t before = 0, total = 0;
     if (a.scanned) {
@@ -335,8 +281,8 @@ __global__ __launch_bounds__(kThreads) void embed_sum_kernel(EmbedSum a) {
     const int lane = threadIdx.x & 63;
     const int64_t unit = (int64_t)blockIdx.x * kWaves + uniform(threadIdx.x >> 6);
     if (unit >= a.sum_units) {
-        const int64_t v = unit - a.sum_units;
-        if (v >= a.zero_rows || as_const(reinterpret_cast<const uint8_t*>(a.flags))[v]) return;
+        const int64_t v = a.zero_from + unit - a.sum_units;
+        if (v >= a.vocab || as_const(reinterpret_cast<const uint8_t*>(a.flags))[v]) return;
         const float zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
         for (int64_t col = lane * 8; col < a.dim; col += kChunk)
             store8<TG>(a.grad, v * a.dim + col, (int)min((int64_t)8, a.dim - col), zero);
@@ -438,6 +384,117 @@ __global__ __launch_bounds__(kThreads) void embed_join_kernel(EmbedSum a) {
     write_row<TG>(a, k, col, n, acc);
 }
 
+// The gradient of up to kEmbedFew tokens, without a sort.  The block holds every
+// token's row; its wave w looks for the others of position 8 * block + w.  The wave
+// that has the first of them sums them all in order, or, of more than kEmbedLong,
+// leaves them to the whole block: each wave an eighth of the positions, the eighths
+// added in order.  The blocks behind write zeros to the rows without a token, 64
+// each.  One launch, whose time is the chain of tokens, comparisons, rows.
+constexpr int kFewWaves = 8, kFewThreads = kFewWaves * 64, kEmbedLong = 32, kFewRows = 64;
+
+template <int TD, int TG>
+__global__ __launch_bounds__(kFewThreads) void embed_few_kernel(EmbedSort t, EmbedSum a) {
+    __shared__ uint32_t keys[kEmbedFew];
+    __shared__ uint16_t list[kFewWaves][kEmbedFew / kFewWaves];
+    __shared__ float part[kFewWaves][kChunk];
+    __shared__ uint32_t longs[kFewWaves];
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+    const int n = (int)t.n_tokens, blocks = (n + kFewWaves - 1) / kFewWaves;
+    const uint32_t none = (uint32_t)t.vocab;
+    if ((int)blockIdx.x >= blocks) {
+        const uint32_t v0 = (blockIdx.x - blocks) * kFewRows;
+        if (threadIdx.x < kFewRows) keys[threadIdx.x] = 0;
+        __syncthreads();
+        for (int i = threadIdx.x; i < n; i += kFewThreads) {
+            const uint32_t k = key_at(t, i);
+            if (k - v0 < (uint32_t)kFewRows) keys[k - v0] = 1;
+        }
+        __syncthreads();
+        const float zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        for (int r = wave; r < kFewRows; r += kFewWaves) {
+            const int64_t v = (int64_t)v0 + r;
+            if (v >= t.vocab) break;
+            if (keys[r]) continue;
+            for (int64_t col = lane * 8; col < a.dim; col += kChunk)
+                store8<TG>(a.grad, v * a.dim + col, (int)min((int64_t)8, a.dim - col), zero);
+        }
+        return;
+    }
+    for (int i = threadIdx.x; i < n; i += kFewThreads) keys[i] = key_at(t, i);
+    __syncthreads();
+    const int mine = blockIdx.x * kFewWaves + wave;
+    const uint32_t key = mine < n ? (uint32_t)uniform((int)keys[mine]) : none;
+    // positions of `k` within [from, to) into this wave's list, in order
+    auto gather = [&](uint32_t k, int from, int to) {
+        int have = 0;
+        for (int j = from; j < to; j += 64) {
+            const bool hit = j + lane < to && keys[j + lane] == k;
+            const uint64_t m = __ballot(hit);
+            if (hit) list[wave][have + __popcll(m & ((1ull << lane) - 1))] = (uint16_t)(j + lane);
+            have += __popcll(m);
+        }
+        return have;
+    };
+    auto sum = [&](int have, int64_t col, int cols, float (&acc)[8]) {
+        for (int j0 = 0; j0 < have; j0 += kEmbedBatch) {
+            float x[kEmbedBatch][8];
+#pragma unroll
+            for (int j = 0; j < kEmbedBatch; ++j)
+                if (j0 + j < have && cols > 0)
+                    load8<TD>(a.dy, (int64_t)uniform(list[wave][j0 + j]) * a.dy_ld + col, cols, x[j]);
+#pragma unroll
+            for (int j = 0; j < kEmbedBatch; ++j)
+                if (j0 + j < have)
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) acc[c] += x[j][c];
+        }
+    };
+    // the first of its token?  how many are there?
+    int count = 0;
+    if (key != none) {
+        bool first = true;
+        for (int j = 0; j < mine && first; j += 64) first = __ballot(j + lane < mine && keys[j + lane] == key) == 0;
+        if (first)
+            for (int j = mine; j < n; j += 64) count += __popcll(__ballot(j + lane < n && keys[j + lane] == key));
+    }
+    if (count > 0 && count <= kEmbedLong) {
+        gather(key, mine, n);
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        for (int64_t c0 = 0; c0 < a.dim; c0 += kChunk) {
+            const int64_t col = c0 + lane * 8;
+            const int cols = (int)min((int64_t)8, a.dim - col);
+            float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+            sum(count, col, cols, acc);
+            if (cols > 0) write_row<TG>(a, key, col, cols, acc);
+        }
+    }
+    if (lane == 0) longs[wave] = count > kEmbedLong ? key : none;
+    __syncthreads();
+    for (int w = 0; w < kFewWaves; ++w) {
+        const uint32_t k = (uint32_t)uniform((int)longs[w]);
+        if (k == none) continue;
+        const int share = (n + kFewThreads - 1) / kFewThreads * 64;
+        const int have = gather(k, min(n, wave * share), min(n, (wave + 1) * share));
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        for (int64_t c0 = 0; c0 < a.dim; c0 += kChunk) {
+            const int64_t col = c0 + lane * 8;
+            const int cols = (int)min((int64_t)8, a.dim - col);
+            float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+            sum(have, col, cols, acc);
+            *reinterpret_cast<v4f*>(&part[wave][lane * 8]) = v4f{acc[0], acc[1], acc[2], acc[3]};
+            *reinterpret_cast<v4f*>(&part[wave][lane * 8 + 4]) = v4f{acc[4], acc[5], acc[6], acc[7]};
+            __syncthreads();
+            if (wave == 0 && cols > 0) {
+                for (int u = 1; u < kFewWaves; ++u)
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) acc[c] += part[u][lane * 8 + c];
+                write_row<TG>(a, k, col, cols, acc);
+            }
+            __syncthreads();
+        }
+    }
+}
+
 int last_error() { return (int)hipGetLastError(); }
 
 template <int TT>
@@ -452,6 +509,13 @@ void sum_to(const EmbedSum& a, int grad, dim3 grid, hipStream_t s) {
     if (grad == ZERO_F32) embed_sum_kernel<TD, ZERO_F32><<<grid, kThreads, 0, s>>>(a);
     else if (grad == ZERO_F16) embed_sum_kernel<TD, ZERO_F16><<<grid, kThreads, 0, s>>>(a);
     else embed_sum_kernel<TD, ZERO_BF16><<<grid, kThreads, 0, s>>>(a);
+}
+
+template <int TD>
+void few_to(const EmbedSort& t, const EmbedSum& a, int grad, dim3 grid, hipStream_t s) {
+    if (grad == ZERO_F32) embed_few_kernel<TD, ZERO_F32><<<grid, kFewThreads, 0, s>>>(t, a);
+    else if (grad == ZERO_F16) embed_few_kernel<TD, ZERO_F16><<<grid, kFewThreads, 0, s>>>(t, a);
+    else embed_few_kernel<TD, ZERO_BF16><<<grid, kFewThreads, 0, s>>>(t, a);
 }
 
 }  // namespace
@@ -481,8 +545,16 @@ int launch_embed_lookup(const EmbedLookupLaunch& l, void* stream) {
 
 int launch_embed_grad(const EmbedGradLaunch& l, void* stream) {
     const hipStream_t s = static_cast<hipStream_t>(stream);
-    char* ws = static_cast<char*>(l.workspace);
     EmbedSort a = l.sort;
+    if (a.n_tokens <= kEmbedFew) {
+        const int64_t rows = l.sum.accumulate ? 0 : a.vocab;
+        const dim3 grid((uint32_t)((a.n_tokens + kFewWaves - 1) / kFewWaves + (rows + kFewRows - 1) / kFewRows));
+        if (l.dy_dtype == ZERO_F32) few_to<ZERO_F32>(a, l.sum, l.grad_dtype, grid, s);
+        else if (l.dy_dtype == ZERO_F16) few_to<ZERO_F16>(a, l.sum, l.grad_dtype, grid, s);
+        else few_to<ZERO_BF16>(a, l.sum, l.grad_dtype, grid, s);
+        return last_error();
+    }
+    char* ws = static_cast<char*>(l.workspace);
     const EmbedWorkspace w = embed_workspace(a.n_tokens, a.vocab, l.sum.dim);
     uint32_t* keys[2] = {reinterpret_cast<uint32_t*>(ws + w.keys[0]), reinterpret_cast<uint32_t*>(ws + w.keys[1])};
     int32_t* places[2] = {reinterpret_cast<int32_t*>(ws + w.places[0]), reinterpret_cast<int32_t*>(ws + w.places[1])};
@@ -495,28 +567,32 @@ int launch_embed_grad(const EmbedGradLaunch& l, void* stream) {
     a.digit_bits = (bits + a.passes - 1) / a.passes;
     a.blocks = (int32_t)((a.n_tokens + kEmbedSortTile - 1) / kEmbedSortTile);
     a.scanned = a.blocks > kEmbedScanBlocks;
+    // each launch of the sort writes so many bytes of zeros beside its work
+    const int64_t row_bytes = l.sum.dim * (l.grad_dtype == ZERO_F32 ? 4 : 2);
+    const int64_t total = l.sum.accumulate ? 0 : a.vocab * row_bytes;
+    a.grad = static_cast<char*>(l.sum.grad);
+    const auto grid = [&]() {
+        a.zero_first = a.zero_last;
+        a.zero_last = total - a.zero_first < kEmbedZeroBytes ? total : a.zero_first + kEmbedZeroBytes;
+        return dim3((uint32_t)(a.blocks + (a.zero_last - a.zero_first + kZeroBlock - 1) / kZeroBlock));
+    };
     int at = 0;
-    if (a.n_tokens <= kEmbedSmall) {
-        a.keys_out = keys[0];
-        a.places_out = places[0];
-        embed_sort_kernel<<<1, 1024, 0, s>>>(a);
+    for (a.pass = 0; a.pass < a.passes; ++a.pass) {
+        a.keys_in = keys[at];
+        a.places_in = places[at];
+        at ^= 1;
+        a.keys_out = keys[at];
+        a.places_out = places[at];
+        dim3 blocks = grid();
+        embed_hist_kernel<<<blocks, kThreads, 0, s>>>(a);
         if (const int e = last_error()) return e;
-    } else {
-        for (a.pass = 0; a.pass < a.passes; ++a.pass) {
-            a.keys_in = keys[at];
-            a.places_in = places[at];
-            at ^= 1;
-            a.keys_out = keys[at];
-            a.places_out = places[at];
-            embed_hist_kernel<<<a.blocks, kThreads, 0, s>>>(a);
-            if (const int e = last_error()) return e;
-            if (a.scanned) {
-                embed_scan_kernel<<<kBins, kThreads, 0, s>>>(a);
-                if (const int e = last_error()) return e;
-            }
-            embed_scatter_kernel<<<a.blocks, kThreads, 0, s>>>(a);
+        if (a.scanned) {
+            embed_scan_kernel<<<kBins, kThreads, 0, s>>>(a);
             if (const int e = last_error()) return e;
         }
+        blocks = grid();
+        embed_scatter_kernel<<<blocks, kThreads, 0, s>>>(a);
+        if (const int e = last_error()) return e;
     }
     EmbedSum b = l.sum;
     b.keys = keys[at];
@@ -530,11 +606,12 @@ int launch_embed_grad(const EmbedGradLaunch& l, void* stream) {
     b.pitch = w.pitch;
     b.chunks = (b.dim + kChunk - 1) / kChunk;
     b.sum_units = b.tiles * b.chunks;
-    b.zero_rows = b.accumulate ? 0 : b.vocab;
-    const dim3 grid((uint32_t)((b.sum_units + b.zero_rows + kWaves - 1) / kWaves));
-    if (l.dy_dtype == ZERO_F32) sum_to<ZERO_F32>(b, l.grad_dtype, grid, s);
-    else if (l.dy_dtype == ZERO_F16) sum_to<ZERO_F16>(b, l.grad_dtype, grid, s);
-    else sum_to<ZERO_BF16>(b, l.grad_dtype, grid, s);
+    // rows that are zero already need no more of it; one that is so in part does
+    b.zero_from = b.accumulate ? b.vocab : a.zero_last / row_bytes;
+    const dim3 sums((uint32_t)((b.sum_units + b.vocab - b.zero_from + kWaves - 1) / kWaves));
+    if (l.dy_dtype == ZERO_F32) sum_to<ZERO_F32>(b, l.grad_dtype, sums, s);
+    else if (l.dy_dtype == ZERO_F16) sum_to<ZERO_F16>(b, l.grad_dtype, sums, s);
+    else sum_to<ZERO_BF16>(b, l.grad_dtype, sums, s);
     if (const int e = last_error()) return e;
     if (b.tiles > 1) {
         const dim3 joins((uint32_t)(b.tiles - 1), (uint32_t)b.chunks);

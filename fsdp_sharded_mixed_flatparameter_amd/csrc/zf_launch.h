@@ -171,8 +171,9 @@ int launch_multi_step(const MultiAdamLaunch& a, const MultiNormLaunch* norm, con
 
 // The embedding (zeroflat_embed.hip).
 constexpr int kEmbedInt8 = 3;            // a table's type beside zero_dtype_t: the INT8 payload
-constexpr int kEmbedSmall = 4096;        // tokens that one block sorts by itself
-constexpr int kEmbedSortTile = 1024;     // tokens of one block of the long sort
+constexpr int kEmbedFew = 4096;          // tokens whose gradient needs no sort
+constexpr int kEmbedSortTile = 1024;     // tokens of one block of the sort
+constexpr int64_t kEmbedZeroBytes = 40 << 20;   // of zeros that a launch of the sort writes beside it
 constexpr int kEmbedScanBlocks = 128;    // blocks that sum the counts before theirs themselves
 constexpr int kEmbedBatch = 8;           // rows that a wave of the sums has in flight
 
@@ -210,6 +211,8 @@ struct EmbedSort {
     uint32_t* hist;
     uint32_t* flags;        // a byte per row, 1 where a token names it; null: not asked for
     int64_t flag_words;
+    char* grad;             // zeros go to bytes [zero_first, zero_last) of it
+    int64_t zero_first, zero_last;
     int32_t wide, has_padding, passes, pass, digit_bits, blocks, scanned;
 };
 struct EmbedSum {
@@ -219,7 +222,8 @@ struct EmbedSum {
     const void* dy;
     void* grad;
     float* partials;        // two fp32 rows of `pitch` per tile: a run from before, a run that goes on
-    int64_t n_tokens, vocab, dim, dy_ld, pitch, tiles, chunks, sum_units, zero_rows;
+    int64_t n_tokens, vocab, dim, dy_ld, pitch, tiles, chunks, sum_units;
+    int64_t zero_from;      // the first row that may need zeros yet
     int32_t tile;           // sorted positions of one tile
     int32_t accumulate;
     float scale;
@@ -242,6 +246,7 @@ struct EmbedWorkspace {
 // beside its rows, short enough that few tokens spread over the chip.
 inline EmbedWorkspace embed_workspace(int64_t n, int64_t vocab, int64_t dim) {
     EmbedWorkspace w{};
+    if (n <= kEmbedFew) return w;
     const auto up = [](int64_t x) { return (x + 255) / 256 * 256; };
     w.tile = n * ((dim + 511) / 512) >= 65536 ? 32 : 8;
     w.tiles = (n + w.tile - 1) / w.tile;

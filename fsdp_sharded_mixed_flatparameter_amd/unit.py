@@ -162,7 +162,7 @@ def zero_embed_lookup_int8(tokens, q_buf, q_scales, n_slots, slot_numel, elem_of
 
 @functools.lru_cache(maxsize=256)
 def zero_embed_grad_workspace(n_tokens, vocab, dim):
-    """The bytes of workspace that zero_embed_grad needs."""
+    """The bytes of workspace that zero_embed_grad needs (0 for few tokens)."""
     b = C.c_int64(0)
     _check(_lib.zero_embed_grad_workspace(n_tokens, vocab, dim, C.byref(b)))
     return b.value
@@ -183,11 +183,14 @@ def zero_embed_grad(tokens, dy, grad, scale=1.0, first=0, padding=None, accumula
     d = _rows(dy, "dy", n, dim, _FLOATS, here)
     _apart(g, d, "grad", "dy")
     _apart(g, t, "grad", "tokens")
-    handle = _on(stream)
-    ws = _scratch(workspace, zero_embed_grad_workspace(n, vocab, dim), grad.device, here, stream, handle)
+    handle, ws, size = _on(stream), None, 0
+    need = zero_embed_grad_workspace(n, vocab, dim)
+    if need or workspace is not None:
+        ws = _scratch(workspace, need, grad.device, here, stream, handle)
+        ws, size = ws.data_ptr(), ws.numel()
     pad = None if padding is None else C.byref(C.c_int64(padding))
     rc = _lib.zero_embed_grad(t[0], t[2], n, first, pad, d[0], d[2], d[3], scale, g[0], g[2], vocab, dim,
-                              ZERO_ACCUMULATE if accumulate else 0, ws.data_ptr(), ws.numel(), handle)
+                              ZERO_ACCUMULATE if accumulate else 0, ws, size, handle)
     if rc:
         _check(rc)
 
