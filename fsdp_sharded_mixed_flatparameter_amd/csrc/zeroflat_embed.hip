@@ -137,7 +137,7 @@ constexpr int64_t kZeroBlock = 16384;
 __device__ __forceinline__ void zero_bytes(char* grad, int64_t first, int64_t last, int64_t block) {
     const int64_t from = first + block * kZeroBlock, to = min(last, from + kZeroBlock);
     for (int64_t at = from + threadIdx.x * 16; at < to; at += kThreads * 16) {
-        if (at + 16 <= to) *reinterpret_cast<v4u_any*>(grad + at) = v4u{0, 0, 0, 0};
+        if (at + 16 <= to) __builtin_nontemporal_store(v4u_any{0, 0, 0, 0}, reinterpret_cast<v4u_any*>(grad + at));
         else
             for (int64_t b = at; b < to; b += 2) *reinterpret_cast<uint16_t*>(grad + b) = 0;
     }
@@ -203,11 +203,17 @@ __global__ __launch_bounds__(kThreads) void embed_scatter_kernel(EmbedSort a) {
         before = a.hist[(int64_t)blockIdx.x * kBins + threadIdx.x];
         total = a.hist[(int64_t)a.blocks * kBins + threadIdx.x];
     } else {
-#pragma unroll 8
-        for (int b = 0; b < a.blocks; ++b) {
-            const uint32_t c = a.hist[(int64_t)b * kBins + threadIdx.x];
-            total += c;
-            if (b < (int)blockIdx.x) before += c;
+        // 32 loads at a time: one after the other they took half the kernel
+        for (int b0 = 0; b0 < a.blocks; b0 += 32) {
+            uint32_t c[32];
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+                c[k] = b0 + k < a.blocks ? a.hist[(int64_t)(b0 + k) * kBins + threadIdx.x] : 0;
+#pragma unroll
+            for (int k = 0; k < 32; ++k) {
+                total += c[k];
+                if (b0 + k < (int)blockIdx.x) before += c[k];
+            }
         }
     }
 #pragma unroll
@@ -235,10 +241,12 @@ __global__ __launch_bounds__(kThreads) void embed_scatter_kernel(EmbedSort a) {
         const int below = __popcll(m & ((1ull << lane) - 1));
         const uint32_t had = live ? count[wave][d] : 0;
         rank[r] = had + below;
-        __syncthreads();
+        // a wave's own counts, and its LDS operations keep their order
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         if (live && below == 0) count[wave][d] = had + __popcll(m);
-        __syncthreads();
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
+    __syncthreads();
     uint32_t at = base;
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) {
@@ -352,13 +360,16 @@ __global__ __launch_bounds__(kThreads) void embed_join_kernel(EmbedSum a) {
     const uint32_t k = keys[base + a.tile - 1];            // every tile but the last is full
     if (k == (uint32_t)a.vocab || keys[base + a.tile] != k) return;
     if (tile > 0 && keys[base] == k && keys[base - 1] == k) return;
-    int64_t lo = tile + 1, hi = a.tiles - 1;               // the last tile whose first key is k
-    while (lo < hi) {
-        const int64_t mid = (lo + hi + 1) / 2;
-        if (keys[mid * a.tile] == k) lo = mid;
-        else hi = mid - 1;
-    }
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+    // the last tile whose first key is k: 64 tiles a look, as the search is a chain of loads
+    int64_t lo = tile + 1;
+    for (;;) {
+        const int64_t t = lo + 1 + lane;
+        const uint64_t on = __ballot(t < a.tiles && a.keys[t * a.tile] == k);
+        const int more = on == ~0ull ? 64 : __builtin_ctzll(~on);
+        lo += more;
+        if (more < 64) break;
+    }
     const int64_t col = (int64_t)blockIdx.y * kChunk + lane * 8;
     const int n = (int)min((int64_t)8, a.dim - col);
     const int64_t many = lo - tile + 1, share = (many + kWaves - 1) / kWaves;
@@ -390,7 +401,7 @@ __global__ __launch_bounds__(kThreads) void embed_join_kernel(EmbedSum a) {
 // leaves them to the whole block: each wave an eighth of the positions, the eighths
 // added in order.  The blocks behind write zeros to the rows without a token, 64
 // each.  One launch, whose time is the chain of tokens, comparisons, rows.
-constexpr int kFewWaves = 8, kFewThreads = kFewWaves * 64, kEmbedLong = 32, kFewRows = 64;
+constexpr int kFewWaves = 8, kFewThreads = kFewWaves * 64, kEmbedLong = 16, kFewRows = 64, kFewBatch = 16;
 
 template <int TD, int TG>
 __global__ __launch_bounds__(kFewThreads) void embed_few_kernel(EmbedSort t, EmbedSum a) {
@@ -436,14 +447,14 @@ __global__ __launch_bounds__(kFewThreads) void embed_few_kernel(EmbedSort t, Emb
         return have;
     };
     auto sum = [&](int have, int64_t col, int cols, float (&acc)[8]) {
-        for (int j0 = 0; j0 < have; j0 += kEmbedBatch) {
-            float x[kEmbedBatch][8];
+        for (int j0 = 0; j0 < have; j0 += kFewBatch) {
+            float x[kFewBatch][8];
 #pragma unroll
-            for (int j = 0; j < kEmbedBatch; ++j)
+            for (int j = 0; j < kFewBatch; ++j)
                 if (j0 + j < have && cols > 0)
                     load8<TD>(a.dy, (int64_t)uniform(list[wave][j0 + j]) * a.dy_ld + col, cols, x[j]);
 #pragma unroll
-            for (int j = 0; j < kEmbedBatch; ++j)
+            for (int j = 0; j < kFewBatch; ++j)
                 if (j0 + j < have)
 #pragma unroll
                     for (int c = 0; c < 8; ++c) acc[c] += x[j][c];
