@@ -132,11 +132,12 @@ __device__ __forceinline__ Place place_of(uint32_t g, const Div& per_row, int64_
     return p;
 }
 __device__ __forceinline__ void keep(const float (&x)[8], int least, int8_t* codes, uint8_t* exponents,
-                                     uint32_t g) {
+                                     uint32_t g, int stream) {
     v2u c;
     uint32_t e;
     quantise(x, least, c, e);
-    reinterpret_cast<v2u*>(codes)[g] = c;
+    if (stream) __builtin_nontemporal_store(c, reinterpret_cast<v2u*>(codes) + g);
+    else reinterpret_cast<v2u*>(codes)[g] = c;
     if ((g & 3) == 0) exponents[g >> 2] = (uint8_t)e;
 }
 
@@ -151,8 +152,8 @@ __global__ __launch_bounds__(kThreads) void act_forward_kernel(ActLaunch a) {
     load8<DT>(a.x, (int64_t)p.row * a.x_ld + p.col, p.n, x);
     float u[8];
     if constexpr (GATED) load8<DT>(a.up, (int64_t)p.row * a.up_ld + p.col, p.n, u);
-    keep(x, a.least, a.codes, a.exponents, g);
-    if constexpr (GATED) keep(u, a.least, a.up_codes, a.up_exponents, g);
+    keep(x, a.least, a.codes, a.exponents, g, 1);
+    if constexpr (GATED) keep(u, a.least, a.up_codes, a.up_exponents, g, 1);
     if constexpr (KIND >= 0) {
         if (p.n <= 0) return;
         float y[8];
@@ -162,7 +163,7 @@ __global__ __launch_bounds__(kThreads) void act_forward_kernel(ActLaunch a) {
             act<KIND>(x[k], y[k], slope);
             if constexpr (GATED) y[k] *= u[k];
         }
-        store8<DT>(a.y, (int64_t)p.row * a.y_ld + p.col, p.n, y);
+        store8<DT>(a.y, (int64_t)p.row * a.y_ld + p.col, p.n, y, a.stream);
     }
 }
 
@@ -181,7 +182,7 @@ __global__ __launch_bounds__(kThreads) void act_backward_kernel(ActLaunch a) {
         restore(cu, a.up_exponents[g >> 2], u);
     }
     if constexpr (KIND < 0) {
-        if (p.n > 0) store8<DT>(a.y, (int64_t)p.row * a.y_ld + p.col, p.n, x);
+        if (p.n > 0) store8<DT>(a.y, (int64_t)p.row * a.y_ld + p.col, p.n, x, a.stream);
     } else {
         float dx[8], du[8], y[8];
 #pragma unroll
@@ -197,14 +198,14 @@ __global__ __launch_bounds__(kThreads) void act_backward_kernel(ActLaunch a) {
             }
         }
         if (p.n > 0) {
-            store8<DT>(a.y, (int64_t)p.row * a.y_ld + p.col, p.n, dx);
-            if constexpr (GATED) store8<DT>(a.dup, (int64_t)p.row * a.dup_ld + p.col, p.n, du);
+            store8<DT>(a.y, (int64_t)p.row * a.y_ld + p.col, p.n, dx, a.stream);
+            if constexpr (GATED) store8<DT>(a.dup, (int64_t)p.row * a.dup_ld + p.col, p.n, du, a.stream);
         }
         if (a.again_codes) {
             // columns beyond the matrix stand for 0 whatever the function makes of 0
 #pragma unroll
             for (int k = 0; k < 8; ++k) y[k] = k < p.n ? y[k] : 0.0f;
-            keep(y, a.least, a.again_codes, a.again_exponents, g);
+            keep(y, a.least, a.again_codes, a.again_exponents, g, 0);
         }
     }
 }
@@ -245,6 +246,7 @@ int launch_act(const ActLaunch& l, int backward, void* stream) {
         const int64_t n = l.rows - r < most ? l.rows - r : most;
         ActLaunch a = l;
         a.per_row = make_div((uint32_t)per_row);
+        a.stream = streams(l.rows * l.cols * size * (l.dup ? 2 : 1));
         a.groups = (uint32_t)(n * per_row);
         a.x = moved(l.x, r * l.x_ld * size);
         a.up = moved(l.up, r * l.up_ld * size);

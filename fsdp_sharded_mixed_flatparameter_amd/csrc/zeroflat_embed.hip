@@ -88,7 +88,7 @@ __global__ __launch_bounds__(kThreads) void embed_lookup_kernel(EmbedLookup a) {
 #pragma unroll
         for (int k = 0; k < 8; ++k) x[k] *= a.scale;
     }
-    store8<TO>(a.out, (int64_t)t * a.out_ld + col, n, x);
+    store8<TO>(a.out, (int64_t)t * a.out_ld + col, n, x, a.stream);
 }
 
 // ---------------------------------------------------------------- sort
@@ -134,10 +134,12 @@ __device__ __forceinline__ uint32_t key_at(const EmbedSort& a, int64_t i) {
 // Zeros over [first, last) bytes of a gradient, both multiples of two: 16 KiB a
 // block, 16 bytes a lane and store at any address.
 constexpr int64_t kZeroBlock = 16384;
-__device__ __forceinline__ void zero_bytes(char* grad, int64_t first, int64_t last, int64_t block) {
+__device__ __forceinline__ void zero_bytes(char* grad, int64_t first, int64_t last, int64_t block, int stream) {
     const int64_t from = first + block * kZeroBlock, to = min(last, from + kZeroBlock);
     for (int64_t at = from + threadIdx.x * 16; at < to; at += kThreads * 16) {
-        if (at + 16 <= to) __builtin_nontemporal_store(v4u_any{0, 0, 0, 0}, reinterpret_cast<v4u_any*>(grad + at));
+        v4u_any* p = reinterpret_cast<v4u_any*>(grad + at);
+        if (at + 16 <= to && stream) __builtin_nontemporal_store(v4u_any{0, 0, 0, 0}, p);
+        else if (at + 16 <= to) *p = v4u_any{0, 0, 0, 0};
         else
             for (int64_t b = at; b < to; b += 2) *reinterpret_cast<uint16_t*>(grad + b) = 0;
     }
@@ -149,7 +151,7 @@ __device__ __forceinline__ void zero_bytes(char* grad, int64_t first, int64_t la
 __global__ __launch_bounds__(kThreads) void embed_hist_kernel(EmbedSort a) {
     __shared__ uint32_t count[kBins];
     if (blockIdx.x >= (uint32_t)a.blocks) {
-        zero_bytes(a.grad, a.zero_first, a.zero_last, blockIdx.x - a.blocks);
+        zero_bytes(a.grad, a.zero_first, a.zero_last, blockIdx.x - a.blocks, a.stream);
         return;
     }
     count[threadIdx.x] = 0;
@@ -194,7 +196,7 @@ __global__ __launch_bounds__(kThreads) void embed_scatter_kernel(EmbedSort a) {
     __shared__ uint32_t count[kWaves][kBins];
     __shared__ uint32_t sums[kWaves];
     if (blockIdx.x >= (uint32_t)a.blocks) {
-        zero_bytes(a.grad, a.zero_first, a.zero_last, blockIdx.x - a.blocks);
+        zero_bytes(a.grad, a.zero_first, a.zero_last, blockIdx.x - a.blocks, a.stream);
         return;
     }
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -279,7 +281,7 @@ __device__ __forceinline__ void write_row(const EmbedSum& a, uint32_t row, int64
 #pragma unroll
         for (int k = 0; k < 8; ++k) y[k] += old[k];
     }
-    store8<TG>(a.grad, at, n, y);
+    store8<TG>(a.grad, at, n, y, a.stream);
 }
 
 // A wave takes a tile of a.tile sorted positions and 512 columns; the waves
@@ -293,7 +295,7 @@ __global__ __launch_bounds__(kThreads) void embed_sum_kernel(EmbedSum a) {
         if (v >= a.vocab || as_const(reinterpret_cast<const uint8_t*>(a.flags))[v]) return;
         const float zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
         for (int64_t col = lane * 8; col < a.dim; col += kChunk)
-            store8<TG>(a.grad, v * a.dim + col, (int)min((int64_t)8, a.dim - col), zero);
+            store8<TG>(a.grad, v * a.dim + col, (int)min((int64_t)8, a.dim - col), zero, a.stream);
         return;
     }
     const int64_t tile = unit / a.chunks;
@@ -427,7 +429,7 @@ __global__ __launch_bounds__(kFewThreads) void embed_few_kernel(EmbedSort t, Emb
             if (v >= t.vocab) break;
             if (keys[r]) continue;
             for (int64_t col = lane * 8; col < a.dim; col += kChunk)
-                store8<TG>(a.grad, v * a.dim + col, (int)min((int64_t)8, a.dim - col), zero);
+                store8<TG>(a.grad, v * a.dim + col, (int)min((int64_t)8, a.dim - col), zero, a.stream);
         }
         return;
     }
@@ -539,6 +541,7 @@ int launch_embed_lookup(const EmbedLookupLaunch& l, void* stream) {
     EmbedLookup a = l.args;
     a.dim = l.dim;
     a.per_row = make_div((uint32_t)per_row);
+    a.stream = streams(l.n_tokens * l.dim * (l.out_dtype == ZERO_F32 ? 4 : 2));
     for (int64_t t = 0; t < l.n_tokens; t += most) {
         const int64_t n = l.n_tokens - t < most ? l.n_tokens - t : most;
         a.tokens = static_cast<const char*>(l.args.tokens) + t * (a.wide ? 8 : 4);
@@ -557,12 +560,16 @@ int launch_embed_lookup(const EmbedLookupLaunch& l, void* stream) {
 int launch_embed_grad(const EmbedGradLaunch& l, void* stream) {
     const hipStream_t s = static_cast<hipStream_t>(stream);
     EmbedSort a = l.sort;
+    const int64_t row_bytes = l.sum.dim * (l.grad_dtype == ZERO_F32 ? 4 : 2);
+    EmbedSum b = l.sum;
+    // of an accumulated gradient only the rows that tokens name are written
+    b.stream = streams((b.accumulate ? (a.n_tokens < a.vocab ? a.n_tokens : a.vocab) : a.vocab) * row_bytes);
     if (a.n_tokens <= kEmbedFew) {
         const int64_t rows = l.sum.accumulate ? 0 : a.vocab;
         const dim3 grid((uint32_t)((a.n_tokens + kFewWaves - 1) / kFewWaves + (rows + kFewRows - 1) / kFewRows));
-        if (l.dy_dtype == ZERO_F32) few_to<ZERO_F32>(a, l.sum, l.grad_dtype, grid, s);
-        else if (l.dy_dtype == ZERO_F16) few_to<ZERO_F16>(a, l.sum, l.grad_dtype, grid, s);
-        else few_to<ZERO_BF16>(a, l.sum, l.grad_dtype, grid, s);
+        if (l.dy_dtype == ZERO_F32) few_to<ZERO_F32>(a, b, l.grad_dtype, grid, s);
+        else if (l.dy_dtype == ZERO_F16) few_to<ZERO_F16>(a, b, l.grad_dtype, grid, s);
+        else few_to<ZERO_BF16>(a, b, l.grad_dtype, grid, s);
         return last_error();
     }
     char* ws = static_cast<char*>(l.workspace);
@@ -579,9 +586,9 @@ int launch_embed_grad(const EmbedGradLaunch& l, void* stream) {
     a.blocks = (int32_t)((a.n_tokens + kEmbedSortTile - 1) / kEmbedSortTile);
     a.scanned = a.blocks > kEmbedScanBlocks;
     // each launch of the sort writes so many bytes of zeros beside its work
-    const int64_t row_bytes = l.sum.dim * (l.grad_dtype == ZERO_F32 ? 4 : 2);
     const int64_t total = l.sum.accumulate ? 0 : a.vocab * row_bytes;
     a.grad = static_cast<char*>(l.sum.grad);
+    a.stream = b.stream;
     const auto grid = [&]() {
         a.zero_first = a.zero_last;
         a.zero_last = total - a.zero_first < kEmbedZeroBytes ? total : a.zero_first + kEmbedZeroBytes;
@@ -605,7 +612,6 @@ int launch_embed_grad(const EmbedGradLaunch& l, void* stream) {
         embed_scatter_kernel<<<blocks, kThreads, 0, s>>>(a);
         if (const int e = last_error()) return e;
     }
-    EmbedSum b = l.sum;
     b.keys = keys[at];
     b.places = places[at];
     b.flags = a.flags;

@@ -177,6 +177,15 @@ constexpr int64_t kEmbedZeroBytes = 40 << 20;   // of zeros that a launch of the
 constexpr int kEmbedScanBlocks = 128;    // blocks that sum the counts before theirs themselves
 constexpr int kEmbedBatch = 8;           // rows that a wave of the sums has in flight
 
+// Whether a call's output of so many bytes goes past the caches: from half the
+// memory-side cache on, where its reader would not find the beginning any more.
+// Written and then copied, cached and past the caches, us: embedding rows 64 MiB 44, 50,
+// 96 MiB 65, 72, 128 MiB 101, 99, 256 MiB 201, 195; an activation's gradient 47, 52; 74,
+// 81; 115, 110; 213, 215.  Written alone, 128 MiB of rows from an INT8 payload 55, 31: the
+// payload stays cached.
+constexpr int64_t kStreamBytes = (int64_t)128 << 20;
+inline int streams(int64_t bytes) { return bytes >= kStreamBytes; }
+
 // n / d by a product (see zf_vec.h)
 struct Div {
     uint32_t d, m, s;
@@ -191,6 +200,7 @@ struct EmbedLookup {
     int64_t out_ld, first, vocab, dim;
     Div per_row;            // groups of eight columns in a row
     uint32_t groups;
+    int32_t stream;         // 1: the output goes past the caches
     int32_t wide;           // 1: 64-bit tokens
     float scale;
 };
@@ -213,6 +223,7 @@ struct EmbedSort {
     int64_t flag_words;
     char* grad;             // zeros go to bytes [zero_first, zero_last) of it
     int64_t zero_first, zero_last;
+    int32_t stream;         // 1: they go past the caches
     int32_t wide, has_padding, passes, pass, digit_bits, blocks, scanned;
 };
 struct EmbedSum {
@@ -226,6 +237,7 @@ struct EmbedSum {
     int64_t zero_from;      // the first row that may need zeros yet
     int32_t tile;           // sorted positions of one tile
     int32_t accumulate;
+    int32_t stream;         // 1: the gradient goes past the caches
     float scale;
 };
 struct EmbedGradLaunch {
@@ -285,6 +297,7 @@ struct ActLaunch {
     int64_t rows, cols, x_ld, up_ld, y_ld, dup_ld;
     Div per_row;                 // groups of eight columns in a checkpoint's row
     uint32_t groups;
+    int32_t stream;              // 1: y and dup go past the caches
     int32_t dtype, kind;
     int32_t least;               // the least exponent that a checkpoint takes
 };

@@ -65,26 +65,40 @@ __device__ __forceinline__ void load8(const void* base, int64_t i, int n, float 
 #pragma unroll
     for (int k = 0; k < 8; ++k) x[k] = k < n ? to_f32<DT>(p[k]) : 0.0f;
 }
-template <int DT>
-__device__ __forceinline__ void store8(void* base, int64_t i, int n, const float (&x)[8]) {
+// STREAM: past the caches, for what is not read again while it would be there.
+template <int DT, bool STREAM>
+__device__ __forceinline__ void store8_as(void* base, int64_t i, int n, const float (&x)[8]) {
     using T = typename Elem<DT>::type;
     T* p = static_cast<T*>(base) + i;
     if (n >= 8) {
         if constexpr (DT == ZERO_F32) {
-            *reinterpret_cast<v4f_any*>(p) = v4f{x[0], x[1], x[2], x[3]};
-            *reinterpret_cast<v4f_any*>(p + 4) = v4f{x[4], x[5], x[6], x[7]};
+            v4f_any* q = reinterpret_cast<v4f_any*>(p);
+            const v4f_any a = {x[0], x[1], x[2], x[3]}, b = {x[4], x[5], x[6], x[7]};
+            if constexpr (STREAM) {
+                __builtin_nontemporal_store(a, q);
+                __builtin_nontemporal_store(b, q + 1);
+            } else {
+                q[0] = a;
+                q[1] = b;
+            }
         } else {
-            v4u a;
+            v4u_any a;
 #pragma unroll
             for (int k = 0; k < 4; ++k)
                 a[k] = (uint32_t)from_f32<DT>(x[2 * k]) | (uint32_t)from_f32<DT>(x[2 * k + 1]) << 16;
-            *reinterpret_cast<v4u_any*>(p) = a;
+            if constexpr (STREAM) __builtin_nontemporal_store(a, reinterpret_cast<v4u_any*>(p));
+            else *reinterpret_cast<v4u_any*>(p) = a;
         }
         return;
     }
 #pragma unroll
     for (int k = 0; k < 8; ++k)
         if (k < n) p[k] = from_f32<DT>(x[k]);
+}
+template <int DT>
+__device__ __forceinline__ void store8(void* base, int64_t i, int n, const float (&x)[8], int stream) {
+    if (stream) store8_as<DT, true>(base, i, n, x);
+    else store8_as<DT, false>(base, i, n, x);
 }
 
 __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
