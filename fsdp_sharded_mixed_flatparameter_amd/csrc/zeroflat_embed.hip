@@ -138,8 +138,11 @@ __device__ __forceinline__ void zero_bytes(char* grad, int64_t first, int64_t la
     const int64_t from = first + block * kZeroBlock, to = min(last, from + kZeroBlock);
     for (int64_t at = from + threadIdx.x * 16; at < to; at += kThreads * 16) {
         v4u_any* p = reinterpret_cast<v4u_any*>(grad + at);
-        if (at + 16 <= to && stream) __builtin_nontemporal_store(v4u_any{0, 0, 0, 0}, p);
-        else if (at + 16 <= to) *p = v4u_any{0, 0, 0, 0};
+        if (at + 16 <= to && stream) {
+            ZF_APART;
+            __builtin_nontemporal_store(v4u_any{0, 0, 0, 0}, p);
+            ZF_APART;
+        } else if (at + 16 <= to) *p = v4u_any{0, 0, 0, 0};
         else
             for (int64_t b = at; b < to; b += 2) *reinterpret_cast<uint16_t*>(grad + b) = 0;
     }
@@ -268,25 +271,62 @@ __global__ __launch_bounds__(kThreads) void embed_scatter_kernel(EmbedSort a) {
 }
 
 // ---------------------------------------------------------------- sums
+// Columns col .. col + 7 of a row's sum into the gradient; of a row's last columns a
+// lane has eight that end with the row, and writes those from `skip` on.
 template <int TG>
-__device__ __forceinline__ void write_row(const EmbedSum& a, uint32_t row, int64_t col, int n,
+__device__ __forceinline__ void write_row(const EmbedSum& a, uint32_t row, int64_t col, int skip, int n,
                                           float (&acc)[8]) {
     const int64_t at = (int64_t)row * a.dim + col;
     float y[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) y[k] = acc[k] * a.scale;
-    if (a.accumulate) {
-        float old[8];
-        load8<TG>(a.grad, at, n, old);
+    if (skip == 0 && n >= 8) {
+        if (a.accumulate) {
+            const Raw8<TG> old = fetch8<TG>(a.grad, at);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) y[k] += old[k];
+            for (int k = 0; k < 8; ++k) y[k] += element<TG>(old, k);
+        }
+        store8<TG>(a.grad, at, 8, y, a.stream);
+        return;
     }
-    store8<TG>(a.grad, at, n, y, a.stream);
+    auto* p = static_cast<typename Elem<TG>::type*>(a.grad) + at;
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        if (k >= skip && k < n) p[k] = from_f32<TG>(a.accumulate ? y[k] + to_f32<TG>(p[k]) : y[k]);
+}
+
+// The eight columns that a lane loads for its group at `col`: those, or the row's
+// last eight, of which it owns the ones from `skip` on; of a row of less than eight
+// the first n.
+struct Window {
+    int64_t col;
+    int skip, n;
+};
+__device__ __forceinline__ Window window_at(int64_t col, int64_t dim) {
+    const int64_t w = max((int64_t)0, min(col, dim - 8));
+    return Window{w, (int)min((int64_t)8, col - w), (int)min((int64_t)8, dim - w)};
+}
+template <int TD, bool NARROW>
+__device__ __forceinline__ Raw8<TD> fetch_row(const EmbedSum& a, int64_t place, const Window& w) {
+    if constexpr (!NARROW) {
+        return fetch8<TD>(a.dy, place * a.dy_ld + w.col);
+    } else {
+        const auto* p = static_cast<const typename Elem<TD>::type*>(a.dy) + place * a.dy_ld;
+        Raw8<TD> r;
+        r.lo = r.hi = v4u{0, 0, 0, 0};
+#pragma unroll
+        for (int k = 0; k < 7; ++k) {
+            const auto x = p[min(k, w.n - 1)];             // columns behind the last repeat it
+            if constexpr (TD == ZERO_F32) (k < 4 ? r.lo : r.hi)[k % 4] = __float_as_uint(x);
+            else r.lo[k / 2] |= (uint32_t)x << (16 * (k & 1));
+        }
+        return r;
+    }
 }
 
 // A wave takes a tile of a.tile sorted positions and 512 columns; the waves
 // behind them write zeros to the rows that no token names.
-template <int TD, int TG>
+template <int TD, int TG, bool NARROW>
 __global__ __launch_bounds__(kThreads) void embed_sum_kernel(EmbedSum a) {
     const int lane = threadIdx.x & 63;
     const int64_t unit = (int64_t)blockIdx.x * kWaves + uniform(threadIdx.x >> 6);
@@ -298,56 +338,61 @@ __global__ __launch_bounds__(kThreads) void embed_sum_kernel(EmbedSum a) {
             store8<TG>(a.grad, v * a.dim + col, (int)min((int64_t)8, a.dim - col), zero, a.stream);
         return;
     }
-    const int64_t tile = unit / a.chunks;
-    const int64_t col = (unit - tile * a.chunks) * kChunk + lane * 8;
-    const int n = (int)min((int64_t)8, a.dim - col);       // <= 0: the lane has no columns
+    const int64_t tile = unit / a.chunks, col = (unit - tile * a.chunks) * kChunk + lane * 8;
+    const Window w = window_at(col, a.dim);
     const int64_t base = tile * a.tile;
     const int len = (int)min((int64_t)a.tile, a.n_tokens - base);
-    const auto* keys = as_const(a.keys) + base;
-    const auto* places = as_const(a.places) + base;
+    // lane j holds the tile's j-th key and place, lane 62 the key before, lane 63 the one behind
+    static_assert(kEmbedTile <= 62, "two lanes are left");
     const uint32_t none = (uint32_t)a.vocab;
-    uint32_t cur = keys[0];
+    const int64_t at = lane == 62 ? base - 1 : lane == 63 ? base + len : base + min(lane, len - 1);
+    const uint32_t key_here = at >= 0 && at < a.n_tokens ? a.keys[at] : none;
+    const int32_t place_here = a.places[base + min(lane, len - 1)];
+    const auto key = [&](int j) { return (uint32_t)__builtin_amdgcn_readlane((int)key_here, j); };
+    uint32_t cur = key(0);
     if (cur == none) return;
-    bool before = tile > 0 && keys[-1] == cur;             // the run began in an earlier tile
-    const uint32_t after = base + len < a.n_tokens ? keys[len] : none;
+    bool before = key(62) == cur;                          // the run began in an earlier tile
+    const uint32_t after = key(63);
     float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
     auto partial = [&](int which) {
-        if (n > 0) {
+        if (w.skip < 8) {
             float* p = a.partials + (tile * 2 + which) * a.pitch + col;
-            *reinterpret_cast<v4f*>(p) = v4f{acc[0], acc[1], acc[2], acc[3]};
-            *reinterpret_cast<v4f*>(p + 4) = v4f{acc[4], acc[5], acc[6], acc[7]};
+            if (w.skip == 0) {
+                *reinterpret_cast<v4f*>(p) = v4f{acc[0], acc[1], acc[2], acc[3]};
+                *reinterpret_cast<v4f*>(p + 4) = v4f{acc[4], acc[5], acc[6], acc[7]};
+            } else {
+#pragma unroll
+                for (int k = 1; k < 8; ++k)
+                    if (k >= w.skip) p[k - w.skip] = acc[k];
+            }
         }
     };
     for (int j0 = 0; j0 < len; j0 += kEmbedBatch) {
-        float x[kEmbedBatch][8];
+        // places behind the tile's end repeat its last one: their rows are not used
+        Raw8<TD> raw[kEmbedBatch];
+#pragma unroll
+        for (int j = 0; j < kEmbedBatch; ++j)
+            raw[j] = fetch_row<TD, NARROW>(a, __builtin_amdgcn_readlane(place_here, j0 + j), w);
 #pragma unroll
         for (int j = 0; j < kEmbedBatch; ++j) {
-            const bool live = j0 + j < len && keys[j0 + j] != none;
-            if (live && n > 0) load8<TD>(a.dy, (int64_t)places[j0 + j] * a.dy_ld + col, n, x[j]);
-        }
+            if (j0 + j >= len) break;
+            const uint32_t k = key(j0 + j);
+            if (k != cur) {
+                if (before) partial(0);
+                else write_row<TG>(a, cur, w.col, w.skip, w.n, acc);
+                before = false;
+                cur = k;
 #pragma unroll
-        for (int j = 0; j < kEmbedBatch; ++j) {
-            if (j0 + j < len && cur != none) {
-                const uint32_t k = keys[j0 + j];
-                if (k != cur) {
-                    if (before) partial(0);
-                    else if (n > 0) write_row<TG>(a, cur, col, n, acc);
-                    before = false;
-                    cur = k;
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) acc[c] = 0.0f;
-                }
-                if (cur != none) {
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) acc[c] += x[j][c];
-                }
+                for (int c = 0; c < 8; ++c) acc[c] = 0.0f;
             }
+            if (cur == none) return;                       // the others are behind the last token
+#pragma unroll
+            for (int c = 0; c < 8; ++c) acc[c] += element<TD>(raw[j], c);
         }
     }
-    if (cur == none) return;
     if (before) partial(0);
     else if (after == cur) partial(1);
-    else if (n > 0) write_row<TG>(a, cur, col, n, acc);
+    else write_row<TG>(a, cur, w.col, w.skip, w.n, acc);
 }
 
 // The block of tile t and 512 columns, if a run begins in t and ends in a later
@@ -394,7 +439,7 @@ __global__ __launch_bounds__(kThreads) void embed_join_kernel(EmbedSum a) {
     for (int w = 1; w < kWaves; ++w)
 #pragma unroll
         for (int c = 0; c < 8; ++c) acc[c] += part[w][lane * 8 + c];
-    write_row<TG>(a, k, col, n, acc);
+    write_row<TG>(a, k, col, 0, n, acc);
 }
 
 // The gradient of up to kEmbedFew tokens, without a sort.  The block holds every
@@ -478,7 +523,7 @@ __global__ __launch_bounds__(kFewThreads) void embed_few_kernel(EmbedSort t, Emb
             const int cols = (int)min((int64_t)8, a.dim - col);
             float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
             sum(count, col, cols, acc);
-            if (cols > 0) write_row<TG>(a, key, col, cols, acc);
+            if (cols > 0) write_row<TG>(a, key, col, 0, cols, acc);
         }
     }
     if (lane == 0) longs[wave] = count > kEmbedLong ? key : none;
@@ -501,7 +546,7 @@ __global__ __launch_bounds__(kFewThreads) void embed_few_kernel(EmbedSort t, Emb
                 for (int u = 1; u < kFewWaves; ++u)
 #pragma unroll
                     for (int c = 0; c < 8; ++c) acc[c] += part[u][lane * 8 + c];
-                write_row<TG>(a, k, col, cols, acc);
+                write_row<TG>(a, k, col, 0, cols, acc);
             }
             __syncthreads();
         }
@@ -517,11 +562,16 @@ void lookup_to(const EmbedLookup& a, int out, dim3 grid, hipStream_t s) {
     else embed_lookup_kernel<TT, ZERO_BF16><<<grid, kThreads, 0, s>>>(a);
 }
 
+template <int TD, int TG>
+void sum_of(const EmbedSum& a, dim3 grid, hipStream_t s) {
+    if (a.dim >= 8) embed_sum_kernel<TD, TG, false><<<grid, kThreads, 0, s>>>(a);
+    else embed_sum_kernel<TD, TG, true><<<grid, kThreads, 0, s>>>(a);
+}
 template <int TD>
 void sum_to(const EmbedSum& a, int grad, dim3 grid, hipStream_t s) {
-    if (grad == ZERO_F32) embed_sum_kernel<TD, ZERO_F32><<<grid, kThreads, 0, s>>>(a);
-    else if (grad == ZERO_F16) embed_sum_kernel<TD, ZERO_F16><<<grid, kThreads, 0, s>>>(a);
-    else embed_sum_kernel<TD, ZERO_BF16><<<grid, kThreads, 0, s>>>(a);
+    if (grad == ZERO_F32) sum_of<TD, ZERO_F32>(a, grid, s);
+    else if (grad == ZERO_F16) sum_of<TD, ZERO_F16>(a, grid, s);
+    else sum_of<TD, ZERO_BF16>(a, grid, s);
 }
 
 template <int TD>

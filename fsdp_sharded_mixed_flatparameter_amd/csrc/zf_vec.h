@@ -95,10 +95,48 @@ __device__ __forceinline__ void store8_as(void* base, int64_t i, int n, const fl
     for (int k = 0; k < 8; ++k)
         if (k < n) p[k] = from_f32<DT>(x[k]);
 }
+// Eight consecutive elements as they lie in memory, to be converted later: loads
+// that nothing waits for between them.
+template <int DT>
+struct Raw8 {
+    v4u lo, hi;                            // hi: fp32 only
+};
+template <int DT>
+__device__ __forceinline__ Raw8<DT> fetch8(const void* base, int64_t i) {
+    const auto* p = static_cast<const typename Elem<DT>::type*>(base) + i;
+    Raw8<DT> r;
+    if constexpr (DT == ZERO_F32) {
+        r.lo = __builtin_bit_cast(v4u, *reinterpret_cast<const v4f_any*>(p));
+        r.hi = __builtin_bit_cast(v4u, *reinterpret_cast<const v4f_any*>(p + 4));
+    } else {
+        r.lo = *reinterpret_cast<const v4u_any*>(p);
+    }
+    return r;
+}
+template <int DT>
+__device__ __forceinline__ float element(const Raw8<DT>& r, int k) {
+    if constexpr (DT == ZERO_F32) {
+        const uint32_t w = k < 4 ? r.lo[k] : r.hi[k - 4];
+        return __uint_as_float(w);
+    } else {
+        const uint32_t w = r.lo[k / 2];
+        if constexpr (DT == ZERO_BF16) return __uint_as_float(k & 1 ? w & 0xffff0000u : w << 16);
+        else return to_f32<DT>((uint16_t)(k & 1 ? w >> 16 : w));
+    }
+}
+
+// The compiler would make one plain store of the two branches: empty statements
+// that it cannot move keep them apart.
+#define ZF_APART asm volatile("" ::: "memory")
 template <int DT>
 __device__ __forceinline__ void store8(void* base, int64_t i, int n, const float (&x)[8], int stream) {
-    if (stream) store8_as<DT, true>(base, i, n, x);
-    else store8_as<DT, false>(base, i, n, x);
+    if (stream) {
+        ZF_APART;
+        store8_as<DT, true>(base, i, n, x);
+        ZF_APART;
+    } else {
+        store8_as<DT, false>(base, i, n, x);
+    }
 }
 
 __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
