@@ -136,8 +136,13 @@ __device__ __forceinline__ void keep(const float (&x)[8], int least, int8_t* cod
     v2u c;
     uint32_t e;
     quantise(x, least, c, e);
-    if (stream) __builtin_nontemporal_store(c, reinterpret_cast<v2u*>(codes) + g);
-    else reinterpret_cast<v2u*>(codes)[g] = c;
+    if (stream) {
+        ZF_APART;
+        __builtin_nontemporal_store(c, reinterpret_cast<v2u*>(codes) + g);
+        ZF_APART;
+    } else {
+        reinterpret_cast<v2u*>(codes)[g] = c;
+    }
     if ((g & 3) == 0) exponents[g >> 2] = (uint8_t)e;
 }
 

@@ -309,7 +309,7 @@ __device__ __forceinline__ Window window_at(int64_t col, int64_t dim) {
 template <int TD, bool NARROW>
 __device__ __forceinline__ Raw8<TD> fetch_row(const EmbedSum& a, int64_t place, const Window& w) {
     if constexpr (!NARROW) {
-        return fetch8<TD>(a.dy, place * a.dy_ld + w.col);
+        return fetch8<TD, true>(a.dy, place * a.dy_ld + w.col);
     } else {
         const auto* p = static_cast<const typename Elem<TD>::type*>(a.dy) + place * a.dy_ld;
         Raw8<TD> r;

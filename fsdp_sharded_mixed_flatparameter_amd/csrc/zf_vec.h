@@ -101,15 +101,17 @@ template <int DT>
 struct Raw8 {
     v4u lo, hi;                            // hi: fp32 only
 };
-template <int DT>
+template <int DT, bool STREAM = false>
 __device__ __forceinline__ Raw8<DT> fetch8(const void* base, int64_t i) {
     const auto* p = static_cast<const typename Elem<DT>::type*>(base) + i;
     Raw8<DT> r;
     if constexpr (DT == ZERO_F32) {
-        r.lo = __builtin_bit_cast(v4u, *reinterpret_cast<const v4f_any*>(p));
-        r.hi = __builtin_bit_cast(v4u, *reinterpret_cast<const v4f_any*>(p + 4));
+        const v4f_any* q = reinterpret_cast<const v4f_any*>(p);
+        r.lo = __builtin_bit_cast(v4u, STREAM ? __builtin_nontemporal_load(q) : q[0]);
+        r.hi = __builtin_bit_cast(v4u, STREAM ? __builtin_nontemporal_load(q + 1) : q[1]);
     } else {
-        r.lo = *reinterpret_cast<const v4u_any*>(p);
+        const v4u_any* q = reinterpret_cast<const v4u_any*>(p);
+        r.lo = STREAM ? __builtin_nontemporal_load(q) : q[0];
     }
     return r;
 }
