@@ -11,7 +11,7 @@
 // by atomics its roundings would depend on the order of arrival, and a frequent
 // token's row would be one address for the whole chip.  Sorted, the positions
 // are cut into tiles of one length whatever the tokens are, so that every wave
-// has the same work; a run inside a tile is summed in registers and written
+// has the same work; a run inside a tile is summed in registers and LDS and written
 // once, and one that crosses tiles leaves an fp32 partial row per tile, which
 // the join adds in order.  Few tokens need no sort: the wave of a token's first
 // position finds the others by comparing.  Every sum's order is fixed by the
@@ -324,51 +324,64 @@ __device__ __forceinline__ Raw8<TD> fetch_row(const EmbedSum& a, int64_t place, 
     }
 }
 
-// A wave takes a tile of a.tile sorted positions and 512 columns; the waves
-// behind them write zeros to the rows that no token names.
+// A block takes 512 columns of a tile of sorted positions, a wave a quarter of it.  A
+// run that crosses quarters is added up in LDS; one that crosses tiles leaves the
+// tile's share in its first partial row (it began before) or its second (it begins
+// here and goes on).  Blocks behind them write zeros to the rows that no token
+// names, a row per wave.
 template <int TD, int TG, bool NARROW>
 __global__ __launch_bounds__(kThreads) void embed_sum_kernel(EmbedSum a) {
-    const int lane = threadIdx.x & 63;
-    const int64_t unit = (int64_t)blockIdx.x * kWaves + uniform(threadIdx.x >> 6);
-    if (unit >= a.sum_units) {
-        const int64_t v = a.zero_from + unit - a.sum_units;
+    __shared__ float heads[kWaves][kChunk], tails[kWaves][kChunk];
+    __shared__ int32_t state[kWaves];                      // of a quarter, as bits:
+    constexpr int kHead = 1, kThrough = 2, kTail = 4;      // a run from before; the only one, and it goes on; one that begins and goes on
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+    if (blockIdx.x >= (uint32_t)a.sum_blocks) {
+        const int64_t v = a.zero_from + (int64_t)(blockIdx.x - a.sum_blocks) * kWaves + wave;
         if (v >= a.vocab || as_const(reinterpret_cast<const uint8_t*>(a.flags))[v]) return;
         const float zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
         for (int64_t col = lane * 8; col < a.dim; col += kChunk)
             store8<TG>(a.grad, v * a.dim + col, (int)min((int64_t)8, a.dim - col), zero, a.stream);
         return;
     }
-    const int64_t tile = unit / a.chunks, col = (unit - tile * a.chunks) * kChunk + lane * 8;
+    const int64_t tile = blockIdx.x / (uint32_t)a.chunks;
+    const int64_t col = (blockIdx.x - tile * a.chunks) * kChunk + lane * 8;
     const Window w = window_at(col, a.dim);
-    const int64_t base = tile * a.tile;
-    const int len = (int)min((int64_t)a.tile, a.n_tokens - base);
-    // lane j holds the tile's j-th key and place, lane 62 the key before, lane 63 the one behind
-    static_assert(kEmbedTile <= 62, "two lanes are left");
+    const int quarter = a.tile / kWaves;
+    const int64_t base = tile * a.tile + wave * quarter;
+    const int len = (int)max((int64_t)0, min((int64_t)quarter, a.n_tokens - base));
+    // lane j holds the quarter's j-th key and place, lane 62 the key before, lane 63 the one behind
+    static_assert(kEmbedTile / kWaves <= 62, "two lanes are left");
     const uint32_t none = (uint32_t)a.vocab;
     const int64_t at = lane == 62 ? base - 1 : lane == 63 ? base + len : base + min(lane, len - 1);
     const uint32_t key_here = at >= 0 && at < a.n_tokens ? a.keys[at] : none;
-    const int32_t place_here = a.places[base + min(lane, len - 1)];
+    const int32_t place_here = len > 0 ? a.places[base + min(lane, len - 1)] : 0;
     const auto key = [&](int j) { return (uint32_t)__builtin_amdgcn_readlane((int)key_here, j); };
-    uint32_t cur = key(0);
-    if (cur == none) return;
-    bool before = key(62) == cur;                          // the run began in an earlier tile
-    const uint32_t after = key(63);
+    uint32_t cur = len > 0 ? key(0) : none;
+    bool before = cur != none && key(62) == cur;           // the run began in an earlier quarter
     float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    auto partial = [&](int which) {
-        if (w.skip < 8) {
-            float* p = a.partials + (tile * 2 + which) * a.pitch + col;
-            if (w.skip == 0) {
-                *reinterpret_cast<v4f*>(p) = v4f{acc[0], acc[1], acc[2], acc[3]};
-                *reinterpret_cast<v4f*>(p + 4) = v4f{acc[4], acc[5], acc[6], acc[7]};
-            } else {
+    const auto keep = [&](float* to) {
+        *reinterpret_cast<v4f*>(to + lane * 8) = v4f{acc[0], acc[1], acc[2], acc[3]};
+        *reinterpret_cast<v4f*>(to + lane * 8 + 4) = v4f{acc[4], acc[5], acc[6], acc[7]};
+    };
+    const auto add = [&](const float* from) {
+        const v4f x = *reinterpret_cast<const v4f*>(from + lane * 8), y = *reinterpret_cast<const v4f*>(from + lane * 8 + 4);
 #pragma unroll
-                for (int k = 1; k < 8; ++k)
-                    if (k >= w.skip) p[k - w.skip] = acc[k];
-            }
+        for (int c = 0; c < 4; ++c) { acc[c] += x[c]; acc[4 + c] += y[c]; }
+    };
+    const auto partial = [&](int which) {
+        float* p = a.partials + (tile * 2 + which) * a.pitch + col;
+        if (w.skip == 0) {
+            *reinterpret_cast<v4f*>(p) = v4f{acc[0], acc[1], acc[2], acc[3]};
+            *reinterpret_cast<v4f*>(p + 4) = v4f{acc[4], acc[5], acc[6], acc[7]};
+        } else {
+#pragma unroll
+            for (int k = 1; k < 8; ++k)
+                if (k >= w.skip) p[k - w.skip] = acc[k];
         }
     };
-    for (int j0 = 0; j0 < len; j0 += kEmbedBatch) {
-        // places behind the tile's end repeat its last one: their rows are not used
+    int mine = 0;
+    for (int j0 = 0; j0 < len && cur != none; j0 += kEmbedBatch) {
+        // places behind the end repeat the last one: their rows are not used
         Raw8<TD> raw[kEmbedBatch];
 #pragma unroll
         for (int j = 0; j < kEmbedBatch; ++j)
@@ -378,21 +391,53 @@ __global__ __launch_bounds__(kThreads) void embed_sum_kernel(EmbedSum a) {
             if (j0 + j >= len) break;
             const uint32_t k = key(j0 + j);
             if (k != cur) {
-                if (before) partial(0);
-                else write_row<TG>(a, cur, w.col, w.skip, w.n, acc);
+                if (before) {
+                    keep(heads[wave]);
+                    mine = kHead;
+                } else {
+                    write_row<TG>(a, cur, w.col, w.skip, w.n, acc);
+                }
                 before = false;
                 cur = k;
 #pragma unroll
                 for (int c = 0; c < 8; ++c) acc[c] = 0.0f;
+                if (cur == none) break;                    // the others are behind the last token
             }
-            if (cur == none) return;                       // the others are behind the last token
 #pragma unroll
             for (int c = 0; c < 8; ++c) acc[c] += element<TD>(raw[j], c);
         }
     }
-    if (before) partial(0);
-    else if (after == cur) partial(1);
-    else write_row<TG>(a, cur, w.col, w.skip, w.n, acc);
+    if (cur != none) {
+        const bool open = key(63) == cur;
+        if (before) {
+            keep(heads[wave]);
+            mine = open ? kHead | kThrough : kHead;
+        } else if (open) {
+            keep(tails[wave]);
+            mine |= kTail;
+        } else {
+            write_row<TG>(a, cur, w.col, w.skip, w.n, acc);
+        }
+    }
+    if (lane == 0) state[wave] = mine;
+    __syncthreads();
+    if (mine & kTail) {
+        // the quarters behind, as far as the run goes (acc is the tail still)
+        int u = wave + 1;
+        for (; u < kWaves; ++u) {
+            add(heads[u]);
+            if (!(uniform(state[u]) & kThrough)) break;
+        }
+        if (u < kWaves) write_row<TG>(a, cur, w.col, w.skip, w.n, acc);
+        else partial(1);
+    }
+    if (wave == 0 && (mine & kHead)) {
+#pragma unroll
+        for (int c = 0; c < 8; ++c) acc[c] = 0.0f;
+        add(heads[0]);
+        for (int u = 0; u < kWaves - 1 && (uniform(state[u]) & kThrough); ++u) add(heads[u + 1]);
+        partial(0);
+    }
 }
 
 // The block of tile t and 512 columns, if a run begins in t and ends in a later
@@ -672,10 +717,10 @@ int launch_embed_grad(const EmbedGradLaunch& l, void* stream) {
     b.tiles = w.tiles;
     b.pitch = w.pitch;
     b.chunks = (b.dim + kChunk - 1) / kChunk;
-    b.sum_units = b.tiles * b.chunks;
+    b.sum_blocks = b.tiles * b.chunks;
     // rows that are zero already need no more of it; one that is so in part does
     b.zero_from = b.accumulate ? b.vocab : a.zero_last / row_bytes;
-    const dim3 sums((uint32_t)((b.sum_units + b.vocab - b.zero_from + kWaves - 1) / kWaves));
+    const dim3 sums((uint32_t)(b.sum_blocks + (b.vocab - b.zero_from + kWaves - 1) / kWaves));
     if (l.dy_dtype == ZERO_F32) sum_to<ZERO_F32>(b, l.grad_dtype, sums, s);
     else if (l.dy_dtype == ZERO_F16) sum_to<ZERO_F16>(b, l.grad_dtype, sums, s);
     else sum_to<ZERO_BF16>(b, l.grad_dtype, sums, s);

@@ -175,7 +175,7 @@ constexpr int kEmbedFew = 4096;          // tokens whose gradient needs no sort
 constexpr int kEmbedSortTile = 1024;     // tokens of one block of the sort
 constexpr int64_t kEmbedZeroBytes = 40 << 20;   // of zeros that a launch of the sort writes beside it
 constexpr int kEmbedScanBlocks = 128;    // blocks that sum the counts before theirs themselves
-constexpr int kEmbedTile = 32;           // sorted positions of a wave of the sums, at most
+constexpr int kEmbedTile = 128;          // sorted positions of a block of the sums, at most
 constexpr int kEmbedBatch = 8;           // rows that a wave of the sums has in flight
 
 // Whether a call's output of so many bytes goes past the caches: from half the
@@ -234,7 +234,7 @@ struct EmbedSum {
     const void* dy;
     void* grad;
     float* partials;        // two fp32 rows of `pitch` per tile: a run from before, a run that goes on
-    int64_t n_tokens, vocab, dim, dy_ld, pitch, tiles, chunks, sum_units;
+    int64_t n_tokens, vocab, dim, dy_ld, pitch, tiles, chunks, sum_blocks;
     int64_t zero_from;      // the first row that may need zeros yet
     int32_t tile;           // sorted positions of one tile
     int32_t accumulate;
@@ -261,7 +261,7 @@ inline EmbedWorkspace embed_workspace(int64_t n, int64_t vocab, int64_t dim) {
     EmbedWorkspace w{};
     if (n <= kEmbedFew) return w;
     const auto up = [](int64_t x) { return (x + 255) / 256 * 256; };
-    w.tile = n * ((dim + 511) / 512) >= 65536 ? kEmbedTile : 8;
+    w.tile = n * ((dim + 511) / 512) >= 65536 ? kEmbedTile : 32;
     w.tiles = (n + w.tile - 1) / w.tile;
     w.pitch = (dim + 7) / 8 * 8;
     int64_t at = 0;
