@@ -28,6 +28,7 @@ _FLOATS = {getattr(torch, n): c for n, c in _DTYPE_CODES.items()}
 _HALVES = {t: c for t, c in _FLOATS.items() if t != torch.float32}
 _FP32, _INT8, _UINT8 = {torch.float32: 0}, {torch.int8: 1}, {torch.uint8: 1}
 _TOKENS = {torch.int64: 8, torch.int32: 4}
+_SIZE = (4, 2, 2)                # of the types' codes
 _device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
 
 
@@ -67,18 +68,16 @@ def _rows(t, name, rows, cols, codes, here, written=False):
     if code is None or t.get_device() != here:
         _refuse(t, name, codes)
     shape = t.shape
-    if not shape or shape[-1] != cols or t.numel() != rows * cols:
+    if shape != (rows, cols) and (not shape or shape[-1] != cols or t.numel() != rows * cols):
         raise ValueError("%s must hold %d rows of %d, not %s" % (name, rows, cols, tuple(shape)))
-    p = t.data_ptr()
+    p, size = t.data_ptr(), _SIZE[code]
     if t.is_contiguous():
-        return p, p + t.nbytes, code, cols
+        return p, p + rows * cols * size, code, cols
     ld, step = t.stride() if len(shape) == 2 else (0, 0)
-    if rows == 1 and step == 1:
-        return p, p + t.nbytes, code, cols
     if len(shape) != 2 or (cols > 1 and step != 1) or (written and rows > 1 and ld < cols):
         raise ValueError("%s must be contiguous, or a matrix whose rows are" % name)
     ld = ld if rows > 1 else cols
-    return p, p + ((rows - 1) * ld + cols) * t.element_size(), code, ld
+    return p, p + ((rows - 1) * ld + cols) * size, code, ld
 
 
 def _apart(a, b, name_a, name_b):
@@ -200,32 +199,42 @@ class Saved8:
     """The checkpoint of a (rows, cols) matrix in 8 bits: `codes` (rows, pitch) int8,
     pitch the columns rounded up to blocks of 32, and `exponents` (rows, pitch / 32)
     uint8.  A value stands for code * 2^(exponent - 133), NaN in a block whose
-    exponent is 255.  The memory is uninitialised until a call fills it."""
+    exponent is 255.  The memory is uninitialised until a call fills it; both tensors
+    stay where they are, and are loaded by copying into them."""
+
+    __slots__ = ("_rows", "_cols", "_codes", "_exponents", "_at")
 
     def __init__(self, rows, cols, device="cuda"):
         rows, cols = int(rows), int(cols)
         if rows < 0 or cols < 0:
             raise ValueError("negative size")
-        self.rows, self.cols = rows, cols
-        self.codes = torch.empty(rows, -(-cols // ZERO_BLOCK8) * ZERO_BLOCK8, dtype=torch.int8, device=device)
-        self.exponents = torch.empty(rows, -(-cols // ZERO_BLOCK8), dtype=torch.uint8, device=device)
+        blocks = -(-cols // ZERO_BLOCK8)
+        self._rows, self._cols = rows, cols
+        self._codes = torch.empty(rows, blocks * ZERO_BLOCK8, dtype=torch.int8, device=device)
+        self._exponents = torch.empty(rows, blocks, dtype=torch.uint8, device=device)
+        # device, codes and exponents as _flat gives them
+        c, e = self._codes.data_ptr(), self._exponents.data_ptr()
+        self._at = (self._codes.get_device(), (c, c + self._codes.numel(), 1), (e, e + self._exponents.numel(), 1))
+
+    rows = property(lambda self: self._rows)
+    cols = property(lambda self: self._cols)
+    codes = property(lambda self: self._codes)
+    exponents = property(lambda self: self._exponents)
 
 
-_NONE = (None, None)
+_NONE = (None, None, None)
 
 
-def _saved(s, name, here, rows=None, cols=None):
-    """(codes, exponents) of a checkpoint argument, as _flat gives them."""
+def _saved(s, name, here=None, rows=None, cols=None):
+    """(device, codes, exponents) of a checkpoint argument."""
     if s is None:
         return _NONE
-    if rows is not None and (s.rows != rows or s.cols != cols):
-        raise ValueError("%s is of a (%d, %d) matrix, not (%d, %d)" % (name, s.rows, s.cols, rows, cols))
-    c, e = _flat(s.codes, name + ".codes", _INT8, here), _flat(s.exponents, name + ".exponents", _UINT8, here)
-    blocks = -(-s.cols // ZERO_BLOCK8)
-    if s.codes.shape != (s.rows, blocks * ZERO_BLOCK8) or s.exponents.shape != (s.rows, blocks):
-        raise ValueError("%s.codes must be (%d, %d), its exponents (%d, %d)"
-                         % (name, s.rows, blocks * ZERO_BLOCK8, s.rows, blocks))
-    return c, e
+    if rows is not None and (s._rows != rows or s._cols != cols):
+        raise ValueError("%s is of a (%d, %d) matrix, not (%d, %d)" % (name, s._rows, s._cols, rows, cols))
+    at = s._at
+    if at[0] != here and (here is not None or at[0] < 0 or at[0] != _device()):
+        _refuse(s._codes, name, _INT8)
+    return at
 
 
 def _at(x):
@@ -236,52 +245,38 @@ def _apart_all(written, read, same=()):
     """Refuses overlaps of what is written with one another and with what is read,
     but for the pairs in `same`, which may be one and the same matrix.  Arguments
     are (name, what _flat or _rows gave, or None)."""
-    written = [x for x in written if x[1] is not None]
-    read = [x for x in read if x[1] is not None]
-    # nothing meets where every written range ends before the next range begins
-    ranges = sorted([x[1][:2] + (True,) for x in written if x[1][0] < x[1][1]]
-                    + [x[1][:2] + (False,) for x in read if x[1][0] < x[1][1]])
-    end, end_read, clash = 0, 0, False
-    for first, last, w in ranges:
-        if first < end or (w and first < end_read):
-            clash = True
-            break
-        if w:
-            end = max(end, last)
-        else:
-            end_read = max(end_read, last)
-    if not clash:
-        return
     for k, (name_a, a) in enumerate(written):
-        for name_b, b in written[k + 1:] + read:
-            if not ((name_a, name_b) in same and a == b):
-                _apart(a, b, name_a, name_b)
+        if a is None:
+            continue
+        first, last = a[0], a[1]
+        for other in (written[k + 1:], read):
+            for name_b, b in other:
+                if b is not None and first < b[1] and b[0] < last and not ((name_a, name_b) in same and a == b):
+                    _apart(a, b, name_a, name_b)
 
 
 def _parts(name, s):
-    return [(name + ".codes", s[0]), (name + ".exponents", s[1])]
+    return [] if s is _NONE else [(name + ".codes", s[1]), (name + ".exponents", s[2])]
 
 
 def zero_act_save8(x, saved, stream=None):
-    """The checkpoint of x, a (saved.rows, saved.cols) matrix."""
-    here = _here(saved.codes, "saved.codes", _INT8)
-    c, e = _saved(saved, "saved", here)
-    m = _rows(x, "x", saved.rows, saved.cols, _FLOATS, here)
+    """The checkpoint of x, a (saved._rows, saved._cols) matrix."""
+    here, c, e = _saved(saved, "saved")
+    m = _rows(x, "x", saved._rows, saved._cols, _FLOATS, here)
     _apart(c, m, "saved.codes", "x")
     _apart(e, m, "saved.exponents", "x")
-    rc = _lib.zero_act_save8(m[0], m[2], saved.rows, saved.cols, m[3], c[0], e[0], _on(stream))
+    rc = _lib.zero_act_save8(m[0], m[2], saved._rows, saved._cols, m[3], c[0], e[0], _on(stream))
     if rc:
         _check(rc)
 
 
 def zero_act_restore8(saved, out, stream=None):
     """out = the values that the checkpoint stands for, in out's type."""
-    here = _here(saved.codes, "saved.codes", _INT8)
-    c, e = _saved(saved, "saved", here)
-    m = _rows(out, "out", saved.rows, saved.cols, _FLOATS, here, True)
+    here, c, e = _saved(saved, "saved")
+    m = _rows(out, "out", saved._rows, saved._cols, _FLOATS, here, True)
     _apart(m, c, "out", "saved.codes")
     _apart(m, e, "out", "saved.exponents")
-    rc = _lib.zero_act_restore8(c[0], e[0], saved.rows, saved.cols, m[0], m[2], m[3], _on(stream))
+    rc = _lib.zero_act_restore8(c[0], e[0], saved._rows, saved._cols, m[0], m[2], m[3], _on(stream))
     if rc:
         _check(rc)
 
@@ -292,8 +287,10 @@ def zero_act_forward8(kind, x, out, saved, up=None, saved_up=None, stream=None):
     columns of one buffer; out may be x or up itself."""
     if (up is None) != (saved_up is None):
         raise ValueError("up and saved_up go together")
-    here, rows, cols = _here(saved.codes, "saved.codes", _INT8), saved.rows, saved.cols
-    s, su = _saved(saved, "saved", here), _saved(saved_up, "saved_up", here, rows, cols)
+    rows, cols = saved._rows, saved._cols
+    s = _saved(saved, "saved")
+    here = s[0]
+    su = _saved(saved_up, "saved_up", here, rows, cols)
     m = _rows(x, "x", rows, cols, _FLOATS, here)
     dt = {x.dtype: m[2]}
     y = _rows(out, "out", rows, cols, dt, here, True)
@@ -301,7 +298,7 @@ def zero_act_forward8(kind, x, out, saved, up=None, saved_up=None, stream=None):
     _apart_all([("out", y)] + _parts("saved", s) + _parts("saved_up", su), [("x", m), ("up", u)],
                (("out", "x"), ("out", "up")))
     rc = _lib.zero_act_forward8(kind, m[0], m[3], _at(u), 0 if u is None else u[3], m[2], rows, cols, y[0], y[3],
-                                s[0][0], s[1][0], _at(su[0]), _at(su[1]), _on(stream))
+                                s[1][0], s[2][0], _at(su[1]), _at(su[2]), _on(stream))
     if rc:
         _check(rc)
 
@@ -313,8 +310,10 @@ def zero_act_backward8(kind, dy, saved, dx, saved_up=None, dup=None, again=None,
     may be dy itself."""
     if (dup is None) != (saved_up is None):
         raise ValueError("dup and saved_up go together")
-    here, rows, cols = _here(saved.codes, "saved.codes", _INT8), saved.rows, saved.cols
-    s, su = _saved(saved, "saved", here), _saved(saved_up, "saved_up", here, rows, cols)
+    rows, cols = saved._rows, saved._cols
+    s = _saved(saved, "saved")
+    here = s[0]
+    su = _saved(saved_up, "saved_up", here, rows, cols)
     sa = _saved(again, "again", here, rows, cols)
     d = _rows(dy, "dy", rows, cols, _FLOATS, here)
     dt = {dy.dtype: d[2]}
@@ -322,8 +321,8 @@ def zero_act_backward8(kind, dy, saved, dx, saved_up=None, dup=None, again=None,
     u = None if dup is None else _rows(dup, "dup", rows, cols, dt, here, True)
     _apart_all([("dx", x), ("dup", u)] + _parts("again", sa),
                [("dy", d)] + _parts("saved", s) + _parts("saved_up", su), (("dx", "dy"), ("dup", "dy")))
-    rc = _lib.zero_act_backward8(kind, d[0], d[3], d[2], rows, cols, s[0][0], s[1][0], _at(su[0]), _at(su[1]), x[0], x[3],
-                                 _at(u), 0 if u is None else u[3], _at(sa[0]), _at(sa[1]), _on(stream))
+    rc = _lib.zero_act_backward8(kind, d[0], d[3], d[2], rows, cols, s[1][0], s[2][0], _at(su[1]), _at(su[2]), x[0], x[3],
+                                 _at(u), 0 if u is None else u[3], _at(sa[1]), _at(sa[2]), _on(stream))
     if rc:
         _check(rc)
 
@@ -342,12 +341,11 @@ def zero_weight_grad8(dy, saved, grad, accumulate=False, workspace=None, stream=
     checkpoint of its input; with `accumulate` added to what grad holds.  dy: (rows,
     outs), fp16 or bf16; grad: a view of the flat gradient, fp32, fp16 or bf16.
     The workspace is as zero_embed_grad's."""
-    here = _here(saved.codes, "saved.codes", _INT8)
-    c, e = _saved(saved, "saved", here)
+    here, c, e = _saved(saved, "saved")
     g = _flat(grad, "grad", _FLOATS, here)
-    if grad.dim() != 2 or grad.shape[1] != saved.cols:
-        raise ValueError("grad must be a matrix of %d columns" % saved.cols)
-    rows, cols, outs = saved.rows, saved.cols, grad.shape[0]
+    if grad.dim() != 2 or grad.shape[1] != saved._cols:
+        raise ValueError("grad must be a matrix of %d columns" % saved._cols)
+    rows, cols, outs = saved._rows, saved._cols, grad.shape[0]
     d = _rows(dy, "dy", rows, outs, _HALVES, here)
     _apart(g, d, "grad", "dy")
     _apart(g, c, "grad", "saved.codes")
