@@ -919,6 +919,9 @@ int zero_embed_grad(const void* tokens, int32_t token_bytes, int64_t n_tokens, i
     if (w.bytes > 0 && (!workspace || workspace_bytes < w.bytes))
         return fail(ZERO_EINVAL, "%s: the workspace needs %lld bytes", fn, (long long)w.bytes);
     if (w.bytes > 0 && !aligned(workspace, 16)) return fail(ZERO_EALIGN, "%s: workspace not 16-byte aligned", fn);
+    // (a row distance of 0 asks for more sums than dy has memory)
+    if (w.tiles * ((dim + 511) / 512) + vocab / 4 >= (int64_t)1 << 24)
+        return fail(ZERO_ERANGE, "%s: more than 2^24 tiles of sums", fn);
     zf::EmbedGradLaunch l;
     memset(&l, 0, sizeof l);
     l.sort.tokens = tokens;
@@ -1080,8 +1083,8 @@ int zero_act_backward8(int32_t kind, const void* dy, int64_t dy_ld, int32_t dtyp
 namespace {
 int weight_plan(const char* fn, int64_t rows, int64_t outs, int64_t cols, zf::WeightGrad* a, int64_t* bytes) {
     if (rows < 0 || outs < 0 || cols < 0) return fail(ZERO_EINVAL, "%s: negative size", fn);
-    if (rows > (int64_t)1 << 36 || outs > kMaxCols || cols > kMaxCols || outs * cols > (int64_t)1 << 38)
-        return fail(ZERO_ERANGE, "%s: more than 2^36 rows, 2^24 columns or 2^38 weights", fn);
+    if (rows > (int64_t)1 << 34 || outs > kMaxCols || cols > kMaxCols || outs * cols > (int64_t)1 << 38)
+        return fail(ZERO_ERANGE, "%s: more than 2^34 rows, 2^24 columns or 2^38 weights", fn);
     memset(a, 0, sizeof *a);
     a->rows = rows;
     a->outs = outs;

@@ -468,12 +468,21 @@ __global__ __launch_bounds__(kThreads) void embed_join_kernel(EmbedSum a) {
     const int64_t from = min(many, wave * share), to = min(many, from + share);
     float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
     if (n > 0) {
-#pragma unroll 4
-        for (int64_t j = from; j < to; ++j) {
-            const float* p = a.partials + ((tile + j) * 2 + (j == 0)) * a.pitch + col;
-            const v4f x = *reinterpret_cast<const v4f*>(p), y = *reinterpret_cast<const v4f*>(p + 4);
+        for (int64_t j0 = from; j0 < to; j0 += kEmbedBatch) {
+            // places behind the last repeat it: their rows are not used
+            v4f x[kEmbedBatch], y[kEmbedBatch];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) { acc[c] += x[c]; acc[4 + c] += y[c]; }
+            for (int j = 0; j < kEmbedBatch; ++j) {
+                const int64_t t = min(j0 + j, to - 1);
+                const float* p = a.partials + ((tile + t) * 2 + (t == 0)) * a.pitch + col;
+                x[j] = *reinterpret_cast<const v4f*>(p);
+                y[j] = *reinterpret_cast<const v4f*>(p + 4);
+            }
+#pragma unroll
+            for (int j = 0; j < kEmbedBatch; ++j)
+                if (j0 + j < to)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) { acc[c] += x[j][c]; acc[4 + c] += y[j][c]; }
         }
     }
     *reinterpret_cast<v4f*>(&part[wave][lane * 8]) = v4f{acc[0], acc[1], acc[2], acc[3]};
@@ -488,14 +497,15 @@ __global__ __launch_bounds__(kThreads) void embed_join_kernel(EmbedSum a) {
 }
 
 // The gradient of up to kEmbedFew tokens, without a sort.  The block holds every
-// token's row; its wave w looks for the others of position 8 * block + w.  The wave
-// that has the first of them sums them all in order, or, of more than kEmbedLong,
-// leaves them to the whole block: each wave an eighth of the positions, the eighths
-// added in order.  The blocks behind write zeros to the rows without a token, 64
-// each.  One launch, whose time is the chain of tokens, comparisons, rows.
-constexpr int kFewWaves = 8, kFewThreads = kFewWaves * 64, kEmbedLong = 16, kFewRows = 64, kFewBatch = 16;
+// token's row and takes 512 columns; its wave w looks for the others of position
+// 8 * block + w.  The wave that has the first of them sums them all in order, or, of
+// more than kEmbedLong, leaves them to the whole block: each wave an eighth of the
+// positions, the eighths added in order.  The blocks behind write zeros to the rows
+// without a token, 16 each.  One launch, whose time is the chain of tokens,
+// comparisons, rows.
+constexpr int kFewWaves = 8, kFewThreads = kFewWaves * 64, kEmbedLong = 16, kFewRows = 16, kFewBatch = 16;
 
-template <int TD, int TG>
+template <int TD, int TG, bool NARROW>
 __global__ __launch_bounds__(kFewThreads) void embed_few_kernel(EmbedSort t, EmbedSum a) {
     __shared__ uint32_t keys[kEmbedFew];
     __shared__ uint16_t list[kFewWaves][kEmbedFew / kFewWaves];
@@ -504,7 +514,9 @@ __global__ __launch_bounds__(kFewThreads) void embed_few_kernel(EmbedSort t, Emb
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     const int n = (int)t.n_tokens, blocks = (n + kFewWaves - 1) / kFewWaves;
     const uint32_t none = (uint32_t)t.vocab;
+    const int64_t col = (int64_t)blockIdx.y * kChunk + lane * 8;
     if ((int)blockIdx.x >= blocks) {
+        if (blockIdx.y) return;                            // whole rows
         const uint32_t v0 = (blockIdx.x - blocks) * kFewRows;
         if (threadIdx.x < kFewRows) keys[threadIdx.x] = 0;
         __syncthreads();
@@ -518,15 +530,17 @@ __global__ __launch_bounds__(kFewThreads) void embed_few_kernel(EmbedSort t, Emb
             const int64_t v = (int64_t)v0 + r;
             if (v >= t.vocab) break;
             if (keys[r]) continue;
-            for (int64_t col = lane * 8; col < a.dim; col += kChunk)
-                store8<TG>(a.grad, v * a.dim + col, (int)min((int64_t)8, a.dim - col), zero, a.stream);
+            for (int64_t c = lane * 8; c < a.dim; c += kChunk)
+                store8<TG>(a.grad, v * a.dim + c, (int)min((int64_t)8, a.dim - c), zero, a.stream);
         }
         return;
     }
     for (int i = threadIdx.x; i < n; i += kFewThreads) keys[i] = key_at(t, i);
     __syncthreads();
+    const Window w = window_at(col, a.dim);
     const int mine = blockIdx.x * kFewWaves + wave;
     const uint32_t key = mine < n ? (uint32_t)uniform((int)keys[mine]) : none;
+    float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
     // positions of `k` within [from, to) into this wave's list, in order
     auto gather = [&](uint32_t k, int from, int to) {
         int have = 0;
@@ -536,20 +550,22 @@ __global__ __launch_bounds__(kFewThreads) void embed_few_kernel(EmbedSort t, Emb
             if (hit) list[wave][have + __popcll(m & ((1ull << lane) - 1))] = (uint16_t)(j + lane);
             have += __popcll(m);
         }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         return have;
     };
-    auto sum = [&](int have, int64_t col, int cols, float (&acc)[8]) {
+    auto sum = [&](int have) {
         for (int j0 = 0; j0 < have; j0 += kFewBatch) {
-            float x[kFewBatch][8];
+            // places behind the end repeat the last one: their rows are not used
+            const int here = list[wave][min(j0 + (lane & (kFewBatch - 1)), have - 1)];
+            Raw8<TD> raw[kFewBatch];
 #pragma unroll
             for (int j = 0; j < kFewBatch; ++j)
-                if (j0 + j < have && cols > 0)
-                    load8<TD>(a.dy, (int64_t)uniform(list[wave][j0 + j]) * a.dy_ld + col, cols, x[j]);
+                raw[j] = fetch_row<TD, NARROW>(a, __builtin_amdgcn_readlane(here, j), w);
 #pragma unroll
             for (int j = 0; j < kFewBatch; ++j)
                 if (j0 + j < have)
 #pragma unroll
-                    for (int c = 0; c < 8; ++c) acc[c] += x[j][c];
+                    for (int c = 0; c < 8; ++c) acc[c] += element<TD>(raw[j], c);
         }
     };
     // the first of its token?  how many are there?
@@ -561,40 +577,28 @@ __global__ __launch_bounds__(kFewThreads) void embed_few_kernel(EmbedSort t, Emb
             for (int j = mine; j < n; j += 64) count += __popcll(__ballot(j + lane < n && keys[j + lane] == key));
     }
     if (count > 0 && count <= kEmbedLong) {
-        gather(key, mine, n);
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        for (int64_t c0 = 0; c0 < a.dim; c0 += kChunk) {
-            const int64_t col = c0 + lane * 8;
-            const int cols = (int)min((int64_t)8, a.dim - col);
-            float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-            sum(count, col, cols, acc);
-            if (cols > 0) write_row<TG>(a, key, col, 0, cols, acc);
-        }
+        sum(gather(key, mine, n));
+        write_row<TG>(a, key, w.col, w.skip, w.n, acc);
     }
     if (lane == 0) longs[wave] = count > kEmbedLong ? key : none;
     __syncthreads();
-    for (int w = 0; w < kFewWaves; ++w) {
-        const uint32_t k = (uint32_t)uniform((int)longs[w]);
+    for (int other = 0; other < kFewWaves; ++other) {
+        const uint32_t k = (uint32_t)uniform((int)longs[other]);
         if (k == none) continue;
         const int share = (n + kFewThreads - 1) / kFewThreads * 64;
-        const int have = gather(k, min(n, wave * share), min(n, (wave + 1) * share));
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        for (int64_t c0 = 0; c0 < a.dim; c0 += kChunk) {
-            const int64_t col = c0 + lane * 8;
-            const int cols = (int)min((int64_t)8, a.dim - col);
-            float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-            sum(have, col, cols, acc);
-            *reinterpret_cast<v4f*>(&part[wave][lane * 8]) = v4f{acc[0], acc[1], acc[2], acc[3]};
-            *reinterpret_cast<v4f*>(&part[wave][lane * 8 + 4]) = v4f{acc[4], acc[5], acc[6], acc[7]};
-            __syncthreads();
-            if (wave == 0 && cols > 0) {
-                for (int u = 1; u < kFewWaves; ++u)
 #pragma unroll
-                    for (int c = 0; c < 8; ++c) acc[c] += part[u][lane * 8 + c];
-                write_row<TG>(a, k, col, 0, cols, acc);
-            }
-            __syncthreads();
+        for (int c = 0; c < 8; ++c) acc[c] = 0.0f;
+        sum(gather(k, min(n, wave * share), min(n, (wave + 1) * share)));
+        *reinterpret_cast<v4f*>(&part[wave][lane * 8]) = v4f{acc[0], acc[1], acc[2], acc[3]};
+        *reinterpret_cast<v4f*>(&part[wave][lane * 8 + 4]) = v4f{acc[4], acc[5], acc[6], acc[7]};
+        __syncthreads();
+        if (wave == 0) {
+            for (int u = 1; u < kFewWaves; ++u)
+#pragma unroll
+                for (int c = 0; c < 8; ++c) acc[c] += part[u][lane * 8 + c];
+            write_row<TG>(a, k, w.col, w.skip, w.n, acc);
         }
+        __syncthreads();
     }
 }
 
@@ -619,11 +623,16 @@ void sum_to(const EmbedSum& a, int grad, dim3 grid, hipStream_t s) {
     else sum_of<TD, ZERO_BF16>(a, grid, s);
 }
 
+template <int TD, int TG>
+void few_of(const EmbedSort& t, const EmbedSum& a, dim3 grid, hipStream_t s) {
+    if (a.dim >= 8) embed_few_kernel<TD, TG, false><<<grid, kFewThreads, 0, s>>>(t, a);
+    else embed_few_kernel<TD, TG, true><<<grid, kFewThreads, 0, s>>>(t, a);
+}
 template <int TD>
 void few_to(const EmbedSort& t, const EmbedSum& a, int grad, dim3 grid, hipStream_t s) {
-    if (grad == ZERO_F32) embed_few_kernel<TD, ZERO_F32><<<grid, kFewThreads, 0, s>>>(t, a);
-    else if (grad == ZERO_F16) embed_few_kernel<TD, ZERO_F16><<<grid, kFewThreads, 0, s>>>(t, a);
-    else embed_few_kernel<TD, ZERO_BF16><<<grid, kFewThreads, 0, s>>>(t, a);
+    if (grad == ZERO_F32) few_of<TD, ZERO_F32>(t, a, grid, s);
+    else if (grad == ZERO_F16) few_of<TD, ZERO_F16>(t, a, grid, s);
+    else few_of<TD, ZERO_BF16>(t, a, grid, s);
 }
 
 }  // namespace
@@ -659,9 +668,10 @@ int launch_embed_grad(const EmbedGradLaunch& l, void* stream) {
     EmbedSum b = l.sum;
     // of an accumulated gradient only the rows that tokens name are written
     b.stream = streams((b.accumulate ? (a.n_tokens < a.vocab ? a.n_tokens : a.vocab) : a.vocab) * row_bytes);
-    if (a.n_tokens <= kEmbedFew) {
+    if (embed_few(a.n_tokens, b.dim)) {
         const int64_t rows = l.sum.accumulate ? 0 : a.vocab;
-        const dim3 grid((uint32_t)((a.n_tokens + kFewWaves - 1) / kFewWaves + (rows + kFewRows - 1) / kFewRows));
+        const dim3 grid((uint32_t)((a.n_tokens + kFewWaves - 1) / kFewWaves + (rows + kFewRows - 1) / kFewRows),
+                        (uint32_t)((b.dim + kChunk - 1) / kChunk));
         if (l.dy_dtype == ZERO_F32) few_to<ZERO_F32>(a, b, l.grad_dtype, grid, s);
         else if (l.dy_dtype == ZERO_F16) few_to<ZERO_F16>(a, b, l.grad_dtype, grid, s);
         else few_to<ZERO_BF16>(a, b, l.grad_dtype, grid, s);

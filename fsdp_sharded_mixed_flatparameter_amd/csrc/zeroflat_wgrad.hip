@@ -263,9 +263,8 @@ __global__ __launch_bounds__(WO * WI * 64) void weight_grad_kernel(WeightGrad a)
     const uint16_t* yread = ysh + krow * ly + kcol + wo * 16;
     auto xfrag = [&](int buf, int i) { return frag(xread + buf * kDepth * lx + i * 16, lx); };
     auto yfrag = [&](int buf, int o) { return frag(yread + buf * kDepth * ly + o * 16, ly); };
-    // Multiplies the step whose operands are held ; row by row they
-    // give way to those of the next one, in the other buffer, and `work` gets its
-    // turns beside them.
+    // Multiplies the step whose operands are held; row by row they give way to those of
+    // the next one, in the other buffer, and `work` gets its turns beside them.
     auto multiply = [&](int buf, bool more, auto work) {
 #pragma unroll
         for (int o = 0; o < S::fo; ++o) {

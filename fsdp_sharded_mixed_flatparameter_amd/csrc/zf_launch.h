@@ -171,7 +171,7 @@ int launch_multi_step(const MultiAdamLaunch& a, const MultiNormLaunch* norm, con
 
 // The embedding (zeroflat_embed.hip).
 constexpr int kEmbedInt8 = 3;            // a table's type beside zero_dtype_t: the INT8 payload
-constexpr int kEmbedFew = 4096;          // tokens whose gradient needs no sort
+constexpr int kEmbedFew = 2048;          // tokens whose gradient needs no sort, at most
 constexpr int kEmbedSortTile = 1024;     // tokens of one block of the sort
 constexpr int64_t kEmbedZeroBytes = 40 << 20;   // of zeros that a launch of the sort writes beside it
 constexpr int kEmbedScanBlocks = 128;    // blocks that sum the counts before theirs themselves
@@ -249,17 +249,29 @@ struct EmbedGradLaunch {
 };
 int launch_embed_grad(const EmbedGradLaunch& a, void* stream);
 
+// Few tokens find one another by comparing, in one launch: n * n comparisons for
+// every 512 columns.  In us, and by the sort with its five launches at least (zipf tokens,
+// added to 32000 bf16 rows): 512 x 256 8, 26; 512 x 4096 10, 25; 1024 x 1024 10, 26;
+// 2048 x 256 17, 29; beyond the limit 1024 x 4096 27, 27; 2048 x 1024 29, 28; 4096 x 256
+// 31, 30.  One token 2048 times: 30, 26.
+inline bool embed_few(int64_t n, int64_t dim) {
+    const int64_t chunks = dim > 512 ? (dim + 511) / 512 : 1;
+    return n <= kEmbedFew && n * n * chunks <= (int64_t)kEmbedFew * kEmbedFew;
+}
+
 // The parts of its workspace, as byte offsets.
 struct EmbedWorkspace {
     int64_t keys[2], places[2], hist, flags, partials, bytes;
     int64_t tiles, pitch;
     int32_t tile;
 };
-// The tile: long enough that its partial rows (fp32, two at most) are little
-// beside its rows, short enough that few tokens spread over the chip.
+// The tile: long enough that its partial rows (fp32, two at most) are little beside
+// its rows, short enough that few tokens spread over the chip.  128 and 32 positions,
+// us: 5000 x 512 37, 30; 16384 x 512 41, 34; 32768 x 512 44, 42; 16384 x 2048 59, 58;
+// 65536 x 512 57, 59; 131072 x 1024 117, 118.
 inline EmbedWorkspace embed_workspace(int64_t n, int64_t vocab, int64_t dim) {
     EmbedWorkspace w{};
-    if (n <= kEmbedFew) return w;
+    if (embed_few(n, dim)) return w;
     const auto up = [](int64_t x) { return (x + 255) / 256 * 256; };
     w.tile = n * ((dim + 511) / 512) >= 65536 ? kEmbedTile : 32;
     w.tiles = (n + w.tile - 1) / w.tile;

@@ -610,8 +610,8 @@ int zero_multi_adamw_step_args(const zero_multi_step_args_t* args, void* stream)
  * sorted by token, and no atomic adds values.  padding: HOST pointer or NULL.
  * dy_ld >= 0 elements between rows (0: every token has the same row).
  * workspace: DEVICE, 16-byte aligned, of the bytes that zero_embed_grad_workspace
- *   gives (0 up to 4,096 tokens; else about 17 bytes per token, one per row and an fp32 row
- *   per 64 tokens), used from the call's first kernel to its last: calls that overlap
+ *   gives (0 for few tokens; else about 17 bytes per token, one per row and an fp32 row per
+ *   64 tokens), used from the call's first kernel to its last: calls that overlap
  *   need one each.
  * At most 2^28 tokens, 2^25 rows, 2^24 columns.
  * ---------------------------------------------------------------------- */

@@ -60,7 +60,7 @@ def test_lookup_in_the_payload_refuses(zf, kw, code):
     (dict(token_bytes=0), EINVAL), (dict(n=-1), EINVAL), (dict(tokens=None), EINVAL), (dict(ddt=3), EINVAL),
     (dict(gdt=9), EINVAL), (dict(ld=-1), EINVAL), (dict(n=1 << 28, ld=1 << 40), ERANGE), (dict(flags=1), EINVAL),
     (dict(dy=None), EINVAL), (dict(g=None), EINVAL), (dict(dy=at(0x10001)), EALIGN), (dict(g=at(0x10002), gdt=0), EALIGN),
-    (dict(n=5000, ws=None), EINVAL), (dict(n=5000, bytes_=100), EINVAL), (dict(n=5000, ws=at(0x10008)), EALIGN)])
+    (dict(n=1 << 28, dim=1 << 14, ld=0, bytes_=1 << 62), ERANGE), (dict(n=5000, ws=None), EINVAL), (dict(n=5000, bytes_=100), EINVAL), (dict(n=5000, ws=at(0x10008)), EALIGN)])
 def test_grad_refuses(zf, kw, code):
     assert grad(zf, **kw) == code
     assert zf.lib().zero_last_error().decode().startswith("zero_embed_grad: ")

@@ -165,6 +165,11 @@ GRADS = [  # tokens, vocab, dim, dy, grad, accumulate, shift, wide
     (4097, 65536, 8, "bf16", "fp32", False, 1, True), (5000, 2, 33, "fp32", "fp32", True, 0, True),
     (30011, 50021, 24, "bf16", "fp32", True, 1, True), (20000, 300000, 8, "fp16", "bf16", False, 0, True),
     (131072, 777, 8, "bf16", "fp32", False, 0, True), (131073, 70000, 8, "bf16", "fp16", True, 0, False),
+    # either side of where the sort begins: tokens, and tokens by columns
+    (2048, 300, 24, "bf16", "bf16", False, 1, True), (2049, 300, 24, "bf16", "bf16", False, 1, True),
+    (600, 50, 4100, "bf16", "fp32", True, 0, True), (700, 50, 4100, "fp16", "fp16", False, 3, True),
+    (1024, 400, 1030, "fp32", "bf16", False, 0, True), (2048, 5, 3, "fp32", "fp32", True, 1, False),
+    (2100, 5, 3, "fp16", "fp32", False, 1, False), (300, 17, 8, "bf16", "bf16", True, 1, True),
     (70000, 1, 5, "fp32", "fp32", False, 0, True), (0, 50, 16, "bf16", "bf16", False, 0, True),
     (0, 50, 16, "bf16", "bf16", True, 0, True), (9, 0, 16, "bf16", "bf16", False, 0, True),
     (9, 5, 0, "bf16", "bf16", False, 0, True)]
@@ -195,7 +200,8 @@ def test_grad(zf, n, vocab, dim, dyt, gt, accumulate, shift, wide):
         assert torch.equal(grad[~hit[:-1]], old[~hit[:-1]])
 
 
-@pytest.mark.parametrize("n,vocab,dim", [(3000, 40, 24), (4096, 4096, 8), (50000, 3000, 17), (200000, 60000, 9)])
+@pytest.mark.parametrize("n,vocab,dim", [(500, 3, 40), (2000, 40, 24), (3000, 40, 24), (4096, 4096, 8), (50000, 3000, 17),
+                                         (200000, 60000, 9), (70000, 300, 1500)])
 @pytest.mark.parametrize("accumulate", (False, True))
 def test_grad_of_whole_numbers_is_exact(zf, n, vocab, dim, accumulate):
     """Whole numbers whose sums fp32 holds: every order of adding gives the same,
