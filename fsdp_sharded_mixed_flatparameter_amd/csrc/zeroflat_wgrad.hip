@@ -143,8 +143,8 @@ struct Tile {
     static_assert(y_loads * 8 * threads == kDepth * TO && x_loads * 16 * threads == kDepth * TI, "whole loads");
 };
 
-template <int DT, int TO, int TI, int WO, int WI>
-__global__ __launch_bounds__(WO * WI * 64) void weight_grad_kernel(WeightGrad a) {
+template <int DT, int TO, int TI, int WO, int WI, int SETS>
+__global__ __launch_bounds__(WO * WI * 64, 2) void weight_grad_kernel(WeightGrad a) {
     using S = Tile<TO, TI, WO, WI>;
     constexpr int ly = TO + kPad, lx = TI + kPad;
     __shared__ __attribute__((aligned(16))) uint16_t ysh[2 * kDepth * ly];
@@ -178,9 +178,10 @@ __global__ __launch_bounds__(WO * WI * 64) void weight_grad_kernel(WeightGrad a)
     const uint32_t eat = (uint32_t)(xk * (a.pitch / 32) + i / 32);
     const int64_t ystep = yrows * a.dy_ld * 2, xstep = xrows * a.pitch;
 
-    // two steps' loads on their way
-    v4u yreg[2][S::y_loads], xreg[2][S::x_loads];
-    uint32_t ereg[2][S::x_loads];
+    // SETS steps' loads on their way
+    static_assert(SETS % 2 == 0, "a set goes to one buffer");
+    v4u yreg[SETS][S::y_loads], xreg[SETS][S::x_loads];
+    uint32_t ereg[SETS][S::x_loads];
     auto fetch_y = [&](int set, int j) { yreg[set][j] = *reinterpret_cast<const v4u_any*>(yp + j * ystep + yat); };
     auto fetch_x = [&](int set, int j) {
         xreg[set][j] = *reinterpret_cast<const v4u*>(xp + j * xstep + xat);
@@ -226,9 +227,9 @@ __global__ __launch_bounds__(WO * WI * 64) void weight_grad_kernel(WeightGrad a)
             }
         }
     };
-    // set k goes to buffer k
+    // set k goes to buffer k % 2
     auto stage_y = [&](int set, int j) {
-        *reinterpret_cast<v4u*>(&ysh[(set * kDepth + yk + j * yrows) * ly + ycol]) = yreg[set][j];
+        *reinterpret_cast<v4u*>(&ysh[(set % 2 * kDepth + yk + j * yrows) * ly + ycol]) = yreg[set][j];
     };
     v4u half;
     auto stage_x = [&](int set, int w) {       // word w % 4 of load w / 4
@@ -236,7 +237,7 @@ __global__ __launch_bounds__(WO * WI * 64) void weight_grad_kernel(WeightGrad a)
         half[2 * (w & 1)] = r[0];
         half[2 * (w & 1) + 1] = r[1];
         if (w & 1)
-            *reinterpret_cast<v4u*>(&xsh[(set * kDepth + xk + w / 4 * xrows) * lx + xcol + (w & 2) * 4]) = half;
+            *reinterpret_cast<v4u*>(&xsh[(set % 2 * kDepth + xk + w / 4 * xrows) * lx + xcol + (w & 2) * 4]) = half;
     };
     auto stage = [&](int set) {
 #pragma unroll
@@ -281,14 +282,14 @@ __global__ __launch_bounds__(WO * WI * 64) void weight_grad_kernel(WeightGrad a)
 
     // Step s multiplies what was read from buffer s % 2 during step s - 1, reads step
     // s + 1 from the other buffer, writes step s + 2 over its own and issues the loads
-    // of step s + 4.
+    // of step s + 2 + SETS.  Step n's loads are in set n % SETS.
     if (steps > 0) {
         fetch(0, 0);
         fetch(1, 1);
         stage(0);
         if (steps > 1) stage(1);
-        fetch(0, 2);
-        fetch(1, 3);
+#pragma unroll
+        for (int n = 2; n < 2 + SETS; ++n) fetch(n % SETS, n);
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < S::fi; ++i) x[i] = xfrag(0, i);
@@ -297,35 +298,38 @@ __global__ __launch_bounds__(WO * WI * 64) void weight_grad_kernel(WeightGrad a)
         __syncthreads();
     }
     int s = 0;
-    yp += 4 * kDepth * a.dy_ld * 2;
-    xp += 4 * kDepth * a.pitch;
-    ep += 4 * kDepth * (a.pitch / 32);
-    for (; s + 5 < whole; s += 2) {
+    yp += (2 + SETS) * kDepth * a.dy_ld * 2;
+    xp += (2 + SETS) * kDepth * a.pitch;
+    ep += (2 + SETS) * kDepth * (a.pitch / 32);
+    for (; s + 2 * SETS + 1 < whole; s += SETS) {
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            multiply(k, true, [&](int o) {
+        for (int k = 0; k < SETS; ++k) {
+            constexpr int fo = S::fo;
+            const int set = (k + 2) % SETS;
+            multiply(k % 2, true, [&](int o) {
 #pragma unroll
-                for (int j = o * S::y_loads / S::fo; j < (o + 1) * S::y_loads / S::fo; ++j) {
-                    stage_y(k, j);
-                    fetch_y(k, j);
+                for (int j = o * S::y_loads / fo; j < (o + 1) * S::y_loads / fo; ++j) {
+                    stage_y(set, j);
+                    fetch_y(set, j);
                 }
 #pragma unroll
-                for (int w = o * 4 * S::x_loads / S::fo; w < (o + 1) * 4 * S::x_loads / S::fo; ++w) {
-                    stage_x(k, w);
-                    if (w % 4 == 3) fetch_x(k, w / 4);
+                for (int w = o * 4 * S::x_loads / fo; w < (o + 1) * 4 * S::x_loads / fo; ++w) {
+                    stage_x(set, w);
+                    if (w % 4 == 3) fetch_x(set, w / 4);
                 }
             });
             advance();
             __syncthreads();
         }
     }
-    for (; s < steps; s += 2) {
+    for (; s < steps; s += SETS) {
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
+        for (int k = 0; k < SETS; ++k) {
             if (s + k < steps) {
-                if (s + k + 2 < steps) stage(k);
-                fetch(k, s + k + 4);
-                multiply(k, s + k + 1 < steps, [](int) {});
+                const int set = (k + 2) % SETS;
+                if (s + k + 2 < steps) stage(set);
+                fetch(set, s + k + 2 + SETS);
+                multiply(k % 2, s + k + 1 < steps, [](int) {});
                 __syncthreads();
             }
         }
@@ -376,19 +380,19 @@ __global__ __launch_bounds__(256) void weight_join_kernel(WeightGrad a) {
     finish4(a, row * a.cols + col, n, sum);
 }
 
-template <int DT, int TO, int TI, int WO, int WI>
+template <int DT, int TO, int TI, int WO, int WI, int SETS>
 int launch_tile(const WeightGrad& a, hipStream_t s) {
     const int64_t rest = a.tiles - a.whole_tiles;
-    weight_grad_kernel<DT, TO, TI, WO, WI><<<(uint32_t)(a.whole_tiles + rest * a.splits), WO * WI * 64, 0, s>>>(a);
+    weight_grad_kernel<DT, TO, TI, WO, WI, SETS><<<(uint32_t)(a.whole_tiles + rest * a.splits), WO * WI * 64, 0, s>>>(a);
     if (const int e = (int)hipGetLastError()) return e;
     if (rest) weight_join_kernel<TO, TI, WO, WI><<<(uint32_t)(rest * (TO * TI / 1024)), 256, 0, s>>>(a);
     return (int)hipGetLastError();
 }
 template <int DT>
 int launch_dt(const WeightGrad& a, hipStream_t s) {
-    if (a.tile == 256) return launch_tile<DT, 256, 256, 2, 4>(a, s);
-    if (a.tile == 128) return launch_tile<DT, 128, 128, 2, 2>(a, s);
-    return launch_tile<DT, 64, 64, 1, 2>(a, s);
+    if (a.tile == 256) return launch_tile<DT, 256, 256, 2, 4, 2>(a, s);
+    if (a.tile == 128) return launch_tile<DT, 128, 128, 2, 2, 4>(a, s);
+    return launch_tile<DT, 64, 64, 1, 2, 4>(a, s);
 }
 
 }  // namespace
