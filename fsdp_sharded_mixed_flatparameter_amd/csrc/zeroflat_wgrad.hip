@@ -14,7 +14,6 @@
 namespace zf {
 namespace {
 
-constexpr int kDepth = 32;                 // rows t of one step
 
 typedef signed char v4c __attribute__((ext_vector_type(4)));
 typedef short v4s __attribute__((ext_vector_type(4)));
@@ -133,35 +132,36 @@ __device__ __forceinline__ Unit unit_of(const WeightGrad& a, uint32_t b) {
     return u;
 }
 
-// A block's tile is TO outputs o by TI inputs i, its waves WO by WI of them.
-template <int TO, int TI, int WO, int WI>
+// A block's tile is TO outputs o by TI inputs i, its waves WO by WI of them; a step is
+// DEPTH rows t, 32 for every matrix instruction.
+template <int TO, int TI, int WO, int WI, int DEPTH>
 struct Tile {
     static constexpr int threads = WO * WI * 64;
     static constexpr int fo = TO / WO / 16, fi = TI / WI / 16;      // 16 x 16 fragments of a wave
-    static constexpr int y_loads = kDepth * TO / 8 / threads;       // 16 bytes each
-    static constexpr int x_loads = kDepth * TI / 16 / threads;
-    static_assert(y_loads * 8 * threads == kDepth * TO && x_loads * 16 * threads == kDepth * TI, "whole loads");
+    static constexpr int y_loads = DEPTH * TO / 8 / threads;       // 16 bytes each
+    static constexpr int x_loads = DEPTH * TI / 16 / threads;
+    static_assert(y_loads * 8 * threads == DEPTH * TO && x_loads * 16 * threads == DEPTH * TI, "whole loads");
 };
 
-template <int DT, int TO, int TI, int WO, int WI, int SETS>
+template <int DT, int TO, int TI, int WO, int WI, int DEPTH, int SETS>
 __global__ __launch_bounds__(WO * WI * 64, 2) void weight_grad_kernel(WeightGrad a) {
-    using S = Tile<TO, TI, WO, WI>;
+    using S = Tile<TO, TI, WO, WI, DEPTH>;
     constexpr int ly = TO + kPad, lx = TI + kPad;
-    __shared__ __attribute__((aligned(16))) uint16_t ysh[2 * kDepth * ly];
-    __shared__ __attribute__((aligned(16))) uint16_t xsh[2 * kDepth * lx];
+    __shared__ __attribute__((aligned(16))) uint16_t ysh[2 * DEPTH * ly];
+    __shared__ __attribute__((aligned(16))) uint16_t xsh[2 * DEPTH * lx];
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
     const Unit u = unit_of(a, blockIdx.x);
     const int64_t o0 = (int64_t)u.to * TO, i0 = (int64_t)u.ti * TI;
     const bool shared = u.shared;
     const int64_t t0 = shared ? u.split * a.share : 0, t1 = shared ? min(a.rows, t0 + a.share) : a.rows;
-    const int steps = (int)((t1 - t0 + kDepth - 1) / kDepth);
+    const int steps = (int)((t1 - t0 + DEPTH - 1) / DEPTH);
     // Steps whose loads need no test.  Columns beyond the matrix are read from
     // inside it (their results are not written), but for a last group of fewer
     // than eight outputs, which runs into the next row: there has to be one.  A
     // thread's rows are within 32 bits of a step's first.
     const bool over = a.outs % 8 != 0;
     const int whole = a.outs < 8 || (over && a.dy_ld < a.outs) || a.dy_ld > (int64_t)1 << 25 ? 0
-        : (int)((min(t1, a.rows - (over ? 1 : 0)) - t0) / kDepth);
+        : (int)((min(t1, a.rows - (over ? 1 : 0)) - t0) / DEPTH);
 
     // This thread's part of a step: groups of eight outputs and of sixteen codes.
     constexpr int ywide = TO / 8, xwide = TI / 16;             // in a row
@@ -188,9 +188,9 @@ __global__ __launch_bounds__(WO * WI * 64, 2) void weight_grad_kernel(WeightGrad
         ereg[set][j] = *reinterpret_cast<const uint8_t*>(ep + j * (xstep / 32) + eat);
     };
     auto advance = [&]() {
-        yp += kDepth * a.dy_ld * 2;
-        xp += kDepth * a.pitch;
-        ep += kDepth * (a.pitch / 32);
+        yp += DEPTH * a.dy_ld * 2;
+        xp += DEPTH * a.pitch;
+        ep += DEPTH * (a.pitch / 32);
     };
     auto fetch = [&](int set, int n) {         // step n, zeros beyond the rows
         if (n >= steps) return;
@@ -200,7 +200,7 @@ __global__ __launch_bounds__(WO * WI * 64, 2) void weight_grad_kernel(WeightGrad
         asm volatile("" : "+v"(id));
         const int yk = id / ywide, xk = id / xwide;
         const int64_t o = min(o0 + id % ywide * 8, (a.outs - 1) / 8 * 8), i = min(i0 + id % xwide * 16, a.pitch - 16);
-        const int64_t t = t0 + (int64_t)n * kDepth;
+        const int64_t t = t0 + (int64_t)n * DEPTH;
 #pragma unroll
         for (int j = 0; j < S::y_loads; ++j) {
             const int64_t row = t + yk + j * yrows;
@@ -229,7 +229,7 @@ __global__ __launch_bounds__(WO * WI * 64, 2) void weight_grad_kernel(WeightGrad
     };
     // set k goes to buffer k % 2
     auto stage_y = [&](int set, int j) {
-        *reinterpret_cast<v4u*>(&ysh[(set % 2 * kDepth + yk + j * yrows) * ly + ycol]) = yreg[set][j];
+        *reinterpret_cast<v4u*>(&ysh[(set % 2 * DEPTH + yk + j * yrows) * ly + ycol]) = yreg[set][j];
     };
     v4u half;
     auto stage_x = [&](int set, int w) {       // word w % 4 of load w / 4
@@ -237,7 +237,7 @@ __global__ __launch_bounds__(WO * WI * 64, 2) void weight_grad_kernel(WeightGrad
         half[2 * (w & 1)] = r[0];
         half[2 * (w & 1) + 1] = r[1];
         if (w & 1)
-            *reinterpret_cast<v4u*>(&xsh[(set % 2 * kDepth + xk + w / 4 * xrows) * lx + xcol + (w & 2) * 4]) = half;
+            *reinterpret_cast<v4u*>(&xsh[(set % 2 * DEPTH + xk + w / 4 * xrows) * lx + xcol + (w & 2) * 4]) = half;
     };
     auto stage = [&](int set) {
 #pragma unroll
@@ -254,7 +254,8 @@ __global__ __launch_bounds__(WO * WI * 64, 2) void weight_grad_kernel(WeightGrad
     const int wo = wave / WI * S::fo, wi = wave % WI * S::fi;
     const int krow = 8 * (lane / 16) + lane % 16 / 4;            // this lane's row of a transposing load
     const int kcol = lane % 4 * 4;
-    v8s x[S::fi], y[S::fo];                     // a step's operands
+    constexpr int parts = DEPTH / 32;
+    v8s x[parts][S::fi], y[parts][S::fo];       // a step's operands
     auto frag = [&](const uint16_t* p, int row) {
         const v4s u = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(p));
         const v4s v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(p + 4 * row));
@@ -262,22 +263,25 @@ __global__ __launch_bounds__(WO * WI * 64, 2) void weight_grad_kernel(WeightGrad
     };
     const uint16_t* xread = xsh + krow * lx + kcol + wi * 16;
     const uint16_t* yread = ysh + krow * ly + kcol + wo * 16;
-    auto xfrag = [&](int buf, int i) { return frag(xread + buf * kDepth * lx + i * 16, lx); };
-    auto yfrag = [&](int buf, int o) { return frag(yread + buf * kDepth * ly + o * 16, ly); };
+    auto xfrag = [&](int buf, int part, int i) { return frag(xread + (buf * DEPTH + part * 32) * lx + i * 16, lx); };
+    auto yfrag = [&](int buf, int part, int o) { return frag(yread + (buf * DEPTH + part * 32) * ly + o * 16, ly); };
     // Multiplies the step whose operands are held; row by row they give way to those of
     // the next one, in the other buffer, and `work` gets its turns beside them.
+    constexpr int turns = parts * S::fo;
     auto multiply = [&](int buf, bool more, auto work) {
 #pragma unroll
-        for (int o = 0; o < S::fo; ++o) {
+        for (int p = 0; p < parts; ++p)
 #pragma unroll
-            for (int i = 0; i < S::fi; ++i) {
-                acc[o][i] = mfma<DT>(x[i], y[o], acc[o][i]);
-                if (more && o == S::fo - 1) x[i] = xfrag(1 - buf, i);
+            for (int o = 0; o < S::fo; ++o) {
+#pragma unroll
+                for (int i = 0; i < S::fi; ++i) {
+                    acc[o][i] = mfma<DT>(x[p][i], y[p][o], acc[o][i]);
+                    if (more && o == S::fo - 1) x[p][i] = xfrag(1 - buf, p, i);
+                }
+                if (more) y[p][o] = yfrag(1 - buf, p, o);
+                work(p * S::fo + o);
+                __builtin_amdgcn_sched_barrier(0);
             }
-            if (more) y[o] = yfrag(1 - buf, o);
-            work(o);
-            __builtin_amdgcn_sched_barrier(0);
-        }
     };
 
     // Step s multiplies what was read from buffer s % 2 during step s - 1, reads step
@@ -292,28 +296,30 @@ __global__ __launch_bounds__(WO * WI * 64, 2) void weight_grad_kernel(WeightGrad
         for (int n = 2; n < 2 + SETS; ++n) fetch(n % SETS, n);
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < S::fi; ++i) x[i] = xfrag(0, i);
+        for (int p = 0; p < parts; ++p) {
 #pragma unroll
-        for (int o = 0; o < S::fo; ++o) y[o] = yfrag(0, o);
+            for (int i = 0; i < S::fi; ++i) x[p][i] = xfrag(0, p, i);
+#pragma unroll
+            for (int o = 0; o < S::fo; ++o) y[p][o] = yfrag(0, p, o);
+        }
         __syncthreads();
     }
     int s = 0;
-    yp += (2 + SETS) * kDepth * a.dy_ld * 2;
-    xp += (2 + SETS) * kDepth * a.pitch;
-    ep += (2 + SETS) * kDepth * (a.pitch / 32);
+    yp += (2 + SETS) * DEPTH * a.dy_ld * 2;
+    xp += (2 + SETS) * DEPTH * a.pitch;
+    ep += (2 + SETS) * DEPTH * (a.pitch / 32);
     for (; s + 2 * SETS + 1 < whole; s += SETS) {
 #pragma unroll
         for (int k = 0; k < SETS; ++k) {
-            constexpr int fo = S::fo;
             const int set = (k + 2) % SETS;
-            multiply(k % 2, true, [&](int o) {
+            multiply(k % 2, true, [&](int turn) {
 #pragma unroll
-                for (int j = o * S::y_loads / fo; j < (o + 1) * S::y_loads / fo; ++j) {
+                for (int j = turn * S::y_loads / turns; j < (turn + 1) * S::y_loads / turns; ++j) {
                     stage_y(set, j);
                     fetch_y(set, j);
                 }
 #pragma unroll
-                for (int w = o * 4 * S::x_loads / fo; w < (o + 1) * 4 * S::x_loads / fo; ++w) {
+                for (int w = turn * 4 * S::x_loads / turns; w < (turn + 1) * 4 * S::x_loads / turns; ++w) {
                     stage_x(set, w);
                     if (w % 4 == 3) fetch_x(set, w / 4);
                 }
@@ -357,9 +363,9 @@ __global__ __launch_bounds__(WO * WI * 64, 2) void weight_grad_kernel(WeightGrad
 }
 
 // The shares' sums of a tile added in order: four elements per thread.
-template <int TO, int TI, int WO, int WI>
+template <int TO, int TI, int WO, int WI, int DEPTH>
 __global__ __launch_bounds__(256) void weight_join_kernel(WeightGrad a) {
-    using S = Tile<TO, TI, WO, WI>;
+    using S = Tile<TO, TI, WO, WI, DEPTH>;
     constexpr uint32_t blocks = TO * TI / 1024;
     const uint32_t rest = (uint32_t)(a.tiles - a.whole_tiles), nth = blockIdx.x / blocks;
     const Unit u = unit_of(a, (uint32_t)a.whole_tiles + nth);
@@ -380,19 +386,19 @@ __global__ __launch_bounds__(256) void weight_join_kernel(WeightGrad a) {
     finish4(a, row * a.cols + col, n, sum);
 }
 
-template <int DT, int TO, int TI, int WO, int WI, int SETS>
+template <int DT, int TO, int TI, int WO, int WI, int DEPTH, int SETS>
 int launch_tile(const WeightGrad& a, hipStream_t s) {
     const int64_t rest = a.tiles - a.whole_tiles;
-    weight_grad_kernel<DT, TO, TI, WO, WI, SETS><<<(uint32_t)(a.whole_tiles + rest * a.splits), WO * WI * 64, 0, s>>>(a);
+    weight_grad_kernel<DT, TO, TI, WO, WI, DEPTH, SETS><<<(uint32_t)(a.whole_tiles + rest * a.splits), WO * WI * 64, 0, s>>>(a);
     if (const int e = (int)hipGetLastError()) return e;
-    if (rest) weight_join_kernel<TO, TI, WO, WI><<<(uint32_t)(rest * (TO * TI / 1024)), 256, 0, s>>>(a);
+    if (rest) weight_join_kernel<TO, TI, WO, WI, DEPTH><<<(uint32_t)(rest * (TO * TI / 1024)), 256, 0, s>>>(a);
     return (int)hipGetLastError();
 }
 template <int DT>
 int launch_dt(const WeightGrad& a, hipStream_t s) {
-    if (a.tile == 256) return launch_tile<DT, 256, 256, 2, 4, 2>(a, s);
-    if (a.tile == 128) return launch_tile<DT, 128, 128, 2, 2, 4>(a, s);
-    return launch_tile<DT, 64, 64, 1, 2, 4>(a, s);
+    if (a.tile == 256) return launch_tile<DT, 256, 256, 2, 4, 32, 2>(a, s);
+    if (a.tile == 128) return launch_tile<DT, 128, 128, 2, 2, 64, 2>(a, s);
+    return launch_tile<DT, 64, 64, 2, 2, 64, 2>(a, s);
 }
 
 }  // namespace
@@ -400,27 +406,29 @@ int launch_dt(const WeightGrad& a, hipStream_t s) {
 // The tile and the split: the least of the times that the measured parts add up to.
 // A tile's blocks fill `slots` places of the chip; whole rounds of tiles are summed
 // by a block each, and the tiles left over, which would leave places empty, may be
-// shared by blocks, whose sums (fp32) cost their writing and reading.  In ns: a step
-// of 32 rows with the chip empty and with every place taken, a block's beginning and
-// end, a share's traffic, the second launch.  Large tiles move fewer bytes per
-// product, small ones spread small gradients over the chip.  Measured, the best split
-// of each, us: 512 x 1024 over 512 rows 10.6, 13.7, 17.5 with tiles of 64, 128, 256;
-// 1024 x 1024 over 8192 rows 43.6, 37.3 with 64, 128; 4096 x 4096 over 2048 rows 96, 67
-// with 128, 256; 4099 x 4001 over 16384 rows 732, 488 (unsplit 906, 825).
+// shared by blocks, whose sums (fp32) cost their writing and reading.  In ns: 32 rows
+// with up to `free` blocks at once and with every place taken, a block's beginning and
+// end, a share's traffic, the second launch.  Large tiles move fewer bytes per product,
+// small ones spread small gradients over the chip.  Measured, the best split of each,
+// us: 512 x 1024 over 512 rows 9.2, 13.2, 17.0 with tiles of 64, 128, 256; 1024 x 1024
+// over 2048 rows 20.9, 21.8, 27.0; over 8192 rows 47.9, 34.8, 41.3; 2048 x 2048 over 2048
+// rows 54.6, 33.5, 43.2; 4096 x 4096 over 2048 rows 96, 67 with 128, 256; 4099 x 4001
+// over 16384 rows 732, 488 (unsplit 906, 825).
 void plan_weight_grad(WeightGrad& a) {
     struct Kind {
-        int64_t tile, slots, step, step_full, ends, part;
+        int64_t tile, slots, free, step, step_full, ends, part;
     };
-    static const Kind kinds[] = {{256, 256, 740, 880, 6000, 86},
-                                 {128, 512, 400, 700, 4500, 22},
-                                 {64, 1024, 400, 500, 4000, 6}};
+    static const Kind kinds[] = {{256, 256, 0, 740, 880, 6000, 86},
+                                 {128, 512, 256, 380, 660, 6000, 22},
+                                 {64, 1024, 256, 235, 775, 5500, 6}};
     static const int64_t splits[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64, 96};
     const int64_t steps = (a.rows + 31) / 32;
     int64_t best = INT64_MAX;
     for (const Kind& k : kinds) {
         const int64_t to = (a.outs + k.tile - 1) / k.tile, ti = (a.cols + k.tile - 1) / k.tile, tiles = to * ti;
         const auto round = [&](int64_t n, int64_t units) {     // n steps of `units` blocks at once
-            return n * (k.step + (k.step_full - k.step) * units / k.slots) + k.ends;
+            const int64_t more = units > k.free ? units - k.free : 0;
+            return n * (k.step + (k.step_full - k.step) * more / (k.slots - k.free)) + k.ends;
         };
         for (const int64_t s : splits) {
             if (s > 1 && s * 2 > steps) break;

@@ -352,7 +352,7 @@ WHOLE = [  # rows, outs, cols, dy, grad, accumulate, shift, row distance more
     (30, 0, 40, "bf16", "fp32", False, 0, 0), (30, 20, 0, "bf16", "fp32", False, 0, 0),
     # tiles of 256 in two rounds, the second shared, all of them shared; tiles of 128 whole and shared
     (400, 4099, 4001, "bf16", "fp32", False, 0, 0), (1500, 4099, 4001, "fp16", "fp32", True, 1, 0),
-    (4000, 2048, 2304, "bf16", "fp32", True, 0, 0), (2000, 2050, 2000, "bf16", "fp32", True, 0, 2),
+    (8000, 2048, 4096, "bf16", "fp32", True, 0, 0), (4000, 2048, 2304, "bf16", "fp32", False, 0, 0), (2000, 2050, 2000, "bf16", "fp32", True, 0, 2),
     (2500, 1000, 1100, "bf16", "fp32", True, 3, 0)]
 
 
@@ -376,7 +376,7 @@ def test_weight_grad_of_whole_numbers_is_exact(zf, rows, outs, cols, dt, gt, acc
     grad = buf[64 + shift:64 + shift + outs * cols].view(outs, cols)
     if accumulate:
         grad.copy_(torch.randint(-50, 51, (outs, cols), generator=g, device="cuda"))
-    # sums are multiples of 1/2 below 5000 * 3 * 254: exact in fp32 in any order
+    # sums are multiples of 1/2 below 8000 * 3 * 254 + 50: exact in fp32 in any order
     want = torch.matmul(dy.double().t().contiguous(), values(s)) + (grad.double() if accumulate else 0.0)
     zf.zero_weight_grad8(dy, s, grad, accumulate=accumulate)
     assert torch.equal(grad.double(), want)
