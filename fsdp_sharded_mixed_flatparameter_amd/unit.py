@@ -95,17 +95,26 @@ def _apart(a, b, name_a, name_b):
     raise ValueError("%s and %s overlap" % (name_a, name_b))
 
 
+def _whole(x, name, most=(1 << 63) - 1):
+    """Refuses a number that would arrive at the library as another one."""
+    if not -most <= x <= most:
+        raise ValueError("%s is out of range" % name)
+
+
 def _on(stream):
     """The call's stream as an integer handle."""
     return _current_raw_stream() if stream is None else _stream(stream).value or 0
 
 
-def _scratch(workspace, need, device, here, stream, handle):
-    """The call's workspace: the caller's, or one of the call's own, which its
-    stream keeps until the kernels are done with it."""
+def _scratch(workspace, need, device, here, stream, handle, used):
+    """The call's workspace: the caller's, apart from the arguments in `used`, or
+    one of the call's own, which its stream keeps until the kernels are done with it."""
     if workspace is not None:
-        if _flat(workspace, "workspace", _UINT8, here) and workspace.numel() < need:
+        w = _flat(workspace, "workspace", _UINT8, here)
+        if workspace.numel() < need:
             raise ValueError("the workspace needs %d bytes" % need)
+        for name, x in used:
+            _apart(w, x, "workspace", name)
         return workspace
     workspace = torch.empty(need, dtype=torch.uint8, device=device)
     if stream is not None and handle != _current_raw_stream():
@@ -125,6 +134,7 @@ def zero_embed_lookup(tokens, table, out, scale=1.0, first=0, stream=None):
     """out[t] = table[tokens[t] - first] * scale, zeros for a token outside the
     table.  tokens: int32 or int64 of any shape; table: (vocab, dim), a view of
     the flat parameter; out: a row per token, fp32, fp16 or bf16."""
+    _whole(first, "first")
     here = _here(tokens, "tokens", _TOKENS)
     t, n = _flat(tokens, "tokens", _TOKENS, here), tokens.numel()
     w, (vocab, dim) = _table(table, "table", here)
@@ -141,6 +151,11 @@ def zero_embed_lookup_int8(tokens, q_buf, q_scales, n_slots, slot_numel, elem_of
     """zero_embed_lookup on a table that lies elem_offset elements into the flat
     parameter whose n_slots INT8 slots have been gathered (the payload that
     zero_dequant_allgather takes)."""
+    if block != 256:
+        raise ValueError("block must be 256")
+    for x, name in ((first, "first"), (slot_numel, "slot_numel"), (elem_offset, "elem_offset"), (vocab, "vocab")):
+        _whole(x, name)
+    _whole(n_slots, "n_slots", (1 << 31) - 1)
     here = _here(tokens, "tokens", _TOKENS)
     t, n = _flat(tokens, "tokens", _TOKENS, here), tokens.numel()
     q, s = _flat(q_buf, "q_buf", _INT8, here), _flat(q_scales, "q_scales", _FP32, here)
@@ -162,6 +177,8 @@ def zero_embed_lookup_int8(tokens, q_buf, q_scales, n_slots, slot_numel, elem_of
 @functools.lru_cache(maxsize=256)
 def zero_embed_grad_workspace(n_tokens, vocab, dim):
     """The bytes of workspace that zero_embed_grad needs (0 for few tokens)."""
+    for x, name in ((n_tokens, "n_tokens"), (vocab, "vocab"), (dim, "dim")):
+        _whole(x, name)
     b = C.c_int64(0)
     _check(_lib.zero_embed_grad_workspace(n_tokens, vocab, dim, C.byref(b)))
     return b.value
@@ -176,6 +193,9 @@ def zero_embed_grad(tokens, dy, grad, scale=1.0, first=0, padding=None, accumula
     in which the GPU does the work.  Without a workspace the call takes one of
     its own from torch's allocator; a captured graph that brings its own must
     not share it with what may run at the same time."""
+    _whole(first, "first")
+    if padding is not None:
+        _whole(padding, "padding")
     here = _here(tokens, "tokens", _TOKENS)
     t, n = _flat(tokens, "tokens", _TOKENS, here), tokens.numel()
     g, (vocab, dim) = _table(grad, "grad", here)
@@ -185,7 +205,7 @@ def zero_embed_grad(tokens, dy, grad, scale=1.0, first=0, padding=None, accumula
     handle, ws, size = _on(stream), None, 0
     need = zero_embed_grad_workspace(n, vocab, dim)
     if need or workspace is not None:
-        ws = _scratch(workspace, need, grad.device, here, stream, handle)
+        ws = _scratch(workspace, need, grad.device, here, stream, handle, (("tokens", t), ("dy", d), ("grad", g)))
         ws, size = ws.data_ptr(), ws.numel()
     pad = None if padding is None else C.byref(C.c_int64(padding))
     rc = _lib.zero_embed_grad(t[0], t[2], n, first, pad, d[0], d[2], d[3], scale, g[0], g[2], vocab, dim,
@@ -209,17 +229,29 @@ class Saved8:
         if rows < 0 or cols < 0:
             raise ValueError("negative size")
         blocks = -(-cols // ZERO_BLOCK8)
-        self._rows, self._cols = rows, cols
-        self._codes = torch.empty(rows, blocks * ZERO_BLOCK8, dtype=torch.int8, device=device)
-        self._exponents = torch.empty(rows, blocks, dtype=torch.uint8, device=device)
+        self._hold(rows, cols, torch.empty(rows, blocks * ZERO_BLOCK8, dtype=torch.int8, device=device),
+                   torch.empty(rows, blocks, dtype=torch.uint8, device=device))
+
+    def _hold(self, rows, cols, codes, exponents):
+        self._rows, self._cols, self._codes, self._exponents = rows, cols, codes, exponents
         # device, codes and exponents as _flat gives them
-        c, e = self._codes.data_ptr(), self._exponents.data_ptr()
-        self._at = (self._codes.get_device(), (c, c + self._codes.numel(), 1), (e, e + self._exponents.numel(), 1))
+        c, e = codes.data_ptr(), exponents.data_ptr()
+        self._at = (codes.get_device(), (c, c + codes.numel(), 1), (e, e + exponents.numel(), 1))
+
+    def __reduce__(self):
+        # a copy, or one loaded from bytes, must ask its own tensors where they are
+        return _held, (self._rows, self._cols, self._codes, self._exponents)
 
     rows = property(lambda self: self._rows)
     cols = property(lambda self: self._cols)
     codes = property(lambda self: self._codes)
     exponents = property(lambda self: self._exponents)
+
+
+def _held(*parts):
+    s = Saved8.__new__(Saved8)
+    s._hold(*parts)
+    return s
 
 
 _NONE = (None, None, None)
@@ -331,6 +363,8 @@ def zero_act_backward8(kind, dy, saved, dx, saved_up=None, dup=None, again=None,
 def zero_weight_grad8_workspace(rows, outs, cols):
     """The bytes of workspace that zero_weight_grad8 needs (0 where it does not split
     its sums)."""
+    for x, name in ((rows, "rows"), (outs, "outs"), (cols, "cols")):
+        _whole(x, name)
     b = C.c_int64(0)
     _check(_lib.zero_weight_grad8_workspace(rows, outs, cols, C.byref(b)))
     return b.value
@@ -353,7 +387,8 @@ def zero_weight_grad8(dy, saved, grad, accumulate=False, workspace=None, stream=
     handle = _on(stream)
     need, ws, size = zero_weight_grad8_workspace(rows, outs, cols), None, 0
     if need or workspace is not None:
-        ws = _scratch(workspace, need, grad.device, here, stream, handle)
+        ws = _scratch(workspace, need, grad.device, here, stream, handle,
+                      (("dy", d), ("grad", g), ("saved.codes", c), ("saved.exponents", e)))
         ws, size = ws.data_ptr(), ws.numel()
     rc = _lib.zero_weight_grad8(d[0], d[2], d[3], rows, outs, c[0], e[0], cols, g[0], g[2],
                                 ZERO_ACCUMULATE if accumulate else 0, ws, size, handle)

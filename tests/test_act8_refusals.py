@@ -181,3 +181,39 @@ def test_shapes_and_overlaps_are_refused(zf, place):
     refused("dy must hold", zf.zero_weight_grad8, make(4, 9, dtype=torch.bfloat16), s, make(8, 40))
     with pytest.raises(AttributeError):
         s.codes = torch.zeros(4, 40, dtype=torch.int8)      # a checkpoint's memory stays where it is
+
+
+def test_a_copied_checkpoint_has_memory_of_its_own(zf):
+    """Copies and what is loaded from bytes name their own tensors, never the first one's."""
+    import copy
+    import io
+    import pickle
+    s = zf.Saved8(4, 40, device="cpu")
+    s.codes.copy_(torch.arange(256).view(4, 64) - 128)
+    s.exponents.fill_(130)
+    f = io.BytesIO()
+    torch.save(s, f)
+    f.seek(0)
+    for c in (copy.deepcopy(s), pickle.loads(pickle.dumps(s)), torch.load(f, weights_only=False)):
+        assert (c.rows, c.cols) == (4, 40) and torch.equal(c.codes, s.codes) and torch.equal(c.exponents, s.exponents)
+        assert c.codes.data_ptr() != s.codes.data_ptr()
+        assert c._at[1] == (c.codes.data_ptr(), c.codes.data_ptr() + 256, 1)
+        assert c._at[2] == (c.exponents.data_ptr(), c.exponents.data_ptr() + 8, 1)
+    c = copy.copy(s)
+    assert c.codes is s.codes and c._at == s._at
+
+
+def test_a_workspace_that_overlaps_is_refused(zf, place, monkeypatch):
+    _, saved = place
+    monkeypatch.setattr(zf.unit, "_current_raw_stream", lambda: 0)
+    monkeypatch.setattr(zf.unit, "_lib", zf.lib())
+    s = saved(5000, 40)
+    need = zf.zero_weight_grad8_workspace(5000, 24, 40)
+    assert need > 0
+    dy, g = Device(torch.zeros(5000, 24, dtype=torch.bfloat16), 1 << 33), Device(torch.zeros(24, 40), 1 << 34)
+    monkeypatch.setattr(zf.unit, "_lib", None)
+    # the workspace's last byte is the argument's first; the exponents' last is the workspace's first
+    for first, name in (((1 << 33) - need + 1, "dy"), ((1 << 34) - need + 1, "grad"),
+                        (s._at[1][0] - need + 1, "saved.codes"), (s._at[2][1] - 1, "saved.exponents")):
+        with pytest.raises(ValueError, match="workspace and %s overlap" % name):
+            zf.zero_weight_grad8(dy, s, g, workspace=Device(torch.zeros(need, dtype=torch.uint8), first))

@@ -161,3 +161,44 @@ def test_rows_and_overlaps(zf):
                  (t[:, 2:5], t[2])):
         with pytest.raises(ValueError, match="a and b overlap"):
             apart(a, b if b.dim() == 2 else b[None])
+
+
+def test_numbers_that_the_library_could_not_hold_are_refused(zf, monkeypatch):
+    """A Python number past the library's integers must not arrive as another one."""
+    monkeypatch.setattr(zf.unit, "_device", lambda: 0)
+    tok, w, y = Device(torch.zeros(4, dtype=torch.int64)), Device(torch.zeros(10, 8), 0, 1 << 21), \
+        Device(torch.zeros(4, 8), 0, 1 << 22)
+    q, s = Device(torch.zeros(80, dtype=torch.int8), 0, 1 << 23), Device(torch.zeros(1), 0, 1 << 24)
+    monkeypatch.setattr(zf.unit, "_lib", None)
+    for first in (1 << 64, -(1 << 64) + 3, 1 << 63):
+        with pytest.raises(ValueError, match="first"):
+            zf.zero_embed_lookup(tok, w, y, first=first)
+        with pytest.raises(ValueError, match="first"):
+            zf.zero_embed_grad(tok, y, w, first=first)
+        with pytest.raises(ValueError, match="first"):
+            zf.zero_embed_lookup_int8(tok, q, s, 1, 80, 0, 10, y, first=first)
+        with pytest.raises(ValueError, match="padding"):
+            zf.zero_embed_grad(tok, y, w, padding=first)
+    good = dict(n_slots=1, slot_numel=80, elem_offset=0, vocab=10, block=256)
+    for name, value in (("n_slots", 1 << 32), ("n_slots", -(1 << 32) + 1), ("slot_numel", -(1 << 64) + 80),
+                        ("elem_offset", 1 << 64), ("vocab", (1 << 64) + 10), ("block", 0), ("block", (1 << 32) + 256)):
+        kw = {**good, name: value}
+        if name == "n_slots":
+            kw["slot_numel"] = 0
+        with pytest.raises(ValueError, match=name):
+            zf.zero_embed_lookup_int8(tok, q, s, out=y, **kw)
+
+
+def test_a_workspace_that_overlaps_is_refused(zf, monkeypatch):
+    monkeypatch.setattr(zf.unit, "_device", lambda: 0)
+    monkeypatch.setattr(zf.unit, "_current_raw_stream", lambda: 0)
+    n, v, d = 5000, 700, 16
+    need = zf.zero_embed_grad_workspace(n, v, d)
+    assert need > 0
+    tok, dy, g = (Device(torch.zeros(n, dtype=torch.int64), 0, 1 << 24), Device(torch.zeros(n, d), 0, 1 << 25),
+                  Device(torch.zeros(v, d), 0, 1 << 26))
+    monkeypatch.setattr(zf.unit, "_lib", None)
+    for other, name in ((tok, "tokens"), (dy, "dy"), (g, "grad")):
+        ws = Device(torch.zeros(need, dtype=torch.uint8), 0, other.base - need + 1)
+        with pytest.raises(ValueError, match="workspace and %s overlap" % name):
+            zf.zero_embed_grad(tok, dy, g, workspace=ws)
