@@ -12,7 +12,7 @@
 //
 // The large tile, 256 x 256 by eight waves, needs every register: a wave's 128 sums,
 // the operands of one step, which give way to the next one's row by row, and two steps
-// of loads.  4096 x 4096 over 16384 rows take 449 us, 1.22 PFLOP/s in bf16 (a library
+// of loads.  4096 x 4096 over 16384 rows take 432 us, 1.27 PFLOP/s in bf16 (a library
 // product of two 8192 x 8192 matrices 1.29, of these two operands in bf16 0.93).  Tried
 // and not kept: both halves of a step's operands held twice (spills; 720 us), four waves
 // of 128 x 128 (the sums move between register files; spills), loads one step ahead
@@ -38,7 +38,7 @@ __device__ __forceinline__ v4f mfma(v8s a, v8s b, v4f c) {
 }
 
 // A row of a tile in LDS is T 16-bit elements and 16 more: the transposing load's
-// sixteen lanes read 32 bytes of four rows, which then lie in different banks, and
+// lanes read 32 bytes of rows in turn, eight of which then fill the banks once, and
 // every address of a lane is one number and a constant.
 constexpr int kPad = 16;
 
@@ -259,13 +259,18 @@ __global__ __launch_bounds__(WO * WI * 64, 2) void weight_grad_kernel(WeightGrad
 #pragma unroll
         for (int i = 0; i < S::fi; ++i) acc[o][i] = v4f{0, 0, 0, 0};
     const int wo = wave / WI * S::fo, wi = wave % WI * S::fi;
-    const int krow = 8 * (lane / 16) + lane % 16 / 4;            // this lane's row of a transposing load
+    // This lane's row of a transposing load.  The sum's order is free as long as both
+    // operands have the same one: a lane's eight values are of rows 4g to 4g + 3 and
+    // 16 more, so that the lanes of a load read sixteen rows in turn (with eight rows in
+    // turn, each second group of four left out, two of them met in every bank: 449 us
+    // for the head's 432, and LDS busy with conflicts for 27% of the time, now 7).
+    const int krow = lane / 4;
     const int kcol = lane % 4 * 4;
     constexpr int parts = DEPTH / 32;
     v8s x[parts][S::fi], y[parts][S::fo];       // a step's operands
     auto frag = [&](const uint16_t* p, int row) {
         const v4s u = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(p));
-        const v4s v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(p + 4 * row));
+        const v4s v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(p + 16 * row));
         return __builtin_shufflevector(u, v, 0, 1, 2, 3, 4, 5, 6, 7);
     };
     const uint16_t* xread = xsh + krow * lx + kcol + wi * 16;
