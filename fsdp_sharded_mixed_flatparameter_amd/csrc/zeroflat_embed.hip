@@ -150,6 +150,32 @@ __device__ __forceinline__ void zero_bytes(char* grad, int64_t first, int64_t la
     }
 }
 
+// Zeros to the rows v0 and on, of `rows` at most, that `hit` does not name: 16 bytes a
+// lane and store, whole lines in turn whatever the rows' length.  (Rows by waves, eight
+// columns a lane, wrote 1 GiB in 468 us behind few tokens and 414 behind the sort.)
+constexpr int64_t kZeroRowsBytes = 32768;
+template <int TG, int THREADS, typename Hit>
+__device__ __forceinline__ void zero_rows(const EmbedSum& a, int64_t v0, int64_t vocab, Hit hit) {
+    using T = typename Elem<TG>::type;
+    constexpr int wide = 16 / sizeof(T);
+    const uint32_t all = (uint32_t)min((int64_t)a.zero_rows, vocab - v0) * a.row_chunks.d;
+    for (uint32_t q = threadIdx.x; q < all; q += THREADS) {
+        const uint32_t r = div_by(q, a.row_chunks);
+        const int64_t col = (int64_t)(q - r * a.row_chunks.d) * wide;
+        if (hit(r)) continue;
+        T* p = static_cast<T*>(a.grad) + (v0 + r) * a.dim + col;
+        if (col + wide <= a.dim && a.stream) {
+            ZF_APART;
+            __builtin_nontemporal_store(v4u_any{0, 0, 0, 0}, reinterpret_cast<v4u_any*>(p));
+            ZF_APART;
+        } else if (col + wide <= a.dim) {
+            *reinterpret_cast<v4u_any*>(p) = v4u_any{0, 0, 0, 0};
+        } else {
+            for (int64_t c = col; c < a.dim; ++c) *p++ = T(0);
+        }
+    }
+}
+
 // One pass, first half: how many of each digit a block of
 // kEmbedSortTile items holds.  The first pass reads the tokens and clears the
 // rows' marks.
@@ -330,7 +356,7 @@ __device__ __forceinline__ Raw8<TD> fetch_row(const EmbedSum& a, int64_t place, 
 // run that crosses quarters is added up in LDS; one that crosses tiles leaves the
 // tile's share in its first partial row (it began before) or its second (it begins
 // here and goes on).  Blocks behind them write zeros to the rows that no token
-// names, a row per wave.
+// names, 32 KiB each.
 template <int TD, int TG, bool NARROW>
 __global__ __launch_bounds__(kThreads) void embed_sum_kernel(EmbedSum a) {
     __shared__ float heads[kWaves][kChunk], tails[kWaves][kChunk];
@@ -338,11 +364,9 @@ __global__ __launch_bounds__(kThreads) void embed_sum_kernel(EmbedSum a) {
     constexpr int kHead = 1, kThrough = 2, kTail = 4;      // a run from before; the only one, and it goes on; one that begins and goes on
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     if (blockIdx.x >= (uint32_t)a.sum_blocks) {
-        const int64_t v = a.zero_from + (int64_t)(blockIdx.x - a.sum_blocks) * kWaves + wave;
-        if (v >= a.vocab || as_const(reinterpret_cast<const uint8_t*>(a.flags))[v]) return;
-        const float zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        for (int64_t col = lane * 8; col < a.dim; col += kChunk)
-            store8<TG>(a.grad, v * a.dim + col, (int)min((int64_t)8, a.dim - col), zero, a.stream);
+        const int64_t v0 = a.zero_from + (int64_t)(blockIdx.x - a.sum_blocks) * a.zero_rows;
+        const uint8_t* named = reinterpret_cast<const uint8_t*>(a.flags) + v0;
+        zero_rows<TG, kThreads>(a, v0, a.vocab, [&](uint32_t r) { return as_const(named)[r] != 0; });
         return;
     }
     const int64_t tile = blockIdx.x / (uint32_t)a.chunks;
@@ -503,9 +527,11 @@ __global__ __launch_bounds__(kThreads) void embed_join_kernel(EmbedSum a) {
 // 8 * block + w.  The wave that has the first of them sums them all in order, or, of
 // more than kEmbedLong, leaves them to the whole block: each wave an eighth of the
 // positions, the eighths added in order.  The blocks behind write zeros to the rows
-// without a token, 16 each.  One launch, whose time is the chain of tokens,
-// comparisons, rows.
+// without a token, 16 each or what leaves two rounds of blocks at most: each looks
+// at every token first.  One launch, whose time is the chain of tokens, comparisons,
+// rows.
 constexpr int kFewWaves = 8, kFewThreads = kFewWaves * 64, kEmbedLong = 16, kFewRows = 16, kFewBatch = 16;
+constexpr int64_t kFewBlocks = 1536;
 
 template <int TD, int TG, bool NARROW>
 __global__ __launch_bounds__(kFewThreads) void embed_few_kernel(EmbedSort t, EmbedSum a) {
@@ -519,22 +545,15 @@ __global__ __launch_bounds__(kFewThreads) void embed_few_kernel(EmbedSort t, Emb
     const int64_t col = (int64_t)blockIdx.y * kChunk + lane * 8;
     if ((int)blockIdx.x >= blocks) {
         if (blockIdx.y) return;                            // whole rows
-        const uint32_t v0 = (blockIdx.x - blocks) * kFewRows;
-        if (threadIdx.x < kFewRows) keys[threadIdx.x] = 0;
+        const uint32_t v0 = (blockIdx.x - blocks) * (uint32_t)a.zero_rows;
+        for (int r = threadIdx.x; r < a.zero_rows; r += kFewThreads) keys[r] = 0;
         __syncthreads();
         for (int i = threadIdx.x; i < n; i += kFewThreads) {
             const uint32_t k = key_at(t, i);
-            if (k - v0 < (uint32_t)kFewRows) keys[k - v0] = 1;
+            if (k - v0 < (uint32_t)a.zero_rows) keys[k - v0] = 1;
         }
         __syncthreads();
-        const float zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        for (int r = wave; r < kFewRows; r += kFewWaves) {
-            const int64_t v = (int64_t)v0 + r;
-            if (v >= t.vocab) break;
-            if (keys[r]) continue;
-            for (int64_t c = lane * 8; c < a.dim; c += kChunk)
-                store8<TG>(a.grad, v * a.dim + c, (int)min((int64_t)8, a.dim - c), zero, a.stream);
-        }
+        zero_rows<TG, kFewThreads>(a, v0, t.vocab, [&](uint32_t r) { return keys[r] != 0; });
         return;
     }
     for (int i = threadIdx.x; i < n; i += kFewThreads) keys[i] = key_at(t, i);
@@ -668,11 +687,16 @@ int launch_embed_grad(const EmbedGradLaunch& l, void* stream) {
     EmbedSort a = l.sort;
     const int64_t row_bytes = l.sum.dim * (l.grad_dtype == ZERO_F32 ? 4 : 2);
     EmbedSum b = l.sum;
+    const int64_t chunks = (row_bytes + 15) / 16;
+    b.row_chunks = make_div((uint32_t)chunks);
     // of an accumulated gradient only the rows that tokens name are written
     b.stream = streams((b.accumulate ? (a.n_tokens < a.vocab ? a.n_tokens : a.vocab) : a.vocab) * row_bytes);
     if (embed_few(a.n_tokens, b.dim)) {
-        const int64_t rows = l.sum.accumulate ? 0 : a.vocab;
-        const dim3 grid((uint32_t)((a.n_tokens + kFewWaves - 1) / kFewWaves + (rows + kFewRows - 1) / kFewRows),
+        const int64_t rows = l.sum.accumulate ? 0 : a.vocab, each = (rows + kFewBlocks - 1) / kFewBlocks;
+        // their marks lie where the tokens' rows do otherwise
+        b.zero_rows = (int32_t)(each < kFewRows ? kFewRows : each > kEmbedFew ? kEmbedFew : each);
+        if (b.zero_rows > (1 << 29) / chunks) b.zero_rows = (int32_t)((1 << 29) / chunks);
+        const dim3 grid((uint32_t)((a.n_tokens + kFewWaves - 1) / kFewWaves + (rows + b.zero_rows - 1) / b.zero_rows),
                         (uint32_t)((b.dim + kChunk - 1) / kChunk));
         if (l.dy_dtype == ZERO_F32) few_to<ZERO_F32>(a, b, l.grad_dtype, grid, s);
         else if (l.dy_dtype == ZERO_F16) few_to<ZERO_F16>(a, b, l.grad_dtype, grid, s);
@@ -732,7 +756,9 @@ int launch_embed_grad(const EmbedGradLaunch& l, void* stream) {
     b.sum_blocks = b.tiles * b.chunks;
     // rows that are zero already need no more of it; one that is so in part does
     b.zero_from = b.accumulate ? b.vocab : a.zero_last / row_bytes;
-    const dim3 sums((uint32_t)(b.sum_blocks + (b.vocab - b.zero_from + kWaves - 1) / kWaves));
+    const int64_t each = kZeroRowsBytes / row_bytes;
+    b.zero_rows = (int32_t)(each < 4 ? 4 : each > 64 ? 64 : each);
+    const dim3 sums((uint32_t)(b.sum_blocks + (b.vocab - b.zero_from + b.zero_rows - 1) / b.zero_rows));
     if (l.dy_dtype == ZERO_F32) sum_to<ZERO_F32>(b, l.grad_dtype, sums, s);
     else if (l.dy_dtype == ZERO_F16) sum_to<ZERO_F16>(b, l.grad_dtype, sums, s);
     else sum_to<ZERO_BF16>(b, l.grad_dtype, sums, s);

@@ -236,6 +236,8 @@ struct EmbedSum {
     float* partials;        // two fp32 rows of `pitch` per tile: a run from before, a run that goes on
     int64_t n_tokens, vocab, dim, dy_ld, pitch, tiles, chunks, sum_blocks;
     int64_t zero_from;      // the first row that may need zeros yet
+    Div row_chunks;         // 16-byte parts of a row
+    int32_t zero_rows;      // rows of one block that writes zeros
     int32_t tile;           // sorted positions of one tile
     int32_t accumulate;
     int32_t stream;         // 1: the gradient goes past the caches

@@ -542,3 +542,61 @@ def test_a_copied_checkpoint_is_read_from_its_own_memory(zf):
     zf.zero_act_save8(-x, s)
     zf.zero_act_restore8(c, z)
     assert torch.equal(y, z) and float(z[69, 44]) > 2.9
+
+
+@pytest.mark.parametrize("rows,outs,cols", [(3, 5, 7), (70, 13, 45), (515, 130, 70), (300, 259, 301), (33, 8, 33)])
+def test_what_lies_beside_the_matrices_takes_no_part(zf, rows, outs, cols):
+    """Inputs are columns of buffers full of NaN and infinities, outputs of ones that stay."""
+    def among(t, beside):
+        b = torch.full((t.shape[0] + 2, t.shape[1] + 11), beside, dtype=t.dtype, device="cuda")
+        b[1:-1, 3:3 + t.shape[1]] = t
+        return b, b[1:-1, 3:3 + t.shape[1]]
+
+    k = torch.arange(rows * cols, device="cuda").view(rows, cols)
+    x = ((k * 7) % 19 - 9).to(torch.bfloat16)
+    dy = ((torch.arange(rows * outs, device="cuda").view(rows, outs) * 5) % 13 - 6).to(torch.bfloat16)
+    plain, s = zf.Saved8(rows, cols), zf.Saved8(rows, cols)
+    zf.zero_act_save8(x, plain)
+    for beside in (math.nan, math.inf):
+        zf.zero_act_save8(among(x, beside)[1], s)
+        assert torch.equal(s.codes, plain.codes) and torch.equal(s.exponents, plain.exponents)
+        g = torch.empty(outs, cols, device="cuda")
+        zf.zero_weight_grad8(among(dy, beside)[1], s, g)
+        # whole numbers below 2^24: exact
+        assert torch.equal(g.double(), (dy.double().t().contiguous() @ x.double()))
+        for f in (lambda o, src: zf.zero_act_restore8(plain, o),
+                  lambda o, src: zf.zero_act_forward8(zf.ZERO_GELU, src, o, s),
+                  lambda o, src: zf.zero_act_backward8(zf.ZERO_GELU, src, plain, o)):
+            want = torch.empty_like(x)
+            f(want, x)
+            b, o = among(torch.zeros_like(x), 3.0)
+            f(o, among(x, beside)[1])
+            assert torch.equal(o, want)
+            o.fill_(3.0)
+            assert bool((b == 3.0).all())
+
+
+def test_two_calls_in_flight(zf):
+    """Work on two streams at once, each with memory of its own, is as it is in turn."""
+    torch.manual_seed(5)
+    jobs = []
+    for n in (0, 1):
+        x = torch.randn(3000, 500 + n, device="cuda").bfloat16()
+        dy = torch.randn(3000, 300 + n, device="cuda").bfloat16()
+        tok = torch.randint(0, 900, (3000,), device="cuda")
+        s, g, e = zf.Saved8(3000, 500 + n), torch.empty(300 + n, 500 + n, device="cuda"), torch.empty(900, 300 + n, device="cuda")
+
+        def run(stream=None, x=x, dy=dy, tok=tok, s=s, g=g, e=e):
+            zf.zero_act_save8(x, s, stream=stream)
+            zf.zero_weight_grad8(dy, s, g, stream=stream)
+            zf.zero_embed_grad(tok, dy, e, stream=stream)
+        run()
+        jobs.append((run, g, e, g.clone(), e.clone()))
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for (run, g, e, _, _), side in zip(jobs, streams):
+            run(side)
+    torch.cuda.synchronize()
+    for _, g, e, g0, e0 in jobs:
+        assert torch.equal(g, g0) and torch.equal(e, e0)
