@@ -333,3 +333,21 @@ def test_captured_calls_replay_as_eager_ones(zf):
         zf.zero_embed_grad(tok, dy, grad2)
         torch.cuda.synchronize()
         assert torch.equal(y, y2) and torch.equal(grad, grad2), k
+
+
+@pytest.mark.parametrize("dim", [1, 3, 7, 8, 13, 33, 130])
+@pytest.mark.parametrize("gt", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("n", [1, 700, 5000])
+def test_rows_without_a_token_are_zeros(zf, n, gt, dim):
+    """Many rows to a block, at every offset of the first one; what lies around stays."""
+    vocab = 70001
+    tok = torch.randint(0, vocab, (n,), device="cuda", generator=torch.Generator(device="cuda").manual_seed(n))
+    tok[-1], tok[0] = vocab - 1, 0
+    dy = torch.ones(n, dim, device="cuda")
+    want = torch.bincount(tok, minlength=vocab).to(gt)[:, None].expand(vocab, dim)
+    for shift in (0, 1, 2, 3, 5, 7):
+        b = torch.full((vocab * dim + 16,), 9.0, dtype=gt, device="cuda")
+        g = b[shift:shift + vocab * dim].view(vocab, dim)
+        zf.zero_embed_grad(tok, dy, g)
+        assert torch.equal(g, want)
+        assert bool((b[:shift] == 9.0).all()) and bool((b[shift + vocab * dim:] == 9.0).all())
