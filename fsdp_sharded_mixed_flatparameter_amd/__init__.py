@@ -209,6 +209,15 @@ def _stream(stream):
     return C.c_void_p(int(stream))
 
 
+def _torch_stream(stream, handle, device):
+    """A call's stream as torch has it, of the given handle on device number `device`."""
+    import torch
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    # 0 and 1 are names of the default stream, which torch does not take by handle
+    return torch.cuda.default_stream(device) if handle in (0, 1) else torch.cuda.ExternalStream(handle, device)
+
+
 def _contig(t, name):
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)

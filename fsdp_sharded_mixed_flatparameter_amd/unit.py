@@ -16,7 +16,7 @@ import functools
 
 import torch
 
-from . import _DTYPE_CODES, _check, _current_raw_stream, _dtype_name, _lib, _stream
+from . import _DTYPE_CODES, _check, _current_raw_stream, _dtype_name, _lib, _stream, _torch_stream
 
 ZERO_ACCUMULATE = 8
 ZERO_GELU, ZERO_GELU_TANH, ZERO_SILU = 0, 1, 2
@@ -107,8 +107,10 @@ def _on(stream):
 
 
 def _scratch(workspace, need, device, here, stream, handle, used):
-    """The call's workspace: the caller's, apart from the arguments in `used`, or
-    one of the call's own, which its stream keeps until the kernels are done with it."""
+    """The call's workspace: the caller's, apart from the arguments in `used`, or one
+    of the call's own.  torch's allocator orders the use of a block behind its last
+    one on the stream that it is taken under, and on no other: the call's own is
+    taken under the stream that its kernels go on."""
     if workspace is not None:
         w = _flat(workspace, "workspace", _UINT8, here)
         if workspace.numel() < need:
@@ -116,10 +118,10 @@ def _scratch(workspace, need, device, here, stream, handle, used):
         for name, x in used:
             _apart(w, x, "workspace", name)
         return workspace
-    workspace = torch.empty(need, dtype=torch.uint8, device=device)
-    if stream is not None and handle != _current_raw_stream():
-        workspace.record_stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(handle))
-    return workspace
+    if stream is None or handle == _current_raw_stream():
+        return torch.empty(need, dtype=torch.uint8, device=device)
+    with torch.cuda.stream(_torch_stream(stream, handle, here)):
+        return torch.empty(need, dtype=torch.uint8, device=device)
 
 
 # ------------------------------------------------------------------ embedding
