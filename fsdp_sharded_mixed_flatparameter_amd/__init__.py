@@ -218,6 +218,17 @@ def _torch_stream(stream, handle, device):
     return torch.cuda.default_stream(device) if handle in (0, 1) else torch.cuda.ExternalStream(handle, device)
 
 
+def _empty_like(t, stream):
+    """Memory like device tensor t for kernels on `stream`: taken under that stream,
+    as torch's allocator orders its use behind the block's last one nowhere else."""
+    import torch
+    handle = None if stream is None else _stream(stream).value or 0
+    if handle is None or handle == _current_raw_stream():
+        return torch.empty_like(t)
+    with torch.cuda.stream(_torch_stream(stream, handle, t.get_device())):
+        return torch.empty_like(t)
+
+
 def _contig(t, name):
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)

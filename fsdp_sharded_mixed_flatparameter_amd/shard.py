@@ -5,7 +5,7 @@ arithmetic happens here; every part of the step runs in libzeroflat.
 """
 import torch
 
-from . import (ZERO_AVG, StepState, _current_raw_stream, zero_adamw_hparams_t,
+from . import (ZERO_AVG, StepState, _current_raw_stream, _empty_like, zero_adamw_hparams_t,
                zero_adamw_shard_step, zero_grad_accumulate_shard, zero_grad_reduce_shard,
                zero_grad_reduce_shard_int8, zero_offload_step, zero_unscale_norm)
 
@@ -35,16 +35,17 @@ class ShardOptimizer:
             self._h = (key, zero_adamw_hparams_t(**self.hp))
         return self._h[1]
 
-    def reduced_buffer(self):
+    def reduced_buffer(self, stream=None):
+        """The fp32 gradient shard, taken for kernels on `stream` when first asked for."""
         if self._red is None:
-            self._red = torch.empty_like(self.master)
+            self._red = _empty_like(self.master, stream)
         return self._red
 
     def step_from_rank_buffers(self, grad_bufs, elem_offset, allgather_buf, slot_offset,
                                op=ZERO_AVG, q_buf=None, q_scales=None, q_slot_offset=0,
                                q_scale_offset=0, stream=None):
         """Reduce-Scatter's reduce over the N rank buffers, then the step."""
-        red = self.reduced_buffer()
+        red = self.reduced_buffer(stream)
         if stream is None:
             stream = _current_raw_stream()   # one lookup for both calls
         zero_grad_reduce_shard(grad_bufs, elem_offset, self.numel, op, red, self.state,
@@ -57,7 +58,7 @@ class ShardOptimizer:
                              q_scale_offset=0, stream=None):
         """Reduce over the N ranks' INT8-quantised gradient slices for this rank
         (ZeRO++'s quantised Reduce-Scatter), then the step."""
-        red = self.reduced_buffer()
+        red = self.reduced_buffer(stream)
         if stream is None:
             stream = _current_raw_stream()
         zero_grad_reduce_shard_int8(q_slices, scale_slices, self.numel, op, red, self.state,
@@ -70,7 +71,7 @@ class ShardOptimizer:
         """One micro-step of gradient accumulation into the fp32 gradient shard:
         the first overwrites it (reduce), later ones add to it, and the last one
         also takes the step statistics over the accumulated shard."""
-        red = self.reduced_buffer()
+        red = self.reduced_buffer(stream)
         st = self.state if last else None
         if first:
             zero_grad_reduce_shard(grad_bufs, elem_offset, self.numel, op, red, st, stream=stream)
@@ -183,9 +184,9 @@ class MultiShardOptimizer:
             if len(x) != len(self.master):
                 raise ValueError("one entry per unit expected (%d units)" % len(self.master))
 
-    def _reduced(self, u):
+    def _reduced(self, u, stream):
         if self._red[u] is None:
-            self._red[u] = torch.empty_like(self.master[u])
+            self._red[u] = _empty_like(self.master[u], stream)
         return self._red[u]
 
     def step_from_rank_buffers(self, grad_bufs, elem_offsets, allgather_bufs, slot_offsets,
@@ -195,7 +196,7 @@ class MultiShardOptimizer:
         payloads of `quant`, see _apply)."""
         self._check(grad_bufs, elem_offsets, allgather_bufs, slot_offsets)
         for u, (bufs, off) in enumerate(zip(grad_bufs, elem_offsets)):
-            zero_grad_reduce_shard(bufs, off, self.master[u].numel(), op, self._reduced(u),
+            zero_grad_reduce_shard(bufs, off, self.master[u].numel(), op, self._reduced(u, stream),
                                    self.state, stream=stream)
         self._apply(self._red, allgather_bufs, slot_offsets, stream, quant)
 
@@ -209,7 +210,7 @@ class MultiShardOptimizer:
         st = self.state if last else None
         for u, (bufs, off) in enumerate(zip(grad_bufs, elem_offsets)):
             fn = zero_grad_reduce_shard if first else zero_grad_accumulate_shard
-            fn(bufs, off, self.master[u].numel(), op, self._reduced(u), st, stream=stream)
+            fn(bufs, off, self.master[u].numel(), op, self._reduced(u, stream), st, stream=stream)
 
     def step_from_accumulated(self, allgather_bufs, slot_offsets, quant=None, stream=None):
         """The step of every unit on the shards accumulated by micro_step."""

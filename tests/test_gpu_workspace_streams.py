@@ -82,3 +82,32 @@ def test_captured_on_a_forked_stream(zf):
         zf.zero_embed_grad(tok, dy, want)
         torch.cuda.synchronize()
         assert torch.equal(grad, want)
+
+
+def test_an_optimizers_first_step(zf):
+    """The gradient shard that the first step takes."""
+    n = 100000
+    g = torch.Generator(device="cuda").manual_seed(4)
+    hp = dict(lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.01, max_grad_norm=1.0)
+    bufs = [torch.randn(n, generator=g, device="cuda").bfloat16() for _ in range(2)]
+    start = torch.randn(n, generator=g, device="cuda")
+
+    def step(several, stream, busy):
+        master, slot = start.clone(), torch.zeros(n, dtype=torch.bfloat16, device="cuda")
+        opt = zf.MultiShardOptimizer([master], hp, loss_scale=1.0) if several else zf.ShardOptimizer(master, hp, loss_scale=1.0)
+        torch.cuda.synchronize()
+        if busy:
+            busy_then_given_back(4 * n)
+        if several:
+            opt.step_from_rank_buffers([bufs], [0], [slot], [0], stream=stream)
+        else:
+            opt.step_from_rank_buffers(bufs, 0, slot, 0, stream=stream)
+        torch.cuda.synchronize()
+        return master, slot
+
+    for several in (False, True):
+        want = step(several, None, False)
+        assert not torch.equal(want[0], start)
+        for stream in (torch.cuda.Stream(), torch.cuda.Stream().cuda_stream):
+            got = step(several, stream, True)
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])

@@ -102,3 +102,22 @@ def test_weight_grad(zf, taken, stream, under, handle):
     dy, g = Device(torch.zeros(5000, 24, dtype=torch.bfloat16), 1 << 26), Device(torch.zeros(24, 40), 1 << 27)
     zf.zero_weight_grad8(dy, s, g, stream=stream)
     assert taken == [("memory", under), ("zero_weight_grad8", handle)]
+
+
+@pytest.mark.parametrize("stream,under,handle", CASES)
+@pytest.mark.parametrize("several", (False, True))
+def test_an_optimizers_reduced_shard(zf, taken, monkeypatch, several, stream, under, handle):
+    """The fp32 gradient shard that an optimizer takes at its first step."""
+    monkeypatch.setattr(zf, "_current_raw_stream", lambda: CURRENT)
+    real = torch.empty_like
+    monkeypatch.setattr(torch, "empty_like", lambda t: torch.empty(0) if isinstance(t, Device) else real(t))
+    master = Device(real(torch.zeros(64)), 1 << 24)
+    if several:
+        opt = object.__new__(zf.MultiShardOptimizer)
+        opt.master, opt._red = [master, master], [None, None]
+        a, b = opt._reduced(1, stream), opt._reduced(1, 0x400)
+    else:
+        opt = object.__new__(zf.ShardOptimizer)
+        opt.master, opt._red = master, None
+        a, b = opt.reduced_buffer(stream), opt.reduced_buffer(0x400)
+    assert a is b and taken == [("memory", under)]
