@@ -95,6 +95,9 @@ def _apart(a, b, name_a, name_b):
     raise ValueError("%s and %s overlap" % (name_a, name_b))
 
 
+_INT32 = (1 << 31) - 1
+
+
 def _whole(x, name, most=(1 << 63) - 1):
     """Refuses a number that would arrive at the library as another one."""
     if not -most <= x <= most:
@@ -157,7 +160,7 @@ def zero_embed_lookup_int8(tokens, q_buf, q_scales, n_slots, slot_numel, elem_of
         raise ValueError("block must be 256")
     for x, name in ((first, "first"), (slot_numel, "slot_numel"), (elem_offset, "elem_offset"), (vocab, "vocab")):
         _whole(x, name)
-    _whole(n_slots, "n_slots", (1 << 31) - 1)
+    _whole(n_slots, "n_slots", _INT32)
     here = _here(tokens, "tokens", _TOKENS)
     t, n = _flat(tokens, "tokens", _TOKENS, here), tokens.numel()
     q, s = _flat(q_buf, "q_buf", _INT8, here), _flat(q_scales, "q_scales", _FP32, here)
@@ -319,6 +322,7 @@ def zero_act_forward8(kind, x, out, saved, up=None, saved_up=None, stream=None):
     """out = act(x), times `up` where that is given, and the checkpoints of x and up,
     in one pass.  kind: ZERO_GELU, ZERO_GELU_TANH or ZERO_SILU.  x and up may be
     columns of one buffer; out may be x or up itself."""
+    _whole(kind, "kind", _INT32)
     if (up is None) != (saved_up is None):
         raise ValueError("up and saved_up go together")
     rows, cols = saved._rows, saved._cols
@@ -342,6 +346,7 @@ def zero_act_backward8(kind, dy, saved, dx, saved_up=None, dup=None, again=None,
     one, and dup = dy * act(x).  `again` takes the checkpoint of act(x), times up:
     the next layer's input for its weight gradient, which was not kept.  dx or dup
     may be dy itself."""
+    _whole(kind, "kind", _INT32)
     if (dup is None) != (saved_up is None):
         raise ValueError("dup and saved_up go together")
     rows, cols = saved._rows, saved._cols
