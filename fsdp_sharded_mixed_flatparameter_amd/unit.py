@@ -5,11 +5,12 @@ tokens into the flat gradient, activations kept in 8 bits, the functions that
 keep and read them, and the weight gradient taken from them.  No arithmetic
 happens here.
 
-Every tensor of a call is on the current device.  The calls are ordered on the
-current stream, or on `stream`; tensors used on a stream other than their own
-are ordered, and kept, by the caller.  Matrices are tensors whose last
-dimension is contiguous: a row may be any distance from the next, so a slice of
-columns needs no copy.
+Every tensor of a call is on the current device, and so is its stream.  The calls
+are ordered on the current stream, or on `stream`; tensors used on a stream other
+than their own are ordered, and kept, by the caller; memory that a call takes for
+itself belongs to the stream that it is ordered on.  Matrices are tensors whose
+last dimension is contiguous: a row may be any distance from the next, so a slice
+of columns needs no copy.
 """
 import ctypes as C
 import functools
@@ -106,7 +107,11 @@ def _whole(x, name, most=(1 << 63) - 1):
 
 def _on(stream):
     """The call's stream as an integer handle."""
-    return _current_raw_stream() if stream is None else _stream(stream).value or 0
+    if stream is None:
+        return _current_raw_stream()
+    if isinstance(stream, torch.cuda.Stream) and stream.device.index != _device():
+        raise ValueError("the stream is of cuda:%d, the current device is cuda:%d" % (stream.device.index, _device()))
+    return _stream(stream).value or 0
 
 
 def _scratch(workspace, need, device, here, stream, handle, used):
