@@ -359,7 +359,7 @@ __device__ __forceinline__ Raw8<TD> fetch_row(const EmbedSum& a, int64_t place, 
 // names, 32 KiB each.
 template <int TD, int TG, bool NARROW>
 __global__ __launch_bounds__(kThreads) void embed_sum_kernel(EmbedSum a) {
-    __shared__ float heads[kWaves][kChunk], tails[kWaves][kChunk];
+    __shared__ float heads[kWaves][kChunk];
     __shared__ int32_t state[kWaves];                      // of a quarter, as bits:
     constexpr int kHead = 1, kThrough = 2, kTail = 4;      // a run from before; the only one, and it goes on; one that begins and goes on
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
@@ -439,8 +439,7 @@ __global__ __launch_bounds__(kThreads) void embed_sum_kernel(EmbedSum a) {
             keep(heads[wave]);
             mine = open ? kHead | kThrough : kHead;
         } else if (open) {
-            keep(tails[wave]);
-            mine |= kTail;
+            mine |= kTail;                                 // (the sum stays in registers)
         } else {
             write_row<TG>(a, cur, w.col, w.skip, w.n, acc);
         }
@@ -448,7 +447,7 @@ __global__ __launch_bounds__(kThreads) void embed_sum_kernel(EmbedSum a) {
     if (lane == 0) state[wave] = mine;
     __syncthreads();
     if (mine & kTail) {
-        // the quarters behind, as far as the run goes (acc is the tail still)
+        // the quarters behind, as far as the run goes
         int u = wave + 1;
         for (; u < kWaves; ++u) {
             add(heads[u]);
@@ -527,9 +526,10 @@ __global__ __launch_bounds__(kThreads) void embed_join_kernel(EmbedSum a) {
 // 8 * block + w.  The wave that has the first of them sums them all in order, or, of
 // more than kEmbedLong, leaves them to the whole block: each wave an eighth of the
 // positions, the eighths added in order.  The blocks behind write zeros to the rows
-// without a token, 16 each or what leaves two rounds of blocks at most: each looks
-// at every token first.  One launch, whose time is the chain of tokens, comparisons,
-// rows.
+// without a token.  Each looks at every token first and marks the named ones of its
+// own rows: 16 rows a block, or what leaves kFewBlocks of them, two rounds of the
+// chip, or the kEmbedFew that the marks have room for (beyond 3.1 million rows).  One
+// launch, whose time is the chain of tokens, comparisons, rows.
 constexpr int kFewWaves = 8, kFewThreads = kFewWaves * 64, kEmbedLong = 16, kFewRows = 16, kFewBatch = 16;
 constexpr int64_t kFewBlocks = 1536;
 
