@@ -611,9 +611,10 @@ int zero_multi_adamw_step_args(const zero_multi_step_args_t* args, void* stream)
  * dy_ld >= 0 elements between rows (0: every token has the same row).
  * workspace: DEVICE, 16-byte aligned, of the bytes that zero_embed_grad_workspace
  *   gives (0 for few tokens; else about 17 bytes per token, one per row and an fp32 row per
- *   64 tokens), used from the call's first kernel to its last: calls that overlap
- *   need one each.
- * At most 2^28 tokens, 2^25 rows, 2^24 columns.
+ *   64 tokens, or per 16 where n_tokens * ceil(dim/512) < 65536), used from the call's
+ *   first kernel to its last: calls that overlap need one each.
+ * At most 2^28 tokens, 2^25 rows, 2^24 columns; and of a gradient that needs a workspace
+ * ceil(n_tokens/128) * ceil(dim/512) + vocab/4 below 2^24.
  * ---------------------------------------------------------------------- */
 #define ZERO_ACCUMULATE 8u
 int zero_embed_lookup(const void* tokens, int32_t token_bytes, int64_t n_tokens, int64_t first,
