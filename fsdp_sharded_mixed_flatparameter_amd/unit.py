@@ -385,8 +385,9 @@ def zero_weight_grad8_workspace(rows, outs, cols):
 def zero_weight_grad8(dy, saved, grad, accumulate=False, workspace=None, stream=None):
     """grad = dy^T x, the gradient of a linear layer's (outs, cols) weight from the
     checkpoint of its input; with `accumulate` added to what grad holds.  dy: (rows,
-    outs), fp16 or bf16; grad: a view of the flat gradient, fp32, fp16 or bf16.
-    The workspace is as zero_embed_grad's."""
+    outs), fp16 or bf16 (an fp32 dy is rounded by the caller, who knows its range);
+    grad: a view of the flat gradient, fp32, fp16 or bf16.  The workspace is as
+    zero_embed_grad's."""
     here, c, e = _saved(saved, "saved")
     g = _flat(grad, "grad", _FLOATS, here)
     if grad.dim() != 2 or grad.shape[1] != saved._cols:

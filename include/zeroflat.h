@@ -661,17 +661,19 @@ int zero_embed_grad(const void* tokens, int32_t token_bytes, int64_t n_tokens, i
  * dtype (fp32, fp16 or bf16) is that of every matrix of a call.  Rows of inputs are
  * any number of elements apart (0 repeats one), of outputs cols or more.  dx may be
  * dy itself, y may be x or up itself, and dup dy; no other overlap of what a call
- * writes.  cols <= 2^24.
+ * writes.  rows <= 2^40, cols <= 2^24.
  *
  * zero_weight_grad8: the gradient of a linear layer's weight (outs, cols), y = x W^T,
  * from the checkpoint of its input:
  *     S[o][i] = sum over t < rows of dy[t*dy_ld + o] * round_dy_dtype( x^[t][i] )
  *   flags 0: grad = round_grad_dtype( S ); ZERO_ACCUMULATE: round_grad_dtype( f32(grad) + S ).
- *   dy: DEVICE fp16 or bf16; grad: DEVICE fp32, fp16 or bf16 [outs*cols], contiguous, at
- *   any element offset (a view of the flat gradient).  The products are exact and the
+ *   dy: DEVICE fp16 or bf16 (a caller with fp32 gradients rounds them first, to bf16 or,
+ *   under a loss scale, to fp16); grad: DEVICE fp32, fp16 or bf16 [outs*cols], contiguous,
+ *   at any element offset (a view of the flat gradient).  The products are exact and the
  *   sums fp32, on the matrix cores, in an order that the sizes fix.  workspace: DEVICE,
  *   16-byte aligned, of the bytes that zero_weight_grad8_workspace gives (0 where the
  *   sum is not split), one per call in flight.
+ *   rows <= 2^34, outs <= 2^24, outs * cols <= 2^38.
  * ---------------------------------------------------------------------- */
 typedef enum { ZERO_GELU = 0, ZERO_GELU_TANH = 1, ZERO_SILU = 2 } zero_act_t;
 
