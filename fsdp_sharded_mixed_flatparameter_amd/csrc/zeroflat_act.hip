@@ -211,7 +211,11 @@ __global__ __launch_bounds__(kThreads) void act_backward_kernel(ActLaunch a) {
             if constexpr (GATED) store8<DT>(a.dup, (int64_t)p.row * a.dup_ld + p.col, p.n, du, a.stream);
         }
         if (a.again_codes) {
-            // columns beyond the matrix stand for 0 whatever the function makes of 0
+            // columns beyond the matrix stand for 0 whatever the function makes of 0; the
+            // codes stay cached for the weight gradient that reads them next.  Cached and
+            // past the caches, us, bf16, alone: gated 8192 x 11008 135, 132 (118 without
+            // them), 16384 x 4096 98, 95, plain 66, 59; with that weight gradient (1024
+            // outputs) 345, 349; 236, 239; 204, 206; gated 4096 x 4096 80, 85.
 #pragma unroll
             for (int k = 0; k < 8; ++k) y[k] = k < p.n ? y[k] : 0.0f;
             keep(y, a.least, a.again_codes, a.again_exponents, g, 0);

@@ -173,8 +173,16 @@ int launch_multi_step(const MultiAdamLaunch& a, const MultiNormLaunch* norm, con
 constexpr int kEmbedInt8 = 3;            // a table's type beside zero_dtype_t: the INT8 payload
 constexpr int kEmbedFew = 2048;          // tokens whose gradient needs no sort, at most
 constexpr int kEmbedSortTile = 1024;     // tokens of one block of the sort
-constexpr int64_t kEmbedZeroBytes = 40 << 20;   // of zeros that a launch of the sort writes beside it
-constexpr int kEmbedScanBlocks = 128;    // blocks that sum the counts before theirs themselves
+// Zeros that a launch of the sort writes beside it, as many as its latency hides: 0, 20,
+// 40 and 80 MiB a launch, us: 4096 x 4096 into 32000 bf16 rows 80, 67, 63, 65; 16384 x 4096
+// 101, 91, 90, 93; 30011 x 1001 into 50021 fp32 rows 94, 81, 75, 77; 16384 x 2048 into
+// 131072 251, 236, 227, 220.  Where tokens name most rows they are written in vain: 131072
+// x 512 into 32000 fp32 rows 75, 83, 82, 82.
+constexpr int64_t kEmbedZeroBytes = 40 << 20;
+// Blocks of the sort that sum the counts before theirs themselves; more have a launch
+// between.  So and with it, us, n x 64 added: 16384 tokens 32, 36; 65536 44, 45; 131072 (128
+// blocks) 56, 52; 262144 81, 66; 2^20 223, 145.
+constexpr int kEmbedScanBlocks = 128;
 constexpr int kEmbedTile = 128;          // sorted positions of a block of the sums, at most
 constexpr int kEmbedBatch = 8;           // rows that a wave of the sums has in flight
 
