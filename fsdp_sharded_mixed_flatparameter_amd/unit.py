@@ -21,6 +21,7 @@ from . import _DTYPE_CODES, _check, _current_raw_stream, _dtype_name, _lib, _str
 
 ZERO_ACCUMULATE = 8
 ZERO_GELU, ZERO_GELU_TANH, ZERO_SILU = 0, 1, 2
+_KINDS = frozenset((ZERO_GELU, ZERO_GELU_TANH, ZERO_SILU))      # the library refuses the others
 ZERO_BLOCK8 = 32                 # columns that share an exponent
 
 # the checks below run before every launch, and a small call is as long as its
@@ -327,7 +328,8 @@ def zero_act_forward8(kind, x, out, saved, up=None, saved_up=None, stream=None):
     """out = act(x), times `up` where that is given, and the checkpoints of x and up,
     in one pass.  kind: ZERO_GELU, ZERO_GELU_TANH or ZERO_SILU.  x and up may be
     columns of one buffer; out may be x or up itself."""
-    _whole(kind, "kind", _INT32)
+    if kind not in _KINDS:
+        _whole(kind, "kind", _INT32)
     if (up is None) != (saved_up is None):
         raise ValueError("up and saved_up go together")
     rows, cols = saved._rows, saved._cols
@@ -351,7 +353,8 @@ def zero_act_backward8(kind, dy, saved, dx, saved_up=None, dup=None, again=None,
     one, and dup = dy * act(x).  `again` takes the checkpoint of act(x), times up:
     the next layer's input for its weight gradient, which was not kept.  dx or dup
     may be dy itself."""
-    _whole(kind, "kind", _INT32)
+    if kind not in _KINDS:
+        _whole(kind, "kind", _INT32)
     if (dup is None) != (saved_up is None):
         raise ValueError("dup and saved_up go together")
     rows, cols = saved._rows, saved._cols
