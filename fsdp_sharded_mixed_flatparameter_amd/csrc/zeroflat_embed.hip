@@ -532,8 +532,8 @@ __global__ __launch_bounds__(kThreads) void embed_join_kernel(EmbedSum a) {
 // launch, whose time is the chain of tokens, comparisons, rows.
 // Measured, us: kEmbedLong 4, 8, 16 and 64, tokens by rank, 512 x 4096 added 11.6, 9.9, 9.6,
 // 9.5, 2048 x 256 21.1, 19.2, 19.0, 17.1 (each token 64 times, 512 x 4096: 10.8, 10.5, 10.5,
-// 10.0).  kFewBlocks 768, 1536, 3072 and 6144, 64 x 256 into 131072 bf16 rows 12.3, 11.9, 12.4,
-// 16.2; 512 x 256 20.0, 16.9, 18.6, 21.4; 1024 x 1024 into 32000 28.0, 24.9, 26.0, 29.0.
+// 10.0).  kFewBlocks 768, 1536 and four times that, 64 x 256 into 131072 bf16 rows 12.3, 11.9,
+// 16.2; 512 x 256 20.0, 16.9, 21.4; 1024 x 1024 into 32000 28.0, 24.9, 29.0.
 constexpr int kFewWaves = 8, kFewThreads = kFewWaves * 64, kEmbedLong = 16, kFewRows = 16, kFewBatch = 16;
 constexpr int64_t kFewBlocks = 1536;
 
